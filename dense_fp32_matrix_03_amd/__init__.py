@@ -19,11 +19,12 @@ import re
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libsgemm.so")
 HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "sgemm.h")
+MXFP4_HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "sgemm_mxfp4.h")
 
 
-def _header_constants() -> dict:
+def _header_constants(path: str = HEADER_PATH) -> dict:
     out = {}
-    with open(HEADER_PATH) as f:
+    with open(path) as f:
         for m in re.finditer(r"#define\s+(SGEMM_\w+)\s+\(?(-?\d+)\)?", f.read()):
             out[m.group(1)] = int(m.group(2))
     return out
@@ -34,6 +35,9 @@ SGEMM_OK = _C["SGEMM_OK"]
 VARIANTS = {k[len("SGEMM_VARIANT_"):].lower(): v for k, v in _C.items()
             if k.startswith("SGEMM_VARIANT_")}
 NUM_VARIANTS = _C["SGEMM_NUM_VARIANTS"]
+# Element types of operands: "f32", "bf16", "mxfp4".
+TYPES = {k[len("SGEMM_TYPE_"):].lower(): v
+         for k, v in _header_constants(MXFP4_HEADER_PATH).items() if k.startswith("SGEMM_TYPE_")}
 
 
 class SgemmError(RuntimeError):
@@ -81,6 +85,26 @@ def load_library(path: str = LIB_PATH):
     lib.sgemm_run_bf16x3_ex_noalloc.argtypes = [ci, ci, i64, i64, i64, f32, vp, i64, vp, i64,
                                                 f32, vp, i64, vp]
     lib.sgemm_run_bf16x3_ex_noalloc.restype = ci
+    lib.sgemm_run_grouped.argtypes = [ci, i64, i64, i64, i64, f32, vp, i64, vp, i64, i64, f32, vp,
+                                      i64, vp, vp]
+    lib.sgemm_run_grouped.restype = ci
+    lib.sgemm_run_grouped_k.argtypes = [i64, i64, i64, i64, f32, vp, i64, vp, i64, f32, vp, i64,
+                                        i64, vp, vp]
+    lib.sgemm_run_grouped_k.restype = ci
+    for size in (lib.sgemm_mxfp4_codes_size, lib.sgemm_mxfp4_scales_size):
+        size.argtypes = [i64, i64]
+        size.restype = i64
+    lib.sgemm_mxfp4_workspace_size.argtypes = [ci, i64, i64]
+    lib.sgemm_mxfp4_workspace_size.restype = i64
+    lib.sgemm_mxfp4_quantize.argtypes = [ci, i64, i64, ci, vp, i64, vp, vp, i64, vp]
+    lib.sgemm_mxfp4_quantize.restype = ci
+    lib.sgemm_mxfp4_dequantize.argtypes = [ci, i64, i64, vp, vp, i64, ci, vp, i64, vp]
+    lib.sgemm_mxfp4_dequantize.restype = ci
+    mxfp4_args = [i64, i64, i64, f32, ci, vp, i64, vp, vp, vp, i64, f32, ci, vp, i64]
+    lib.sgemm_run_mxfp4.argtypes = mxfp4_args + [vp, i64, vp]
+    lib.sgemm_run_mxfp4.restype = ci
+    lib.sgemm_run_mxfp4_grouped.argtypes = [i64] + mxfp4_args + [vp, vp, i64, vp]
+    lib.sgemm_run_mxfp4_grouped.restype = ci
     lib.vector_add.argtypes = [i64, vp, vp, vp, vp]
     lib.vector_add.restype = ci
     lib.sgemm_mfma_ceiling.argtypes = [ci, ci, vp, i64, ctypes.POINTER(ctypes.c_double), vp]
@@ -119,6 +143,26 @@ def _stream(s):
     if isinstance(s, int):
         return s
     return s.cuda_stream
+
+
+def _type(t) -> int:
+    return TYPES[t] if isinstance(t, str) else int(t)
+
+
+def _offsets(x):
+    """_ptr of group offsets, which the kernels read as 64-bit integers."""
+    if hasattr(x, "dtype") and str(x.dtype) != "torch.int64":
+        raise TypeError("offsets must be int64")
+    if hasattr(x, "is_contiguous") and not x.is_contiguous():
+        raise ValueError("offsets must be contiguous")
+    return _ptr(x)
+
+
+def _size(fn: str, *args) -> int:
+    r = getattr(load_library(), fn)(*args)
+    if r < 0:
+        raise SgemmError(fn, int(r))
+    return int(r)
 
 
 def _check(fn: str, status: int) -> None:
@@ -202,6 +246,74 @@ def sgemm_run_bf16x3_ex_noalloc(transA, transB, M, N, K, alpha, A, lda, B, ldb, 
     _check("sgemm_run_bf16x3_ex_noalloc", load_library().sgemm_run_bf16x3_ex_noalloc(
         int(transA), int(transB), M, N, K, float(alpha), _ptr(A), lda, _ptr(B), ldb,
         float(beta), _ptr(C), ldc, _stream(stream)))
+
+
+def sgemm_run_grouped(transB, groups, M, N, K, alpha, A, lda, B, ldb, strideB, beta, C, ldc,
+                      offsets, stream=None) -> None:
+    """C(r, :) = alpha A(r, :) op(B_g) + beta C(r, :) for the rows r of each
+    group g (include/sgemm_grouped.h); offsets: groups + 1 int64 on the GPU."""
+    _check("sgemm_run_grouped", load_library().sgemm_run_grouped(
+        int(transB), groups, M, N, K, float(alpha), _ptr(A), lda, _ptr(B), ldb, strideB,
+        float(beta), _ptr(C), ldc, _offsets(offsets), _stream(stream)))
+
+
+def sgemm_run_grouped_k(groups, M, N, K, alpha, A, lda, B, ldb, beta, C, ldc, strideC, offsets,
+                        stream=None) -> None:
+    """C_g = alpha A_g^T B_g + beta C_g over the rows of each group g: the
+    gradient of sgemm_run_grouped's B (include/sgemm_grouped.h)."""
+    _check("sgemm_run_grouped_k", load_library().sgemm_run_grouped_k(
+        groups, M, N, K, float(alpha), _ptr(A), lda, _ptr(B), ldb, float(beta), _ptr(C), ldc,
+        strideC, _offsets(offsets), _stream(stream)))
+
+
+def sgemm_mxfp4_codes_size(rows, K) -> int:
+    """Bytes of the codes of a held rows x K matrix (include/sgemm_mxfp4.h)."""
+    return _size("sgemm_mxfp4_codes_size", rows, K)
+
+
+def sgemm_mxfp4_scales_size(rows, K) -> int:
+    """Bytes of its scales, with lds = rows."""
+    return _size("sgemm_mxfp4_scales_size", rows, K)
+
+
+def sgemm_mxfp4_workspace_size(typeA, M, K) -> int:
+    """Workspace bytes of a 4-bit product whose A has type `typeA`."""
+    return _size("sgemm_mxfp4_workspace_size", _type(typeA), M, K)
+
+
+def sgemm_mxfp4_quantize(trans, rows, K, type, X, ldx, codes, scales, lds, stream=None) -> None:
+    """Cast X (rows x K, or with trans stored K x rows; type "f32" or "bf16")
+    to microscaled 4-bit floats."""
+    _check("sgemm_mxfp4_quantize", load_library().sgemm_mxfp4_quantize(
+        int(trans), rows, K, _type(type), _ptr(X), ldx, _ptr(codes), _ptr(scales), lds,
+        _stream(stream)))
+
+
+def sgemm_mxfp4_dequantize(trans, rows, K, codes, scales, lds, type, X, ldx, stream=None) -> None:
+    """The values of a held matrix, written to X as sgemm_mxfp4_quantize reads it."""
+    _check("sgemm_mxfp4_dequantize", load_library().sgemm_mxfp4_dequantize(
+        int(trans), rows, K, _ptr(codes), _ptr(scales), lds, _type(type), _ptr(X), ldx,
+        _stream(stream)))
+
+
+def sgemm_run_mxfp4(M, N, K, alpha, typeA, A, lda, scalesA, B, scalesB, ldsb, beta, typeC, C, ldc,
+                    workspace=None, workspace_bytes=0, stream=None) -> None:
+    """C = alpha A B^T + beta C with B (and, for typeA "mxfp4", A) held in
+    microscaled 4-bit floats; an "f32" or "bf16" A is cast on the way."""
+    _check("sgemm_run_mxfp4", load_library().sgemm_run_mxfp4(
+        M, N, K, float(alpha), _type(typeA), _ptr(A), lda, _ptr(scalesA), _ptr(B), _ptr(scalesB),
+        ldsb, float(beta), _type(typeC), _ptr(C), ldc, _ptr(workspace), workspace_bytes,
+        _stream(stream)))
+
+
+def sgemm_run_mxfp4_grouped(groups, M, N, K, alpha, typeA, A, lda, scalesA, B, scalesB, ldsb, beta,
+                            typeC, C, ldc, offsets, workspace=None, workspace_bytes=0,
+                            stream=None) -> None:
+    """sgemm_run_mxfp4 for rows in groups, group g with rows g N .. of B."""
+    _check("sgemm_run_mxfp4_grouped", load_library().sgemm_run_mxfp4_grouped(
+        groups, M, N, K, float(alpha), _type(typeA), _ptr(A), lda, _ptr(scalesA), _ptr(B),
+        _ptr(scalesB), ldsb, float(beta), _type(typeC), _ptr(C), ldc, _offsets(offsets),
+        _ptr(workspace), workspace_bytes, _stream(stream)))
 
 
 def vector_add(n, A, B, C, stream=None) -> None:

@@ -58,9 +58,8 @@ int current_device_info(DeviceInfo *out) {
   return device_info(d, out);
 }
 
-constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
-// A launch's work-items (work-groups x threads) must fit 32 bits.
-constexpr int64_t kMaxWorkItems = (int64_t(1) << 32) - 1;
+using sgemm_api::kMaxDim;
+using sgemm_api::kMaxWorkItems;
 // bfloat16-split product: K up to 2^21 keeps a 256-row slice of a plane
 // within a buffer descriptor's range; (M + N) * Kp up to 2^34 keeps the split
 // launches below 2^32 work-items.
@@ -388,6 +387,13 @@ int bf16x3_ex_check(int transA, int transB, int64_t M, int64_t N, int64_t K, flo
   if (M > 0 && N > 0 && !C) return SGEMM_ERR_INVALID_VALUE;
   if (reads_ab && (!A || !B)) return SGEMM_ERR_INVALID_VALUE;
   return SGEMM_OK;
+}
+
+int current_device_cus(int *cus) {
+  DeviceInfo di;
+  const int rc = current_device_info(&di);
+  *cus = di.cus;
+  return rc;
 }
 
 bool ready() { return g_ready.load(std::memory_order_acquire) != 0; }

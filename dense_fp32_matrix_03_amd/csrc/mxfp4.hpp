@@ -1,0 +1,115 @@
+// mxfp4.hpp -- matrices held in microscaled 4-bit floating point
+// (include/sgemm_mxfp4.h): device helpers and host-side launchers.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "common.hpp"
+
+namespace sgemm {
+
+// A held matrix: codes [rows][Kp / 2], scales [Kp / 128][lds][4].
+struct Mxfp4Matrix {
+  const unsigned char *codes;
+  const unsigned *scales;  // one dword: the four scales of 128 k of a row
+  long lds;
+};
+
+inline long mxfp4_kp(long K) { return (K + 127) / 128 * 128; }
+
+struct CastArgs {
+  int rows, K;
+  long ldx;
+  int granules;  // Kp / 128
+  long lds;
+  const void *X;
+  void *codes;
+  unsigned *scales;
+};
+
+hipError_t launch_mxfp4_quantize(bool trans, bool bf16, const CastArgs &p, hipStream_t s);
+hipError_t launch_mxfp4_dequantize(bool trans, bool bf16, const CastArgs &p, hipStream_t s);
+
+// C = alpha A B^T + beta C over held B; A held, or (a_type 0: FP32, 1:
+// bfloat16) cast by the kernel.  offsets: null, or the groups of sgemm_run_mxfp4_grouped.
+struct Mxfp4Args {
+  int M, N, K, groups;
+  float alpha, beta;
+  Mxfp4Matrix a, b;
+  void *C;
+  long ldc;
+  const int64_t *offsets;
+};
+
+hipError_t launch_mxfp4_product(const Mxfp4Args &p, bool c_bf16, int cus, hipStream_t s);
+
+// Four floats (eight bfloat16) at an address aligned to one element.
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+typedef unsigned u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+
+// Eight consecutive values x[0 .. 7], zeros from the n-th on, as floats.
+template <bool BF16>
+__device__ __forceinline__ void load8(const void *x, int n, float v[8]) {
+  if constexpr (BF16) {
+    const unsigned short *p = static_cast<const unsigned short *>(x);
+    if (n >= 8) {
+      const u32x4_any t = *reinterpret_cast<const u32x4_any *>(p);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[2 * e] = __uint_as_float(t[e] << 16);
+        v[2 * e + 1] = __uint_as_float(t[e] & 0xffff0000u);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = e < n ? __uint_as_float((unsigned)p[e] << 16) : 0.f;
+    }
+  } else {
+    const float *p = static_cast<const float *>(x);
+    if (n >= 8) {
+      const f32x4_any lo = *reinterpret_cast<const f32x4_any *>(p);
+      const f32x4_any hi = *reinterpret_cast<const f32x4_any *>(p + 4);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[e] = lo[e];
+        v[4 + e] = hi[e];
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = e < n ? p[e] : 0.f;
+    }
+  }
+}
+
+// Scale byte of a block whose largest magnitude has the bits `top` (the
+// largest of the values' bits without signs: those order as the magnitudes do,
+// with infinities and then NaNs at the top).
+__device__ __forceinline__ unsigned mxfp4_scale(unsigned top) {
+  const unsigned e = top >> 23;
+  return e == 255u ? 255u : (e > 2u ? e - 2u : 0u);
+}
+
+// Codes of eight values of a block with scale byte s, the first in the lowest
+// four bits.  The values are first multiplied by 2^(127 - s), which is exact
+// (the largest ends below 8; what falls below the normal range is far below
+// 0.25 and gets code 0 either way); v_cvt_scalef32_pk_fp4_f32 then rounds to
+// the nearest value of the format, ties to the even code, at most 6.
+__device__ __forceinline__ unsigned mxfp4_codes8(const float v[8], unsigned s) {
+  if (s == 255u) return 0u;
+  const float up = __uint_as_float((254u - s) << 23);
+  unsigned r = 0;
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[0] * up, v[1] * up, 1.f, 0);
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[2] * up, v[3] * up, 1.f, 1);
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[4] * up, v[5] * up, 1.f, 2);
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[6] * up, v[7] * up, 1.f, 3);
+  return r;
+}
+
+__device__ __forceinline__ unsigned magnitude_bits(const float v[8]) {
+  unsigned top = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
+  return top;
+}
+
+}  // namespace sgemm

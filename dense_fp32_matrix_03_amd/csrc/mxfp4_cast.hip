@@ -1,0 +1,197 @@
+// mxfp4_cast.hip -- the cast of matrices to microscaled 4-bit floating point
+// and back (include/sgemm_mxfp4.h).
+//
+// Bound by memory: a cast reads 4 (or 2) bytes a value and writes 17/32.
+// Every value is read once, by a lane that keeps it until the block's scale
+// is known.
+//
+// k along the stored rows' columns (not transposed): a lane has 8 consecutive
+// k, so 4 lanes have a block and 16 a granule of 128 k; the block's largest
+// magnitude is found by two exchanges inside a quad of lanes, and the four
+// scales of a granule are gathered into the dword that is stored.  Values
+// stored transposed: a lane has one row's block, 32 loads that 64 lanes make
+// of consecutive addresses, and its largest magnitude needs no exchange; the
+// four waves of a work-group have the four blocks of a granule.
+#include "mxfp4.hpp"
+
+namespace sgemm {
+
+namespace {
+
+constexpr int kGranule = 128;
+constexpr int kRowsPerGroup = 32;  // rows of a work-group, not transposed
+
+// One granule of 32 rows per work-group of 4 waves: 16 lanes a row.
+template <bool BF16>
+__global__ void __launch_bounds__(256) quantize_kernel(CastArgs p) {
+  const int tid = threadIdx.x;
+  const int g = blockIdx.x % p.granules, tile = blockIdx.x / p.granules;
+  const int l16 = tid % 16;
+  const int k = g * kGranule + l16 * 8;
+  const int left = p.K - k;
+#pragma unroll
+  for (int i = 0; i < kRowsPerGroup / 16; ++i) {
+    const int row = tile * kRowsPerGroup + i * 16 + tid / 16;
+    const bool in = row < p.rows;
+    float v[8];
+    const char *x = static_cast<const char *>(p.X) + ((long)row * p.ldx + k) * (BF16 ? 2 : 4);
+    load8<BF16>(x, in ? left : 0, v);
+    unsigned top = magnitude_bits(v);
+    top = max(top, (unsigned)__shfl_xor((int)top, 1));
+    top = max(top, (unsigned)__shfl_xor((int)top, 2));
+    const unsigned s = mxfp4_scale(top);
+    unsigned all = s << (8 * (l16 / 4));
+    all |= (unsigned)__shfl_xor((int)all, 4);
+    all |= (unsigned)__shfl_xor((int)all, 8);
+    if (in) {
+      const unsigned codes = mxfp4_codes8(v, s);
+      reinterpret_cast<unsigned *>(p.codes)[(long)row * (p.granules * 16) + g * 16 + l16] = codes;
+      if (l16 == 0) p.scales[(long)g * p.lds + row] = all;
+    }
+  }
+}
+
+// 64 rows and a granule per work-group; wave w has block w.
+template <bool BF16>
+__global__ void __launch_bounds__(256) quantize_transposed_kernel(CastArgs p) {
+  const int lane = threadIdx.x % kWave, w = threadIdx.x / kWave;
+  const int g = blockIdx.x % p.granules, tile = blockIdx.x / p.granules;
+  const int row = tile * kWave + lane;
+  const int k0 = g * kGranule + w * 32;
+  const bool in = row < p.rows;
+  float v[32];
+#pragma unroll
+  for (int e = 0; e < 32; ++e) {
+    const long at = (long)(k0 + e) * p.ldx + row;
+    v[e] = 0.f;
+    if (in && k0 + e < p.K) {
+      if constexpr (BF16)
+        v[e] = __uint_as_float((unsigned)static_cast<const unsigned short *>(p.X)[at] << 16);
+      else
+        v[e] = static_cast<const float *>(p.X)[at];
+    }
+  }
+  unsigned top = 0;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) top = max(top, magnitude_bits(v + 8 * q));
+  const unsigned s = mxfp4_scale(top);
+  __shared__ unsigned char scale[kWave][4];
+  scale[lane][w] = (unsigned char)s;
+  if (in) {
+    uint4 c;
+    c.x = mxfp4_codes8(v, s);
+    c.y = mxfp4_codes8(v + 8, s);
+    c.z = mxfp4_codes8(v + 16, s);
+    c.w = mxfp4_codes8(v + 24, s);
+    reinterpret_cast<uint4 *>(p.codes)[(long)row * (p.granules * 4) + g * 4 + w] = c;
+  }
+  __syncthreads();
+  if (w == 0 && in)
+    p.scales[(long)g * p.lds + row] = *reinterpret_cast<const unsigned *>(scale[lane]);
+}
+
+// The scale 2^(s - 127): 2^-127 is below the normal range; 255 is a NaN.
+__device__ __forceinline__ float scale_value(unsigned s) {
+  return __uint_as_float(s == 255u ? 0x7fc00000u : (s ? s << 23 : 0x00400000u));
+}
+
+// The eight values of a dword of codes.
+__device__ __forceinline__ void decode8(unsigned codes, float scale, float v[8]) {
+  constexpr unsigned kGrid = 0xc8643210u;  // twice the magnitudes 0, .5, 1, 1.5, 2, 3, 4, 6
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const unsigned c = codes >> (4 * e) & 15u;
+    const float m = 0.5f * (float)(kGrid >> (4 * (c & 7u)) & 15u);
+    v[e] = (c & 8u ? -m : m) * scale;
+  }
+}
+
+// Exact: a value of the format has at most 2 significant bits.
+__device__ __forceinline__ unsigned short to_bf16(float x) {
+  return __builtin_bit_cast(unsigned short, (__bf16)x);
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(256) dequantize_kernel(CastArgs p) {
+  const int tid = threadIdx.x;
+  const int g = blockIdx.x % p.granules, tile = blockIdx.x / p.granules;
+  const int l16 = tid % 16;
+  const int k = g * kGranule + l16 * 8;
+#pragma unroll
+  for (int i = 0; i < kRowsPerGroup / 16; ++i) {
+    const int row = tile * kRowsPerGroup + i * 16 + tid / 16;
+    if (row >= p.rows) break;
+    const unsigned codes =
+        reinterpret_cast<const unsigned *>(p.codes)[(long)row * (p.granules * 16) + g * 16 + l16];
+    const unsigned s = p.scales[(long)g * p.lds + row] >> (8 * (l16 / 4)) & 255u;
+    float v[8];
+    decode8(codes, scale_value(s), v);
+    char *x = static_cast<char *>(const_cast<void *>(p.X)) +
+              ((long)row * p.ldx + k) * (BF16 ? 2 : 4);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if (k + e >= p.K) break;
+      if constexpr (BF16)
+        reinterpret_cast<unsigned short *>(x)[e] = to_bf16(v[e]);
+      else
+        reinterpret_cast<float *>(x)[e] = v[e];
+    }
+  }
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(256) dequantize_transposed_kernel(CastArgs p) {
+  const int lane = threadIdx.x % kWave, w = threadIdx.x / kWave;
+  const int g = blockIdx.x % p.granules, tile = blockIdx.x / p.granules;
+  const int row = tile * kWave + lane;
+  const int k0 = g * kGranule + w * 32;
+  if (row >= p.rows) return;
+  const uint4 c = reinterpret_cast<const uint4 *>(p.codes)[(long)row * (p.granules * 4) + g * 4 + w];
+  const float scale = scale_value(p.scales[(long)g * p.lds + row] >> (8 * w) & 255u);
+  float v[32];
+  decode8(c.x, scale, v);
+  decode8(c.y, scale, v + 8);
+  decode8(c.z, scale, v + 16);
+  decode8(c.w, scale, v + 24);
+#pragma unroll
+  for (int e = 0; e < 32; ++e) {
+    if (k0 + e >= p.K) break;
+    const long at = (long)(k0 + e) * p.ldx + row;
+    if constexpr (BF16)
+      static_cast<unsigned short *>(const_cast<void *>(p.X))[at] = to_bf16(v[e]);
+    else
+      static_cast<float *>(const_cast<void *>(p.X))[at] = v[e];
+  }
+}
+
+}  // namespace
+
+hipError_t launch_mxfp4_quantize(bool trans, bool bf16, const CastArgs &p, hipStream_t s) {
+  const long tiles = (p.rows + (trans ? kWave : kRowsPerGroup) - 1L) / (trans ? kWave : kRowsPerGroup);
+  const dim3 grid((unsigned)(tiles * p.granules)), block(256);
+  if (trans && bf16)
+    hipLaunchKernelGGL(quantize_transposed_kernel<true>, grid, block, 0, s, p);
+  else if (trans)
+    hipLaunchKernelGGL(quantize_transposed_kernel<false>, grid, block, 0, s, p);
+  else if (bf16)
+    hipLaunchKernelGGL(quantize_kernel<true>, grid, block, 0, s, p);
+  else
+    hipLaunchKernelGGL(quantize_kernel<false>, grid, block, 0, s, p);
+  return hipGetLastError();
+}
+
+hipError_t launch_mxfp4_dequantize(bool trans, bool bf16, const CastArgs &p, hipStream_t s) {
+  const long tiles = (p.rows + (trans ? kWave : kRowsPerGroup) - 1L) / (trans ? kWave : kRowsPerGroup);
+  const dim3 grid((unsigned)(tiles * p.granules)), block(256);
+  if (trans && bf16)
+    hipLaunchKernelGGL(dequantize_transposed_kernel<true>, grid, block, 0, s, p);
+  else if (trans)
+    hipLaunchKernelGGL(dequantize_transposed_kernel<false>, grid, block, 0, s, p);
+  else if (bf16)
+    hipLaunchKernelGGL(dequantize_kernel<true>, grid, block, 0, s, p);
+  else
+    hipLaunchKernelGGL(dequantize_kernel<false>, grid, block, 0, s, p);
+  return hipGetLastError();
+}
+
+}  // namespace sgemm

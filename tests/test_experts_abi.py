@@ -1,0 +1,193 @@
+"""Entry points for products grouped by expert and for microscaled 4-bit
+operands: argument checks, which precede any runtime call (no GPU needed)."""
+import ctypes
+
+import pytest
+
+import dense_fp32_matrix_03_amd as sg
+
+INVALID, LARGE, READY = ("SGEMM_ERR_INVALID_VALUE", "SGEMM_ERR_TOO_LARGE",
+                         "SGEMM_ERR_NOT_INITIALIZED")
+
+
+def _name(rc):
+    return sg.sgemm_status_string(rc)
+
+
+def _grouped(**over):
+    a = dict(transB=0, groups=3, M=8, N=5, K=7, alpha=1.0, A=16, lda=7, B=16, ldb=5, strideB=35,
+             beta=0.0, C=16, ldc=5, offsets=16)
+    a.update(over)
+    return _name(sg.load_library().sgemm_run_grouped(*a.values(), None))
+
+
+@pytest.mark.parametrize("over,status", [
+    ({}, READY),
+    (dict(transB=2), INVALID), (dict(groups=-1), INVALID), (dict(M=-1), INVALID),
+    (dict(N=-1), INVALID), (dict(K=-1), INVALID),
+    (dict(lda=6), INVALID), (dict(ldb=4), INVALID), (dict(ldc=4), INVALID),
+    (dict(transB=1, ldb=6), INVALID), (dict(transB=1, ldb=7), READY),
+    (dict(strideB=-1), INVALID), (dict(strideB=0), READY),
+    (dict(C=None), INVALID), (dict(offsets=None), INVALID), (dict(A=None), INVALID),
+    (dict(B=None), INVALID), (dict(offsets=12), INVALID), (dict(C=18), INVALID),
+    (dict(A=18), INVALID), (dict(B=18), INVALID),
+    (dict(A=None, B=None, alpha=0.0), READY), (dict(A=None, B=None, K=0), READY),
+    (dict(A=None, B=None, C=None, offsets=None, groups=0), READY),
+    (dict(A=None, B=None, C=None, offsets=None, M=0), READY),
+    (dict(groups=4096), READY), (dict(groups=4097), LARGE),
+    (dict(M=2 ** 31), LARGE), (dict(lda=2 ** 22), LARGE), (dict(ldb=2 ** 22), LARGE),
+    (dict(lda=2 ** 22, K=0), READY),
+    # one 256-thread work-group per 16 x 64 block, and one more for each group
+    (dict(M=2 ** 27, N=64, ldb=64, ldc=64), READY),
+    (dict(M=2 ** 28, N=64, ldb=64, ldc=64), LARGE),
+])
+def test_grouped_checks(over, status):
+    assert _grouped(**over) == status
+
+
+def _grouped_k(**over):
+    a = dict(groups=3, M=8, N=5, K=7, alpha=1.0, A=16, lda=8, B=16, ldb=5, beta=0.0, C=16, ldc=5,
+             strideC=40, offsets=16)
+    a.update(over)
+    return _name(sg.load_library().sgemm_run_grouped_k(*a.values(), None))
+
+
+@pytest.mark.parametrize("over,status", [
+    ({}, READY), (dict(groups=-1), INVALID), (dict(M=-1), INVALID), (dict(K=-1), INVALID),
+    (dict(lda=7), INVALID), (dict(ldb=4), INVALID), (dict(ldc=4), INVALID),
+    (dict(strideC=39), INVALID), (dict(strideC=0, groups=1), READY), (dict(strideC=-1), INVALID),
+    (dict(C=None), INVALID), (dict(offsets=None), INVALID), (dict(A=None), INVALID),
+    (dict(A=None, B=None, K=0), READY), (dict(A=None, B=None, alpha=0.0), READY),
+    (dict(offsets=20), INVALID), (dict(groups=4097), LARGE), (dict(lda=2 ** 22), LARGE),
+    (dict(groups=1024, M=4096, N=4096, lda=4096, ldb=4096, ldc=4096, strideC=2 ** 24), LARGE),
+    (dict(groups=512, M=4096, N=4096, lda=4096, ldb=4096, ldc=4096, strideC=2 ** 24), READY),
+])
+def test_grouped_k_checks(over, status):
+    assert _grouped_k(**over) == status
+
+
+def test_mxfp4_sizes():
+    assert sg.sgemm_mxfp4_codes_size(3, 1) == 3 * 64
+    assert sg.sgemm_mxfp4_codes_size(3, 128) == 3 * 64
+    assert sg.sgemm_mxfp4_codes_size(3, 129) == 3 * 128
+    assert sg.sgemm_mxfp4_scales_size(3, 129) == 3 * 8
+    assert sg.sgemm_mxfp4_codes_size(0, 5) == 0 and sg.sgemm_mxfp4_codes_size(5, 0) == 0
+    assert sg.sgemm_mxfp4_workspace_size("mxfp4", 100, 100) == 0
+    assert sg.sgemm_mxfp4_workspace_size("f32", 100, 100) == 100 * (64 + 4)
+    assert sg.sgemm_mxfp4_workspace_size("bf16", 100, 100) == 100 * (64 + 4)
+    lib = sg.load_library()
+    assert _name(lib.sgemm_mxfp4_codes_size(-1, 5)) == INVALID
+    assert _name(lib.sgemm_mxfp4_scales_size(5, 2 ** 21 + 1)) == LARGE
+    assert _name(lib.sgemm_mxfp4_workspace_size(3, 5, 5)) == INVALID
+    assert _name(lib.sgemm_mxfp4_workspace_size(0, 2 ** 31, 5)) == LARGE
+    with pytest.raises(sg.SgemmError):
+        sg.sgemm_mxfp4_codes_size(-1, 5)
+
+
+@pytest.mark.parametrize("over,status", [
+    ({}, READY), (dict(trans=2), INVALID), (dict(type=2), INVALID), (dict(type=-1), INVALID),
+    (dict(rows=-1), INVALID), (dict(K=-1), INVALID), (dict(ldx=6), INVALID),
+    (dict(trans=1, ldx=7), INVALID), (dict(trans=1, ldx=8), READY), (dict(lds=7), INVALID),
+    (dict(X=None), INVALID), (dict(codes=None), INVALID), (dict(scales=None), INVALID),
+    (dict(codes=24), INVALID), (dict(scales=18), INVALID), (dict(X=18), INVALID),
+    (dict(X=18, type=1), READY), (dict(X=17, type=1), INVALID),
+    (dict(rows=0, X=None, codes=None, scales=None), READY),
+    (dict(K=2 ** 21 + 1, ldx=2 ** 22), LARGE), (dict(lds=2 ** 31), LARGE),
+    (dict(rows=2 ** 20, K=2 ** 21, ldx=2 ** 21, lds=2 ** 20), LARGE),
+])
+def test_mxfp4_cast_checks(over, status):
+    a = dict(trans=0, rows=8, K=7, type=0, X=16, ldx=7, codes=16, scales=16, lds=8)
+    a.update(over)
+    lib = sg.load_library()
+    assert _name(lib.sgemm_mxfp4_quantize(*a.values(), None)) == status
+    t, r, k, ty, X, ldx, c, s, lds = a.values()
+    assert _name(lib.sgemm_mxfp4_dequantize(t, r, k, c, s, lds, ty, X, ldx, None)) == status
+
+
+PRODUCT = dict(M=8, N=5, K=7, alpha=1.0, typeA=0, A=16, lda=7, scalesA=None, B=16, scalesB=16,
+               ldsb=15, beta=0.0, typeC=0, C=16, ldc=5)
+WORKSPACE = dict(workspace=256, workspace_bytes=8 * 68)
+
+
+@pytest.mark.parametrize("over,status", [
+    ({}, READY), (dict(typeA=3), INVALID), (dict(typeC=2), INVALID), (dict(M=-1), INVALID),
+    (dict(N=-1), INVALID), (dict(K=-1), INVALID), (dict(lda=6), INVALID), (dict(ldc=4), INVALID),
+    (dict(ldsb=4), INVALID), (dict(A=None), INVALID), (dict(B=None), INVALID),
+    (dict(scalesB=None), INVALID), (dict(C=None), INVALID), (dict(B=24), INVALID),
+    (dict(scalesB=18), INVALID), (dict(C=18), INVALID), (dict(C=18, typeC=1), READY),
+    (dict(A=18), INVALID), (dict(A=18, typeA=1), READY),
+    (dict(workspace=None), INVALID), (dict(workspace=264), INVALID),
+    (dict(workspace_bytes=8 * 68 - 1), INVALID),
+    # held A: lda is the scales' leading dimension, no workspace
+    (dict(typeA=2, lda=8, scalesA=16, workspace=None, workspace_bytes=0), READY),
+    (dict(typeA=2, lda=7, scalesA=16), INVALID), (dict(typeA=2, lda=8), INVALID),
+    (dict(typeA=2, lda=8, scalesA=16, A=24), INVALID),
+    (dict(typeA=2, lda=8, scalesA=18), INVALID),
+    # nothing is read: alpha or K is zero
+    (dict(alpha=0.0, A=None, B=None, scalesB=None, workspace=None), READY),
+    (dict(K=0, A=None, B=None, scalesB=None, workspace=None), READY),
+    (dict(M=0, A=None, B=None, scalesB=None, C=None, workspace=None), READY),
+    (dict(K=2 ** 21 + 1, lda=2 ** 22), LARGE), (dict(M=2 ** 31), LARGE),
+    (dict(ldsb=2 ** 31), LARGE),
+])
+def test_mxfp4_product_checks(over, status):
+    lib = sg.load_library()
+    a = dict(PRODUCT, **WORKSPACE)
+    a.update(over)
+    assert _name(lib.sgemm_run_mxfp4(*a.values(), None)) == status
+    ws, nbytes = a.pop("workspace"), a.pop("workspace_bytes")
+    if a["ldsb"] == 15:  # enough for three groups of five rows
+        run = lib.sgemm_run_mxfp4_grouped
+        assert _name(run(3, *a.values(), 16, ws, nbytes, None)) == status
+        if status == READY:
+            assert _name(run(-1, *a.values(), 16, ws, nbytes, None)) == INVALID
+            assert _name(run(0, *a.values(), None, ws, nbytes, None)) == READY
+            few = dict(a, ldsb=14)
+            assert _name(run(3, *few.values(), 16, ws, nbytes, None)) == INVALID
+            if a["M"]:
+                assert _name(run(3, *a.values(), None, ws, nbytes, None)) == INVALID
+                assert _name(run(3, *a.values(), 12, ws, nbytes, None)) == INVALID
+            many = dict(a, ldsb=4097 * 5)
+            assert _name(run(4097, *many.values(), 16, ws, nbytes, None)) == LARGE
+
+
+def test_binding_checks_offsets():
+    torch = pytest.importorskip("torch")
+    with pytest.raises(TypeError, match="int64"):
+        sg._offsets(torch.zeros(4, dtype=torch.int32))
+    with pytest.raises(ValueError, match="contiguous"):
+        sg._offsets(torch.zeros(8, dtype=torch.int64)[::2])
+    assert sg._offsets(4096) == 4096
+
+
+# ------------------------------------------------------ the map of work-groups
+def _ranges(offsets, M):
+    """The rows of each group as the kernels clamp them."""
+    out = []
+    for s, e in zip(offsets, offsets[1:]):
+        first = min(max(s, 0), M)
+        out.append((first, first if e < first else min(e, M)))
+    return out
+
+
+def test_launched_tile_rows_cover_any_groups():
+    """sum ceil(rows / bm) <= M / bm + min(groups, M) for every way to divide
+    M rows, the bound by which the host sizes a launch."""
+    import random
+    rng = random.Random(7)
+    for _ in range(3000):
+        M, groups = rng.randrange(1, 300), rng.randrange(1, 40)
+        cuts = sorted(rng.randrange(0, M + 1) for _ in range(groups + 1))
+        for bm in (16, 32, 64, 128):
+            tiles = sum((e - s + bm - 1) // bm for s, e in _ranges(cuts, M))
+            assert tiles <= M // bm + min(groups, M)
+
+
+def test_clamped_groups_stay_inside():
+    import random
+    rng = random.Random(8)
+    for _ in range(2000):
+        M = rng.randrange(1, 50)
+        at = [rng.choice([-2 ** 63, -1, 0, rng.randrange(-60, 120), M, 2 ** 62]) for _ in range(9)]
+        for s, e in _ranges(at, M):
+            assert 0 <= s <= e <= M
