@@ -42,7 +42,45 @@ struct Mxfp4Args {
   const int64_t *offsets;
 };
 
+// Picks the kernel for the product.
 hipError_t launch_mxfp4_product(const Mxfp4Args &p, bool c_bf16, int cus, hipStream_t s);
+// mxfp4_tile.hip: tiles of 256 x 256 or 128 x 128 through LDS.
+hipError_t launch_mxfp4_tile(int tile, const Mxfp4Args &p, bool c_bf16, hipStream_t s);
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+// Operands in 4 bits fill the lower half of the scaled matrix instructions'
+// registers; 4 is the code of the format.
+__device__ __forceinline__ i32x8 widen(i32x4 v) {
+  return __builtin_shufflevector(v, v, 0, 1, 2, 3, -1, -1, -1, -1);
+}
+constexpr int kFormatFp4 = 4;
+
+// 16 x 16 x 128 and 32 x 32 x 64 on 4-bit operands, byte S of the scales.
+template <int S>
+__device__ __forceinline__ f32x4 mfma_fp4_16x16x128(i32x4 a, i32x4 b, f32x4 c, int sa, int sb) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(widen(a), widen(b), c, kFormatFp4,
+                                                          kFormatFp4, S, sa, S, sb);
+}
+template <int S>
+__device__ __forceinline__ f32x16 mfma_fp4_32x32x64(i32x4 a, i32x4 b, f32x16 c, int sa, int sb) {
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(widen(a), widen(b), c, kFormatFp4,
+                                                         kFormatFp4, S, sa, S, sb);
+}
+
+// C[at] = alpha sum + beta C[at], rounded to single precision once and then,
+// for bfloat16, to the nearest.  C is read only when beta != 0.
+template <bool CBF16>
+__device__ __forceinline__ void store_c(const Mxfp4Args &p, long at, float sum) {
+  if constexpr (CBF16) {
+    __bf16 *C = static_cast<__bf16 *>(p.C) + at;
+    *C = (__bf16)(p.beta == 0.f ? p.alpha * sum : fmaf(p.alpha, sum, p.beta * (float)*C));
+  } else {
+    float *C = static_cast<float *>(p.C) + at;
+    *C = p.beta == 0.f ? p.alpha * sum : fmaf(p.alpha, sum, p.beta * *C);
+  }
+}
 
 // Four floats (eight bfloat16) at an address aligned to one element.
 typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));

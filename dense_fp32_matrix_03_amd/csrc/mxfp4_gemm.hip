@@ -20,16 +20,6 @@ namespace sgemm {
 
 namespace {
 
-typedef int i32x4 __attribute__((ext_vector_type(4)));
-typedef int i32x8 __attribute__((ext_vector_type(8)));
-
-// Operands in 4 bits fill the lower half of the instruction's registers.
-__device__ __forceinline__ i32x8 widen(i32x4 v) {
-  return __builtin_shufflevector(v, v, 0, 1, 2, 3, -1, -1, -1, -1);
-}
-
-constexpr int kFormatFp4 = 4;
-
 // MT x NT blocks of 16 x 16 per wave; KS waves split k in units of 512.
 template <int MT, int NT, int KS, bool CBF16>
 __global__ void __launch_bounds__(KS *kWave) mxfp4_kernel(Mxfp4Args p, int tiles_m, int tiles_n) {
@@ -97,9 +87,7 @@ __global__ void __launch_bounds__(KS *kWave) mxfp4_kernel(Mxfp4Args p, int tiles
       for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int j = 0; j < NT; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-              widen(a[i][s]), widen(b[j][s]), acc[i][j], kFormatFp4, kFormatFp4, s, as[i], s,
-              bs[j]);
+          acc[i][j] = mfma_fp4_16x16x128<s>(a[i][s], b[j][s], acc[i][j], as[i], bs[j]);
     });
   }
 
@@ -133,15 +121,7 @@ __global__ void __launch_bounds__(KS *kWave) mxfp4_kernel(Mxfp4Args p, int tiles
       for (int j = 0; j < NT; ++j) {
         const int n = n0 + 16 * j + r16;
         if (n >= p.N) continue;
-        const long at = (a_row + m) * p.ldc + n;
-        const float v = p.alpha * acc[i][j][e];
-        if constexpr (CBF16) {
-          __bf16 *C = static_cast<__bf16 *>(p.C) + at;
-          *C = (__bf16)(p.beta == 0.f ? v : fmaf(p.alpha, acc[i][j][e], p.beta * (float)*C));
-        } else {
-          float *C = static_cast<float *>(p.C) + at;
-          *C = p.beta == 0.f ? v : fmaf(p.alpha, acc[i][j][e], p.beta * *C);
-        }
+        store_c<CBF16>(p, (a_row + m) * p.ldc + n, acc[i][j][e]);
       }
     }
 }
@@ -149,6 +129,8 @@ __global__ void __launch_bounds__(KS *kWave) mxfp4_kernel(Mxfp4Args p, int tiles
 }  // namespace
 
 hipError_t launch_mxfp4_product(const Mxfp4Args &p, bool c_bf16, int cus, hipStream_t s) {
+  const long mean = p.M / (p.offsets ? p.groups : 1);
+  if (mean > 64) return launch_mxfp4_tile(mean > 512 ? 256 : 128, p, c_bf16, s);
   const int tiles_n = (p.N + 31) / 32, tiles_m = (p.M + 15) / 16;
   const long rows = p.offsets ? group_tile_rows(p.M, p.groups, 16) : tiles_m;
   const dim3 grid((unsigned)(rows * tiles_n)), block(4 * kWave);

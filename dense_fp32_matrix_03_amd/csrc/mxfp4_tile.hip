@@ -1,0 +1,245 @@
+// mxfp4_tile.hip -- products of matrices held in microscaled 4-bit floating
+// point whose operand slices reach LDS by buffer-to-LDS loads.
+//
+// C(m, n) = alpha sum_b 2^(sa(m, b) + sb(n, b) - 254) sum_{k in b} a(m, k) b(n, k)
+// + beta C(m, n), on v_mfma_scale_f32_32x32x64_f8f6f4: 32 rows of A by 32 rows
+// of B over 64 k, lane half h supplying one block of 32 codes (16 bytes) of row
+// l % 32 of each operand and its scale byte, which op_sel picks from the four
+// bytes of a register.
+//
+// A slice is 256 k: 128 bytes of codes a row, and two granules' dwords of
+// scales.  Half h has granule h of the slice and instruction s its block s, so
+// one dword of scales serves a lane for the slice's four instructions.  The
+// codes' LDS image is [row][8 chunks of 16 bytes], chunk c at c ^ kc_swizzle
+// (mfma_dma.hpp), the scales' [granule][row].
+//
+// Edges.  The descriptors end at the last row's last byte, so rows past it
+// read as zeros.  Where K ends inside a slice the second granule's codes are
+// whatever follows in memory, below that end (every code is finite), but both
+// operands' scales there read as 0: the products are at most 36 2^-254 and
+// vanish in single precision.
+#include "grouped_map.hpp"
+#include "mfma_dma.hpp"
+#include "mxfp4.hpp"
+
+namespace sgemm {
+
+namespace {
+
+constexpr int kSliceBytes = 128;  // codes of a row's slice
+
+template <int BM, int BN, int WM, int WN, bool CBF16>
+__global__ void __launch_bounds__(WM *WN *kWave)
+mxfp4_tile_kernel(Mxfp4Args p, TileMap tmap, int tiles_n) {
+  constexpr int NW = WM * WN;
+  constexpr int WTM = BM / WM, WTN = BN / WN, FM = WTM / 32, FN = WTN / 32;
+  constexpr int QA = BM * kSliceBytes / 1024 / NW, QB = BN * kSliceBytes / 1024 / NW;
+  constexpr int QS = (BM + BN) / 32 / NW;  // loads of 64 rows' scales of a granule
+  static_assert(QA * NW * 1024 == BM * kSliceBytes && QB * NW * 1024 == BN * kSliceBytes &&
+                    QS * NW * 32 == BM + BN,
+                "loads must split evenly over the waves");
+  constexpr int kLoads = QA + QB + QS;
+
+  __shared__ __attribute__((aligned(1024))) float As0[BM * kSliceBytes / 4];
+  __shared__ __attribute__((aligned(1024))) float As1[BM * kSliceBytes / 4];
+  __shared__ __attribute__((aligned(1024))) float Bs0[BN * kSliceBytes / 4];
+  __shared__ __attribute__((aligned(1024))) float Bs1[BN * kSliceBytes / 4];
+  __shared__ __attribute__((aligned(1024))) float Ss0[2 * (BM + BN)];  // A's, then B's
+  __shared__ __attribute__((aligned(1024))) float Ss1[2 * (BM + BN)];
+  auto stage_a = [&](auto S) -> float * { return decltype(S)::value == 0 ? As0 : As1; };
+  auto stage_b = [&](auto S) -> float * { return decltype(S)::value == 0 ? Bs0 : Bs1; };
+  auto stage_s = [&](auto S) -> float * { return decltype(S)::value == 0 ? Ss0 : Ss1; };
+
+  const int lane = threadIdx.x % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int wm = wave / WN, wn = wave % WN;
+  const int r32 = lane % 32, half = lane / 32;
+
+  long a_row = 0, b_row = 0;  // first row of the group in A (and C), and of its B
+  int m0, n0, m_end = p.M;
+  if (p.offsets) {
+    const GroupTile t = group_tile(p.offsets, p.groups, p.M, BM, tiles_n, 8);
+    if (!t.valid) return;
+    a_row = t.row0;
+    b_row = (long)t.g * p.N;
+    m0 = t.tm * BM;
+    n0 = t.tn * BN;
+    m_end = t.rows;
+  } else {
+    int bidx, tm, tn;
+    tmap.tile(xcd_contiguous_id(blockIdx.x, gridDim.x), bidx, tm, tn);
+    m0 = tm * BM;
+    n0 = tn * BN;
+  }
+  const int granules = (p.K + 127) / 128;
+  const int pitch = granules * 64;  // bytes of a row's codes
+  const int rows_a = min(BM, m_end - m0), rows_b = min(BN, p.N - n0);
+  const unsigned char *a0 = p.a.codes + (a_row + m0) * pitch;
+  const unsigned char *b0 = p.b.codes + (b_row + n0) * pitch;
+  const unsigned *sa0 = p.a.scales + a_row + m0;
+  const unsigned *sb0 = p.b.scales + b_row + n0;
+
+  unsigned offA[QA], offB[QB];
+#pragma unroll
+  for (int q = 0; q < QA; ++q) {
+    const int f = (wave + q * NW) * kWave + lane, row = f / 8;
+    offA[q] = (unsigned)(row * pitch + 16 * ((f % 8) ^ kc_swizzle<32, true>(row)));
+  }
+#pragma unroll
+  for (int q = 0; q < QB; ++q) {
+    const int f = (wave + q * NW) * kWave + lane, row = f / 8;
+    offB[q] = (unsigned)(row * pitch + 16 * ((f % 8) ^ kc_swizzle<32, true>(row)));
+  }
+
+  const int nk = (granules + 1) / 2;
+  auto rsrc = [](const void *base, int records) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, records,
+                                             kRawBufferWord3);
+  };
+  auto dma = [&](auto S, int t) {
+    const bool live = t < nk;
+    const int k0 = live ? t * kSliceBytes : 0;
+    const __amdgpu_buffer_rsrc_t ra = rsrc(a0 + k0, live ? rows_a * pitch - k0 : 0);
+    const __amdgpu_buffer_rsrc_t rb = rsrc(b0 + k0, live ? rows_b * pitch - k0 : 0);
+#pragma unroll
+    for (int q = 0; q < QA; ++q)
+      lds_dma<true>(ra, stage_a(S) + (wave + q * NW) * 256, offA[q]);
+#pragma unroll
+    for (int q = 0; q < QB; ++q)
+      lds_dma<true>(rb, stage_b(S) + (wave + q * NW) * 256, offB[q]);
+#pragma unroll
+    for (int q = 0; q < QS; ++q) {
+      const int u = wave + q * NW;  // uniform: which 64 rows of which granule
+      const bool of_a = u < BM / 32;
+      const int v = of_a ? u : u - BM / 32, per = of_a ? BM / 64 : BN / 64;
+      const int j = v / per, r0 = v % per * 64;
+      const int g = 2 * t + j;
+      const long lds = of_a ? p.a.lds : p.b.lds;
+      const unsigned *base = (of_a ? sa0 : sb0) + (g < granules ? g * lds : 0);
+      const int records = g < granules ? 4 * (of_a ? rows_a : rows_b) : 0;
+      lds_dma<false>(rsrc(base, records),
+                     stage_s(S) + (of_a ? 0 : 2 * BM) + j * (of_a ? BM : BN) + r0,
+                     (unsigned)(r0 + lane) * 4u);
+    }
+  };
+
+  const int sw = kc_swizzle<32, true>(r32);
+  struct Ops {
+    i32x4 a[FM], b[FN];
+  };
+  struct Scales {
+    int a[FM], b[FN];
+  };
+  auto read_ops = [&](auto S, int s, Ops &o) {
+    const int ch = ((4 * half + s) ^ sw) * 4;
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+      o.a[i] = *reinterpret_cast<const i32x4 *>(stage_a(S) + (wm * WTM + i * 32 + r32) * 32 + ch);
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+      o.b[j] = *reinterpret_cast<const i32x4 *>(stage_b(S) + (wn * WTN + j * 32 + r32) * 32 + ch);
+  };
+  auto read_scales = [&](auto S, Scales &c) {
+    const int *sa = reinterpret_cast<const int *>(stage_s(S)) + half * BM + wm * WTM + r32;
+    const int *sb = reinterpret_cast<const int *>(stage_s(S)) + 2 * BM + half * BN + wn * WTN + r32;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) c.a[i] = sa[i * 32];
+#pragma unroll
+    for (int j = 0; j < FN; ++j) c.b[j] = sb[j * 32];
+  };
+
+  f32x16 acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+
+  Ops cur, nxt;
+  Scales sc, sn;
+  auto mma = [&](auto STEP, const Ops &o) {
+    constexpr int s = decltype(STEP)::value;
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+        acc[i][j] = mfma_fp4_32x32x64<s>(o.a[i], o.b[j], acc[i][j], sc.a[i], sc.b[j]);
+  };
+  using S0 = std::integral_constant<int, 0>;
+  using S1 = std::integral_constant<int, 1>;
+  // Slice t is in stage S, slice t + 1 on its way to the other one.  The last
+  // step waits for it, and for every wave to be done with stage S, then sends
+  // slice t + 2 there and reads slice t + 1's first operands.
+  auto slice = [&](auto S, int t) {
+    using SN = std::integral_constant<int, 1 - decltype(S)::value>;
+    static_for<4>([&](auto STEP) {
+      constexpr int s = decltype(STEP)::value;
+      if constexpr (s < 3) {
+        read_ops(S, s + 1, nxt);
+      } else {
+        dma_barrier();
+        dma(S, t + 2);
+        read_ops(SN(), 0, nxt);
+        read_scales(SN(), sn);
+      }
+      mma(STEP, cur);
+      cur = nxt;
+    });
+    sc = sn;
+  };
+
+  if (nk > 0) {
+    dma(S0(), 0);
+    dma(S1(), 1);
+    dma_barrier_keep<kLoads>();
+    read_ops(S0(), 0, cur);
+    read_scales(S0(), sc);
+    for (int t = 0; t < nk; t += 2) {
+      slice(S0(), t);
+      if (t + 1 < nk) slice(S1(), t + 1);
+    }
+    // The last slices sent loads past K (no memory traffic): let them retire
+    // before the work-group gives up its LDS.
+    __builtin_amdgcn_s_waitcnt(0x0f70);
+  }
+
+  // Register e of lane l holds row acc32_row(l, e), column l % 32 of a block.
+  const bool full = m0 + BM <= m_end && n0 + BN <= p.N;
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      const int n = n0 + wn * WTN + j * 32 + r32;
+      const int mb = m0 + wm * WTM + i * 32;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int m = mb + acc32_row(lane, e);
+        if (!full && (m >= m_end || n >= p.N)) continue;
+        store_c<CBF16>(p, (a_row + m) * p.ldc + n, acc[i][j][e]);
+      }
+    }
+}
+
+template <int BM, int BN, int WM, int WN>
+hipError_t launch(const Mxfp4Args &p, bool c_bf16, hipStream_t s) {
+  const int tiles_m = (p.M + BM - 1) / BM, tiles_n = (p.N + BN - 1) / BN;
+  const long rows = p.offsets ? group_tile_rows(p.M, p.groups, BM) : tiles_m;
+  const dim3 grid((unsigned)(rows * tiles_n)), block(WM * WN * kWave);
+  const TileMap tmap = make_tile_map(tiles_m, tiles_n, 8);
+  if (c_bf16)
+    hipLaunchKernelGGL((mxfp4_tile_kernel<BM, BN, WM, WN, true>), grid, block, 0, s, p, tmap,
+                       tiles_n);
+  else
+    hipLaunchKernelGGL((mxfp4_tile_kernel<BM, BN, WM, WN, false>), grid, block, 0, s, p, tmap,
+                       tiles_n);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_mxfp4_tile(int tile, const Mxfp4Args &p, bool c_bf16, hipStream_t s) {
+  return tile == 256 ? launch<256, 256, 2, 4>(p, c_bf16, s) : launch<128, 128, 2, 2>(p, c_bf16, s);
+}
+
+}  // namespace sgemm
