@@ -126,11 +126,27 @@ __global__ void __launch_bounds__(KS *kWave) mxfp4_kernel(Mxfp4Args p, int tiles
     }
 }
 
+// The tile through LDS.  In units of a 256 x 256 tile's time, a compute unit
+// takes 0.56 for one tile of 128 x 128, 0.73 for two (they share it), and 0.29
+// a tile for more: measured on 256 compute units with bfloat16 C, 2048^3 24.0
+// us with 64 tiles of 256 x 256 and 13.5 with 256 of 128 x 128, 1024 x 8192 x
+// 8192 56.3 (128 tiles) and 40.8 (512), 4096^3 38.8 (256) and 42.9 (1024),
+// 8192^3 250 (1024) and 298 (4096).  Groups count with their mean length.
+int mxfp4_tile_size(const Mxfp4Args &p, int cus) {
+  const long groups = p.offsets ? p.groups : 1, mean = (p.M + groups - 1) / groups;
+  auto per_cu = [&](long t) {
+    const long tiles = groups * ((mean + t - 1) / t) * ((p.N + t - 1) / t);
+    return (double)((tiles + cus - 1) / cus);
+  };
+  const double n = per_cu(128);
+  return per_cu(256) <= (n == 1 ? 0.56 : n == 2 ? 0.73 : 0.29 * n) ? 256 : 128;
+}
+
 }  // namespace
 
 hipError_t launch_mxfp4_product(const Mxfp4Args &p, bool c_bf16, int cus, hipStream_t s) {
   const long mean = p.M / (p.offsets ? p.groups : 1);
-  if (mean > 64) return launch_mxfp4_tile(mean > 512 ? 256 : 128, p, c_bf16, s);
+  if (mean > 64) return launch_mxfp4_tile(mxfp4_tile_size(p, cus), p, c_bf16, s);
   const int tiles_n = (p.N + 31) / 32, tiles_m = (p.M + 15) / 16;
   const long rows = p.offsets ? group_tile_rows(p.M, p.groups, 16) : tiles_m;
   const dim3 grid((unsigned)(rows * tiles_n)), block(4 * kWave);

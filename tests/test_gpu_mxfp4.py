@@ -207,6 +207,34 @@ def test_product(M, N, K, kind, out):
     _check(*_product(M, N, K, kind, out), out)
 
 
+# Enough tiles of 128 x 128 for the 256 x 256 tile, ragged in all directions.
+@pytest.mark.parametrize("K", [1, 129, 260, 640])
+@pytest.mark.parametrize("kind,out,alpha,beta", [("f32", "f32", 1.0, 0.0), ("mxfp4", "bf16", 1.0, 0.0),
+                                                 ("bf16", "f32", -0.5, 2.0)])
+def test_product_of_many_tiles(K, kind, out, alpha, beta):
+    _check(*_product(4120, 3990, K, kind, out, alpha, beta, pads=(3, 2, 1)), out)
+
+
+def test_product_exact_on_many_tiles():
+    """Values of the format itself under one scale: every sum is exact."""
+    import torch
+    M, N, K = 3900, 4200, 384
+    g = np.random.default_rng(8)
+    pa, pb = (g.integers(0, 256, (r, K // 2)).astype(np.uint8) for r in (M, N))
+    sa, sb = (np.full((K // 128, r, 4), 127, np.uint8) for r in (M, N))
+    C = torch.empty(M, N, device="cuda")
+    sg.sgemm_run_mxfp4(M, N, K, 1.0, "mxfp4", _cuda(pa), M, _cuda(sa), _cuda(pb), _cuda(sb), N,
+                       0.0, "f32", C, N)
+    ref = mx.values(pa, sa, K) @ mx.values(pb, sb, K).T
+    assert np.array_equal(C.cpu().numpy(), ref)
+
+
+def test_grouped_of_many_tiles():
+    lengths = [1500, 0, 2700, 33, 1000]
+    for kind, out in (("bf16", "bf16"), ("mxfp4", "f32")):
+        _check(*_product(sum(lengths) + 10, 4000, 300, kind, out, lengths=lengths, before=4), out)
+
+
 @pytest.mark.parametrize("M,N,K", [(3, 70, 300), (90, 140, 400), (257, 300, 513)])
 @pytest.mark.parametrize("kind,out", [("f32", "f32"), ("bf16", "bf16"), ("mxfp4", "f32")])
 @pytest.mark.parametrize("alpha,beta", [(-1.5, 0.0), (0.5, 2.0), (1.0, -1.0), (0.0, 0.5),
