@@ -13,7 +13,8 @@ namespace {
 using sgemm_api::kMaxDim;
 using sgemm_api::kMaxWorkItems;
 
-constexpr int64_t kMaxLd = int64_t(1) << 22;
+constexpr int64_t kMaxLd = int64_t(1) << 22;   // offsets in a tile of 128 rows: below 2 GiB
+constexpr int64_t kMaxLdc = int64_t(1) << 27;  // offsets in 8 rows of C: below 4 GiB
 
 int64_t tiles(int64_t n, int64_t t) { return (n + t - 1) / t; }
 
@@ -23,7 +24,8 @@ int check(int64_t groups, int64_t M, int64_t N, int64_t K, int64_t a_cols, int64
   if (groups < 0 || M < 0 || N < 0 || K < 0) return SGEMM_ERR_INVALID_VALUE;
   if (lda < (a_cols > 1 ? a_cols : 1) || ldb < (b_cols > 1 ? b_cols : 1) || ldc < (N > 1 ? N : 1))
     return SGEMM_ERR_INVALID_VALUE;
-  if (M > kMaxDim || N > kMaxDim || K > kMaxDim || groups > SGEMM_GROUPED_MAX_GROUPS)
+  if (M > kMaxDim || N > kMaxDim || K > kMaxDim || ldc >= kMaxLdc ||
+      groups > SGEMM_GROUPED_MAX_GROUPS)
     return SGEMM_ERR_TOO_LARGE;
   return SGEMM_OK;
 }

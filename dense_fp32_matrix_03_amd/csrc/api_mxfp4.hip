@@ -15,6 +15,7 @@ using sgemm_api::kMaxDim;
 using sgemm_api::kMaxWorkItems;
 
 constexpr int64_t kMaxK = int64_t(1) << 21;
+constexpr int64_t kMaxLdc = int64_t(1) << 27;  // offsets in 8 rows of C: below 4 GiB
 
 int64_t tiles(int64_t n, int64_t t) { return (n + t - 1) / t; }
 int64_t kp(int64_t K) { return sgemm::mxfp4_kp(K); }
@@ -80,7 +81,7 @@ int run(int64_t groups, int64_t M, int64_t N, int64_t K, float alpha, int typeA,
   if (lda < (a_cols > 1 ? a_cols : 1) || ldc < (N > 1 ? N : 1)) return SGEMM_ERR_INVALID_VALUE;
   if ((__int128)b_groups * N > ldsb) return SGEMM_ERR_INVALID_VALUE;
   if (M > kMaxDim || N > kMaxDim || K > kMaxK || lda > kMaxDim || ldsb > kMaxDim ||
-      ldc > kMaxDim || b_groups > SGEMM_GROUPED_MAX_GROUPS)
+      ldc >= kMaxLdc || b_groups > SGEMM_GROUPED_MAX_GROUPS)
     return SGEMM_ERR_TOO_LARGE;
   const int64_t rows = grouped ? sgemm::group_tile_rows(M, groups, 16) : tiles(M, 16);
   if (rows > kMaxWorkItems / 256 / (N ? tiles(N, 16) : 1)) return SGEMM_ERR_TOO_LARGE;

@@ -1,16 +1,24 @@
-// grouped.hip -- single-precision products whose rows fall into groups of
-// unequal length (include/sgemm_grouped.h).
+// grouped.hip -- single-precision products of short groups of rows
+// (include/sgemm_grouped.h), and the choice between this kernel and the tiles
+// of grouped_tile.hip.
 //
 // C(r, :) = alpha sum_k A(r, k) op(B_g)(k, :) + beta C(r, :) for the rows r of
-// group g, and C_g = alpha sum_r A(r, :)^T B(r, :) + beta C_g.  Both sum
-// products of FP32 values on v_mfma_f32_16x16x4_f32.
+// group g, on v_mfma_f32_16x16x4_f32.  With a few rows a group the time is that
+// of reading the B_g once.  A work-group has 16 rows by 64 columns and splits k
+// over four waves, whose sums are added in order at the end, so that even one
+// short group spreads over the chip; its operands go straight from global
+// memory into registers.
 //
-// Operands go straight from global memory into registers.  K is walked in
-// groups of 16; in one, lane quarter h supplies k = 4 h + t to instruction t,
-// so an operand whose k runs along its stored rows takes its four
-// instructions' values in one 16-byte load.  An operand stored the other way
-// takes four 16-byte loads, one of each k row, and its 64 rows (or columns)
-// are dealt to the four blocks in turn: block j has 4 c + j of lane c.
+// K is walked in groups of 16; in one, lane quarter h supplies k = 4 h + t to
+// instruction t, so an operand whose k runs along its stored rows takes its
+// four instructions' values in one 16-byte load.  B as given takes four 16-byte
+// loads, one of each k row, and its 64 columns are dealt to the four blocks
+// in turn: block j has column 4 c + j of lane c.
+//
+// 24 rows in 16 groups by 2048 x 2048: 31.5 us, 6.4 TB/s of the weights that
+// have rows (part of them stays in the Infinity Cache between calls).
+#include <type_traits>
+
 #include "common.hpp"
 #include "grouped.hpp"
 #include "grouped_map.hpp"
@@ -35,172 +43,110 @@ __device__ __forceinline__ f32x4 load_some(const float *p, int n) {
   return v;
 }
 
-// Where the operands' k runs.
-enum Layout { kNN, kNT, kTN };  // B as given; B transposed; A transposed (grouped_k)
+constexpr int kRows = 16, kCols = 64, kSets = 4;
 
-// MT: blocks of 16 rows per wave; a wave has 64 columns.  WM x WN waves share
-// a tile, each with KS waves that split k between them (16 k in turn).
-template <int LAYOUT, int MT, int WM, int WN, int KS>
-__global__ void __launch_bounds__(WM *WN *KS *kWave) grouped_kernel(GroupedArgs p, int tiles_m,
-                                                                   int tiles_n) {
-  constexpr bool TA = LAYOUT == kTN, TB = LAYOUT == kNT;
-  static_assert(!TA || MT == 4, "a transposed A gives blocks of 64 rows");
-  constexpr int BM = WM * MT * 16, BN = WN * 64;
+template <bool TB>
+__global__ void __launch_bounds__(kSets *kWave) grouped_kernel(GroupedArgs p, int tiles_n) {
   const int lane = threadIdx.x % kWave;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int kq = wave % KS, wm = wave / KS % WM, wn = wave / (KS * WM);
+  const int kq = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int c = lane % 16, h = lane / 16;
 
-  const float *A = p.A, *B = p.B;
-  float *C = p.C;
-  int m0, n0, m_end, K;  // the wave's tile inside the group's rows, and its k
-  if constexpr (TA) {
-    const int per = tiles_m * tiles_n;
-    const int g = blockIdx.x / per, t = blockIdx.x % per;
-    long first, last;
-    group_range(p.offsets, g, p.K, first, last);
-    A += first * p.lda;
-    B += first * p.ldb;
-    C += (long)g * p.strideC;
-    K = (int)(last - first);
-    m0 = t / tiles_n * BM;
-    n0 = t % tiles_n * BN;
-    m_end = p.M;
-  } else {
-    const GroupTile t = group_tile(p.offsets, p.groups, p.M, BM, tiles_n, 8);
-    if (!t.valid) return;
-    A += t.row0 * p.lda;
-    B += (long)t.g * p.strideB;
-    C += t.row0 * p.ldc;
-    K = p.K;
-    m0 = t.tm * BM;
-    n0 = t.tn * BN;
-    m_end = t.rows;
-  }
-  m0 += wm * MT * 16;
-  n0 += wn * 64;
+  const GroupTile t = group_tile(p.offsets, p.groups, p.M, kRows, tiles_n, 8);
+  if (!t.valid) return;
+  const float *A = p.A + t.row0 * p.lda, *B = p.B + (long)t.g * p.strideB;
+  float *C = p.C + t.row0 * p.ldc;
+  const int K = p.alpha != 0.f ? p.K : 0;
+  const int m0 = t.tm * kRows, n0 = t.tn * kCols, m_end = t.rows;
 
   struct Ops {
-    f32x4 a[4], b[4];
+    f32x4 a, b[4];
   };
   // Rows past the end repeat the last one: what they give is not stored.
+  const float *const a_row = A + (long)min(m0 + c, m_end - 1) * p.lda;
   auto load = [&](int k, Ops &o, auto whole) {
     constexpr bool WHOLE = decltype(whole)::value;
-    if constexpr (TA) {
+    o.a = load_some(a_row + k + 4 * h, WHOLE ? 4 : K - k - 4 * h);
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const int kk = k + 4 * h + t, m = m0 + 4 * c;
-        const float *at = A + (long)kk * p.lda + m;
-        o.a[t] = load_some(at, WHOLE ? 4 : (kk < K ? m_end - m : 0));
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        const int m = min(m0 + 16 * i + c, m_end - 1), kk = k + 4 * h;
-        o.a[i] = load_some(A + (long)m * p.lda + kk, WHOLE ? 4 : K - kk);
-      }
-    }
-    if constexpr (TB) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (TB) {
         const int n = min(n0 + 16 * j + c, p.N - 1), kk = k + 4 * h;
         o.b[j] = load_some(B + (long)n * p.ldb + kk, WHOLE ? 4 : K - kk);
-      }
-    } else {
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const int kk = k + 4 * h + t, n = n0 + 4 * c;
-        o.b[t] = load_some(B + (long)kk * p.ldb + n, WHOLE ? 4 : (kk < K ? p.N - n : 0));
+      } else {
+        const int kk = k + 4 * h + j, n = n0 + 4 * c;
+        o.b[j] = load_some(B + (long)kk * p.ldb + n, WHOLE ? 4 : (kk < K ? p.N - n : 0));
       }
     }
   };
-  f32x4 acc[MT][4];
+  f32x4 acc[4];
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  auto mma = [&](const Ops &o) {
+  for (int j = 0; j < 4; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const bool inside = TB || n0 + kCols <= p.N;
+  for (int k = 16 * kq; k < K; k += 16 * kSets) {
+    Ops o;
+    if (inside && k + 16 <= K)
+      load(k, o, std::true_type());
+    else
+      load(k, o, std::false_type());
 #pragma unroll
     for (int t = 0; t < 4; ++t)
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          acc[i][j] = mfma16x16x4(TA ? o.a[t][i] : o.a[i][t], TB ? o.b[j][t] : o.b[t][j],
-                                  acc[i][j]);
-  };
-
-  if (p.alpha != 0.f && m0 < m_end && n0 < p.N) {
-    const bool inside = (!TA || m0 + 64 <= m_end) && (TB || n0 + 64 <= p.N);
-    for (int k = 16 * kq; k < K; k += 16 * KS) {
-      Ops o;
-      if (inside && k + 16 <= K)
-        load(k, o, std::true_type());
-      else
-        load(k, o, std::false_type());
-      mma(o);
-    }
+      for (int j = 0; j < 4; ++j)
+        acc[j] = mfma16x16x4(o.a[t], TB ? o.b[j][t] : o.b[t][j], acc[j]);
   }
 
-  if constexpr (KS > 1) {
-    __shared__ f32x4 red[WM * WN * (KS - 1) * MT * 4 * kWave];
-    f32x4 *mine = red + (wm + wn * WM) * (KS - 1) * MT * 4 * kWave + lane;
-    if (kq > 0) {
+  __shared__ f32x4 red[(kSets - 1) * 4 * kWave];
+  if (kq > 0) {
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) mine[((kq - 1) * MT * 4 + i * 4 + j) * kWave] = acc[i][j];
-    }
-    __syncthreads();
-    if (kq > 0) return;
-#pragma unroll
-    for (int s = 0; s < KS - 1; ++s)
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] += mine[(s * MT * 4 + i * 4 + j) * kWave];
+    for (int j = 0; j < 4; ++j) red[((kq - 1) * 4 + j) * kWave + lane] = acc[j];
   }
+  __syncthreads();
+  if (kq > 0) return;
+#pragma unroll
+  for (int s = 0; s < kSets - 1; ++s)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[j] += red[(s * 4 + j) * kWave + lane];
 
   // Register e of lane l holds row 4 (l / 16) + e, column l % 16 of a block.
-  const bool plain = p.alpha == 1.f && p.beta == 0.f;
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
+  for (int e = 0; e < 4; ++e) {
+    const int m = m0 + 4 * h + e;
+    if (m >= m_end) continue;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int r = 4 * h + e;
-      const int m = TA ? m0 + 4 * r + i : m0 + 16 * i + r;
-      if (m >= m_end) continue;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int n = TB ? n0 + 16 * j + c : n0 + 4 * c + j;
-        if (n >= p.N) continue;
-        float *at = C + (long)m * p.ldc + n;
-        if (plain)
-          *at = acc[i][j][e];
-        else if (p.beta == 0.f)
-          *at = p.alpha * acc[i][j][e];
-        else
-          *at = fmaf(p.alpha, acc[i][j][e], p.beta * *at);
-      }
+    for (int j = 0; j < 4; ++j) {
+      const int n = TB ? n0 + 16 * j + c : n0 + 4 * c + j;
+      if (n >= p.N) continue;
+      float *at = C + (long)m * p.ldc + n;
+      *at = p.beta == 0.f ? p.alpha * acc[j][e] : fmaf(p.alpha, acc[j][e], p.beta * *at);
     }
+  }
 }
 
 }  // namespace
 
+// This kernel or a tile of 32 x 128 through LDS, whichever the rounds of
+// work-groups on the compute units make faster.  A round of the tile takes as
+// long as 2.4 rounds of this kernel, 1.6 where B is transposed or its loads are
+// narrow.  Measured, this kernel first: 1 group of 64 rows by 4096 x 4096 42 us
+// and 75; 16 groups, 24 rows by 2048 x 2048 31.5 and 42.5, 512 rows 61 and 67,
+// 1024 rows 108 and 102; 64 groups, 2048 rows by 1024 x 1024 63 and 45; B
+// transposed 16 groups, 384 rows by 2048 x 2048 96 and 79.  The host knows the
+// number of tiles to within the groups' lengths.
 hipError_t launch_grouped_rows(const GroupedArgs &p, bool tb, int cus, hipStream_t s) {
-  const int tiles_n = (p.N + 63) / 64;
-  const dim3 grid((unsigned)(group_tile_rows(p.M, p.groups, 16) * tiles_n)), block(4 * kWave);
+  const long groups = p.groups < p.M ? p.groups : p.M;
+  auto rounds = [&](long bm, long bn) {
+    const long most = p.M / bm + groups / 2;
+    return ((most > groups ? most : groups) * ((p.N + bn - 1) / bn) + cus - 1) / cus;
+  };
+  const double per_round = tb || p.N % 4 != 0 ? 0.625 : 0.42;
+  if (rounds(kRows, kCols) * per_round > rounds(32, 128))
+    return launch_grouped_tile(p, tb, cus, s);
+  const int tiles_n = (p.N + kCols - 1) / kCols;
+  const dim3 grid((unsigned)(group_tile_rows(p.M, p.groups, kRows) * tiles_n)),
+      block(kSets * kWave);
   if (tb)
-    hipLaunchKernelGGL((grouped_kernel<kNT, 1, 1, 1, 4>), grid, block, 0, s, p, 0, tiles_n);
+    hipLaunchKernelGGL(grouped_kernel<true>, grid, block, 0, s, p, tiles_n);
   else
-    hipLaunchKernelGGL((grouped_kernel<kNN, 1, 1, 1, 4>), grid, block, 0, s, p, 0, tiles_n);
-  return hipGetLastError();
-}
-
-hipError_t launch_grouped_k(const GroupedArgs &p, int cus, hipStream_t s) {
-  const int tiles_m = (p.M + 127) / 128, tiles_n = (p.N + 127) / 128;
-  const dim3 grid((unsigned)((long)tiles_m * tiles_n * p.groups)), block(4 * kWave);
-  hipLaunchKernelGGL((grouped_kernel<kTN, 4, 2, 2, 1>), grid, block, 0, s, p, tiles_m, tiles_n);
+    hipLaunchKernelGGL(grouped_kernel<false>, grid, block, 0, s, p, tiles_n);
   return hipGetLastError();
 }
 

@@ -100,6 +100,23 @@ __device__ __forceinline__ GroupTile group_tile(const int64_t *offsets, int grou
   return t;
 }
 
+// The group with `rank` longer ones before it (equal ones in their order),
+// among up to 64 groups; with more groups, group `rank`.
+__device__ __forceinline__ int group_by_length(const int64_t *offsets, int groups, long M,
+                                               int rank) {
+  if (groups > kWave) return rank;
+  const int lane = threadIdx.x % kWave;
+  long first = 0, last = -1;
+  if (lane < groups) group_range(offsets, lane, M, first, last);
+  const int mine = (int)(last - first);  // -1 past the last group
+  int before = 0;
+  for (int g = 0; g < groups; ++g) {
+    const int other = __builtin_amdgcn_readlane(mine, g);
+    before += other > mine || (other == mine && g < lane);
+  }
+  return __builtin_ctzll(__ballot(before == rank && lane < groups));
+}
+
 // Tile rows that a launch must provide for M rows in `groups` groups.
 inline long group_tile_rows(long M, long groups, long bm) {
   return M / bm + (groups < M ? groups : M);

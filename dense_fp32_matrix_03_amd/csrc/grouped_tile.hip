@@ -1,0 +1,342 @@
+// grouped_tile.hip -- single-precision products of grouped rows
+// (include/sgemm_grouped.h) whose operand slices reach LDS by buffer-to-LDS
+// loads: the pipeline, LDS images and k order of mfma_dma.hpp, with a tile's
+// operands and limits found from the group lengths on the device.
+//
+// C(r, :) = alpha sum_k A(r, k) op(B_g)(k, :) + beta C(r, :), or C_g = alpha
+// sum_r A(r, :)^T B(r, :) + beta C_g, on v_mfma_f32_32x32x2_f32.
+//
+// Edges.  An element outside op(A)'s rows or op(B)'s columns is fetched at an
+// offset past the descriptor's end and reads as zero.  A partial last slice
+// of k goes first, so that the main loop's loads need no test of k: an operand
+// whose k runs along its stored rows ends at the last valid row, the other
+// one compares each load's k (with 4-byte loads where K % 4 != 0, since a
+// 16-byte one would hold values past K).
+#include "grouped.hpp"
+#include "grouped_map.hpp"
+#include "mfma_dma.hpp"
+
+namespace sgemm {
+
+namespace {
+
+// KFORM: groups divide k (grouped_k; A^T and B as given); otherwise they
+// divide the rows of A and C, and TB tells whether the B_g are stored
+// transposed.  VA / VB: A / B take 16-byte loads.
+template <bool KFORM, bool TB, int BM, int BN, int BK, int WM, int WN, int NST, bool VA, bool VB>
+__global__ void __launch_bounds__(WM *WN *kWave, 2)
+grouped_tile_kernel(GroupedArgs p, int tiles_m, int tiles_n) {
+  constexpr bool TA = KFORM;
+  constexpr int NW = WM * WN;
+  constexpr int WTM = BM / WM, WTN = BN / WN, FM = WTM / 32, FN = WTN / 32;
+  constexpr int KH = BK / 2, G = KH / 4;
+  using GA = SliceGeom<BM, BK, TA, VA, true, NW>;
+  using GB = SliceGeom<BN, BK, !TB, VB, true, NW>;
+  static_assert(!GA::SPARE && !GB::SPARE, "loads must split evenly over the waves");
+  constexpr int kLoads = GA::NBW + GB::NBW;
+
+  static_assert(NST >= 2 && NST <= 4, "2 to 4 LDS stages");
+  constexpr int SA = BM * BK, SB = BK * BN;
+  __shared__ __attribute__((aligned(1024))) float As0[SA], As1[SA], As2[NST > 2 ? SA : 1],
+      As3[NST > 3 ? SA : 1];
+  __shared__ __attribute__((aligned(1024))) float Bs0[SB], Bs1[SB], Bs2[NST > 2 ? SB : 1],
+      Bs3[NST > 3 ? SB : 1];
+  auto stage_a = [&](auto S) -> float * {
+    constexpr int i = decltype(S)::value;
+    return i == 0 ? As0 : i == 1 ? As1 : i == 2 ? As2 : As3;
+  };
+  auto stage_b = [&](auto S) -> float * {
+    constexpr int i = decltype(S)::value;
+    return i == 0 ? Bs0 : i == 1 ? Bs1 : i == 2 ? Bs2 : Bs3;
+  };
+
+  const int lane = threadIdx.x % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int wm = wave / WN, wn = wave % WN;
+  const int r32 = lane % 32, half = lane / 32;
+
+  const float *A = p.A, *B = p.B;
+  float *C = p.C;
+  int m0, n0, m_end, K;
+  if constexpr (KFORM) {
+    const int per = tiles_m * tiles_n;
+    // Each group's tiles are spread over the XCDs (a group of tiles per XCD
+    // would leave the chip waiting for the XCD of the longest one), the longest
+    // groups first.
+    const int rank = blockIdx.x / per;
+    const int t = xcd_contiguous_id(blockIdx.x % per, per);
+    const int g = group_by_length(p.offsets, p.groups, p.K, rank);
+    long first, last;
+    group_range(p.offsets, g, p.K, first, last);
+    A += first * p.lda;
+    B += first * p.ldb;
+    C += (long)g * p.strideC;
+    K = (int)(last - first);
+    m0 = t / tiles_n * BM;
+    n0 = t % tiles_n * BN;
+    m_end = p.M;
+  } else {
+    const GroupTile t = group_tile(p.offsets, p.groups, p.M, BM, tiles_n, 8);
+    if (!t.valid) return;
+    A += t.row0 * p.lda;
+    B += (long)t.g * p.strideB;
+    C += t.row0 * p.ldc;
+    K = p.K;
+    m0 = t.tm * BM;
+    n0 = t.tn * BN;
+    m_end = t.rows;
+  }
+  if (p.alpha == 0.f) K = 0;
+
+  unsigned offA[GA::NBW], offB[GB::NBW];
+#pragma unroll
+  for (int q = 0; q < GA::NBW; ++q) {
+    int row, col;
+    GA::elem(wave, lane, q, row, col);
+    offA[q] = m0 + GA::mnof(row, col) < m_end ? (unsigned)(row * p.lda + col) * 4u : kOutOfRange;
+  }
+#pragma unroll
+  for (int q = 0; q < GB::NBW; ++q) {
+    int row, col;
+    GB::elem(wave, lane, q, row, col);
+    offB[q] = n0 + GB::mnof(row, col) < p.N ? (unsigned)(row * p.ldb + col) * 4u : kOutOfRange;
+  }
+  auto rsrc = [](const float *base, int records) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<float *>(base), 0, records,
+                                             kRawBufferWord3);
+  };
+  auto origin_a = [&](int k0) { return TA ? A + (long)k0 * p.lda + m0 : A + (long)m0 * p.lda + k0; };
+  auto origin_b = [&](int k0) { return TB ? B + (long)n0 * p.ldb + k0 : B + (long)k0 * p.ldb + n0; };
+
+  // Position u of the slice order: with a ragged K the partial slice first,
+  // then slice u - 1.  Positions at or past nk get descriptors without
+  // records: nothing is fetched.
+  const int nk = (K + BK - 1) / BK, ragged = K % BK != 0;
+  auto dma = [&](auto S, int u) {
+    const int records = u < nk ? kBufferRecords : 0;
+    const int k0 = u < nk ? (u - ragged) * BK : 0;
+    const __amdgpu_buffer_rsrc_t ra = rsrc(origin_a(k0), records);
+    const __amdgpu_buffer_rsrc_t rb = rsrc(origin_b(k0), records);
+#pragma unroll
+    for (int q = 0; q < GA::NBW; ++q)
+      lds_dma<VA>(ra, stage_a(S) + (wave + q * NW) * GA::FPB, offA[q]);
+#pragma unroll
+    for (int q = 0; q < GB::NBW; ++q)
+      lds_dma<VB>(rb, stage_b(S) + (wave + q * NW) * GB::FPB, offB[q]);
+  };
+  // The partial slice, kl values of k, into stage 0.
+  auto dma_tail = [&](auto geom, float *stage, const float *origin, long ld, int mn_left, int kl) {
+    using Gm = decltype(geom);
+    const __amdgpu_buffer_rsrc_t r = rsrc(origin, Gm::KR ? kl * (int)ld * 4 : kBufferRecords);
+#pragma unroll
+    for (int q = 0; q < Gm::NBW; ++q) {
+      int row, col;
+      Gm::elem(wave, lane, q, row, col);
+      const bool in = Gm::mnof(row, col) < mn_left && (Gm::KR || Gm::kof(row, col) < kl);
+      lds_dma<Gm::E == 4>(r, stage + (wave + q * NW) * Gm::FPB,
+                          in ? (unsigned)(row * ld + col) * 4u : kOutOfRange);
+    }
+  };
+
+  const int sw = kc_swizzle<BK, true>(r32);
+  int a_off[G], b_off[G];
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    a_off[g] = TA ? (half * KH + g * 4) * BM + wm * WTM + r32
+                  : (wm * WTM + r32) * BK + 4 * ((half * (KH / 4) + g) ^ sw);
+    b_off[g] = TB ? (wn * WTN + r32) * BK + 4 * ((half * (KH / 4) + g) ^ sw)
+                  : (half * KH + g * 4) * BN + wn * WTN + r32;
+  }
+  struct Ops {
+    f32x4 a[FM], b[FN];
+  };
+  auto read_ops = [&](auto S, int g, Ops &o) {
+    const float *as = stage_a(S), *bs = stage_b(S);
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      if constexpr (TA) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) o.a[i][t] = as[a_off[g] + t * BM + i * 32];
+      } else {
+        o.a[i] = *reinterpret_cast<const f32x4 *>(as + a_off[g] + i * 32 * BK);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      if constexpr (TB) {
+        o.b[j] = *reinterpret_cast<const f32x4 *>(bs + b_off[g] + j * 32 * BK);
+      } else {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) o.b[j][t] = bs[b_off[g] + t * BN + j * 32];
+      }
+    }
+  };
+  f32x16 acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+  auto mma = [&](const Ops &o) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) acc[i][j] = mfma32x32x2(o.a[i][t], o.b[j][t], acc[i][j]);
+  };
+
+  // As in mfma_dma.hpp: one matrix-core instruction per load in the last group
+  // of a slice, then two per operand read.
+  constexpr int kMfma = 4 * FM * FN;
+  constexpr int kReads = (TA ? 2 * FM : FM) + (TB ? FN : 2 * FN);
+  auto interleave = [&](auto last) {
+    constexpr int loads = decltype(last)::value ? kLoads : 0;
+    static_for<kMfma>([&](auto I) {
+      constexpr int i = decltype(I)::value;
+      constexpr int d = kReads * (i + 1) / kMfma - kReads * i / kMfma;
+      constexpr int v = loads * (i + 1) / kMfma - loads * i / kMfma;
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      if constexpr (d > 0) __builtin_amdgcn_sched_group_barrier(0x100, d, 0);
+      if constexpr (v > 0) __builtin_amdgcn_sched_group_barrier(0x020, v, 0);
+    });
+  };
+  using S0 = std::integral_constant<int, 0>;
+  Ops cur, nxt;
+  auto slice = [&](auto S, int u) {
+    using SN = std::integral_constant<int, (decltype(S)::value + 1) % NST>;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      if (g + 1 < G) {
+        read_ops(S, g + 1, nxt);
+        mma(cur);
+        interleave(std::false_type());
+      } else {
+        dma_barrier_keep<(NST - 2) * kLoads>();
+        dma(S, u + NST);
+        read_ops(SN(), 0, nxt);
+        mma(cur);
+        interleave(std::true_type());
+      }
+      cur = nxt;
+    }
+  };
+
+  if (nk > 0) {
+    if (ragged) {
+      const int k0 = (nk - 1) * BK, kl = K - k0;
+      using GAn = SliceGeom<BM, BK, TA, false, true, NW>;
+      using GBn = SliceGeom<BN, BK, !TB, false, true, NW>;
+      if (!TA && K % 4 != 0)
+        dma_tail(GAn(), As0, origin_a(k0), p.lda, m_end - m0, kl);
+      else
+        dma_tail(GA(), As0, origin_a(k0), p.lda, m_end - m0, kl);
+      if (TB && K % 4 != 0)
+        dma_tail(GBn(), Bs0, origin_b(k0), p.ldb, p.N - n0, kl);
+      else
+        dma_tail(GB(), Bs0, origin_b(k0), p.ldb, p.N - n0, kl);
+    } else {
+      dma(S0(), 0);
+    }
+    static_for<NST - 1>([&](auto I) {
+      using S = std::integral_constant<int, decltype(I)::value + 1>;
+      dma(S(), decltype(I)::value + 1);
+    });
+    dma_barrier_keep<(NST - 1) * kLoads>();
+    read_ops(S0(), 0, cur);
+    for (int u = 0; u < nk; u += NST) {
+      static_for<NST>([&](auto S) {
+        if (decltype(S)::value == 0 || u + decltype(S)::value < nk) slice(S, u + decltype(S)::value);
+      });
+    }
+    // The last slices sent loads past K (no memory traffic): let them retire
+    // before the work-group gives up its LDS.
+    __builtin_amdgcn_s_waitcnt(0x0f70);
+  }
+
+  // Register e of lane l holds row acc32_row(l, e), column l % 32 of a block:
+  // row 4 (l / 32) of a uniform base and a constant number of rows past it.
+  const bool full = m0 + BM <= m_end && n0 + BN <= p.N;
+  const int mw = m0 + wm * WTM, nw = n0 + wn * WTN;
+  float *const origin = C + (long)mw * p.ldc + nw;
+  const unsigned lane_at = (unsigned)(4 * half * p.ldc + r32) * 4u;
+  const int rows = m_end - mw - 4 * half, cols = p.N - nw - r32;
+  auto store = [&](auto whole, auto with_c) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int r = i * 32 + 8 * (e >> 2) + (e & 3);
+        float *const row = origin + r * p.ldc;
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+          if (!decltype(whole)::value && (r >= rows || j * 32 >= cols)) continue;
+          float *const at =
+              reinterpret_cast<float *>(reinterpret_cast<char *>(row + j * 32) + lane_at);
+          const float v = acc[i][j][e];
+          if constexpr (decltype(with_c)::value)
+            *at = fmaf(p.alpha, v, p.beta * *at);
+          else
+            __builtin_nontemporal_store(p.alpha * v, at);
+        }
+      }
+  };
+  if (p.beta != 0.f)
+    store(std::false_type(), std::true_type());
+  else if (full)
+    store(std::true_type(), std::false_type());
+  else
+    store(std::false_type(), std::false_type());
+}
+
+template <bool KFORM, bool TB, int BM, int BN, int BK, int WM, int WN, int NST, bool VA, bool VB>
+hipError_t launch(const GroupedArgs &p, hipStream_t s) {
+  const int tiles_m = (p.M + BM - 1) / BM, tiles_n = (p.N + BN - 1) / BN;
+  const long rows = KFORM ? (long)tiles_m * p.groups : group_tile_rows(p.M, p.groups, BM);
+  hipLaunchKernelGGL((grouped_tile_kernel<KFORM, TB, BM, BN, BK, WM, WN, NST, VA, VB>),
+                     dim3((unsigned)(rows * tiles_n)), dim3(WM * WN * kWave), 0, s, p, tiles_m,
+                     tiles_n);
+  return hipGetLastError();
+}
+
+// B as given is read along n: 16-byte loads need N to be a multiple of 4.
+template <int BM, int BN, int WM, int WN>
+hipError_t launch_rows(const GroupedArgs &p, bool tb, hipStream_t s) {
+  if (tb) return launch<false, true, BM, BN, 32, WM, WN, 2, true, true>(p, s);
+  if (p.N % 4 == 0) return launch<false, false, BM, BN, 32, WM, WN, 2, true, true>(p, s);
+  return launch<false, false, BM, BN, 32, WM, WN, 2, true, false>(p, s);
+}
+
+}  // namespace
+
+// Tiles of 32 x 128 for short groups, 64 x 64 from a mean length of 192 rows
+// on, 64 x 128 where a compute unit gets at least 16 of those.  Measured (B as
+// given, groups of unequal length): 64 groups of 64 rows by 1000 x 777 76 us
+// against 90 (64 x 64) and 98 (64 x 128); 128 of 128 by 1024 x 512 168-177,
+// 180, 180; 8 of 256 by 2048 x 1024 74, 69, 67; 8 of 1024 by 2048 x 1024 267,
+// 255, 265; 4 of 4096 by 2048 x 1024 501, 488, 471.
+hipError_t launch_grouped_tile(const GroupedArgs &p, bool tb, int cus, hipStream_t s) {
+  const long mean = p.M / p.groups;
+  if (mean < 192) return launch_rows<32, 128, 1, 4>(p, tb, s);
+  const double large = ((double)p.M / 64 + 0.5 * p.groups) * ((p.N + 127) / 128);
+  if (large >= 16.0 * cus) return launch_rows<64, 128, 2, 2>(p, tb, s);
+  return launch_rows<64, 64, 2, 2>(p, tb, s);
+}
+
+// Tiles of 128 x 128 where they give every compute unit at least two and pad C
+// by at most 1/16 more than 64 x 128 does; else 64 x 128.  Measured: 8 groups
+// of 512 rows by 2048 x 2048 246 us against 253 (64 x 128), 64 of 64 by 512 x
+// 1024 69 against 73; 32 of 47 by 257 x 1000 26.7 against 25.0.
+hipError_t launch_grouped_k(const GroupedArgs &p, int cus, hipStream_t s) {
+  const bool va = p.M % 4 == 0, vb = p.N % 4 == 0;
+  const long m128 = (p.M + 127) / 128, m64 = (p.M + 63) / 64, n128 = (p.N + 127) / 128;
+  if (va && vb && m128 * n128 * p.groups >= 2L * cus && 16 * 2 * m128 <= 17 * m64)
+    return launch<true, false, 128, 128, 32, 4, 2, 2, true, true>(p, s);
+  if (va && vb) return launch<true, false, 64, 128, 32, 2, 2, 2, true, true>(p, s);
+  if (va) return launch<true, false, 64, 128, 32, 2, 2, 2, true, false>(p, s);
+  if (vb) return launch<true, false, 64, 128, 32, 2, 2, 2, false, true>(p, s);
+  return launch<true, false, 64, 128, 32, 2, 2, 2, false, false>(p, s);
+}
+
+}  // namespace sgemm

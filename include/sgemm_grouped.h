@@ -32,7 +32,8 @@
  * below 2^31, groups <= SGEMM_GROUPED_MAX_GROUPS, one launch below 2^32
  * work-items at 256 for each 16 x 64 block (sgemm_run_grouped, counting
  * one partly filled row of blocks for each group) or 32 x 32 block
- * (sgemm_run_grouped_k) of C, and a leading dimension below 2^22.
+ * (sgemm_run_grouped_k) of C, lda and ldb below 2^22 where A and B are read,
+ * and ldc below 2^27.
  */
 #ifndef SGEMM_GROUPED_H_
 #define SGEMM_GROUPED_H_

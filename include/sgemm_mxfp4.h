@@ -32,7 +32,8 @@
  * on the other).
  *
  * Limits (SGEMM_ERR_TOO_LARGE): sizes below 2^31, K <= 2^21, and for each
- * launch fewer than 2^32 work-items.  Leading dimensions below 2^31.
+ * launch fewer than 2^32 work-items.  Leading dimensions below 2^31, ldc of the
+ * products below 2^27.
  * Everything else -- ownership, streams, asynchrony, no allocation, status
  * codes, checks of arguments before the runtime -- is as in sgemm.h.
  */
@@ -68,9 +69,9 @@ int sgemm_mxfp4_quantize(int trans, int64_t rows, int64_t K, int type, const voi
                          void *codes, void *scales, int64_t lds, void *stream);
 
 /*
- * The values a held matrix stands for, in single precision (exact, but for
- * magnitudes below 2^-149) or rounded to bfloat16 (exact, but for magnitudes
- * below 2^-133), laid out as X above.
+ * The values a held matrix stands for, laid out as X above.  Both types hold
+ * them exactly, but for those of 2^128 and more (s >= 253), which become
+ * infinite.
  */
 int sgemm_mxfp4_dequantize(int trans, int64_t rows, int64_t K, const void *codes,
                            const void *scales, int64_t lds, int type, void *X, int64_t ldx,

@@ -36,7 +36,7 @@ def _grouped(**over):
     (dict(A=None, B=None, C=None, offsets=None, M=0), READY),
     (dict(groups=4096), READY), (dict(groups=4097), LARGE),
     (dict(M=2 ** 31), LARGE), (dict(lda=2 ** 22), LARGE), (dict(ldb=2 ** 22), LARGE),
-    (dict(lda=2 ** 22, K=0), READY),
+    (dict(lda=2 ** 22, K=0), READY), (dict(ldc=2 ** 27), LARGE), (dict(ldc=2 ** 27 - 1), READY),
     # one 256-thread work-group per 16 x 64 block, and one more for each group
     (dict(M=2 ** 27, N=64, ldb=64, ldc=64), READY),
     (dict(M=2 ** 28, N=64, ldb=64, ldc=64), LARGE),
@@ -59,6 +59,7 @@ def _grouped_k(**over):
     (dict(C=None), INVALID), (dict(offsets=None), INVALID), (dict(A=None), INVALID),
     (dict(A=None, B=None, K=0), READY), (dict(A=None, B=None, alpha=0.0), READY),
     (dict(offsets=20), INVALID), (dict(groups=4097), LARGE), (dict(lda=2 ** 22), LARGE),
+    (dict(ldc=2 ** 27, strideC=2 ** 30), LARGE),
     (dict(groups=1024, M=4096, N=4096, lda=4096, ldb=4096, ldc=4096, strideC=2 ** 24), LARGE),
     (dict(groups=512, M=4096, N=4096, lda=4096, ldb=4096, ldc=4096, strideC=2 ** 24), READY),
 ])
@@ -128,7 +129,7 @@ WORKSPACE = dict(workspace=256, workspace_bytes=8 * 68)
     (dict(K=0, A=None, B=None, scalesB=None, workspace=None), READY),
     (dict(M=0, A=None, B=None, scalesB=None, C=None, workspace=None), READY),
     (dict(K=2 ** 21 + 1, lda=2 ** 22), LARGE), (dict(M=2 ** 31), LARGE),
-    (dict(ldsb=2 ** 31), LARGE),
+    (dict(ldsb=2 ** 31), LARGE), (dict(ldc=2 ** 27), LARGE),
 ])
 def test_mxfp4_product_checks(over, status):
     lib = sg.load_library()

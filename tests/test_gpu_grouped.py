@@ -59,10 +59,26 @@ GROUPS = {
 }
 
 
+def _lengths(groups, mean, seed):
+    """Unequal lengths, some of them zero, around `mean`."""
+    g = np.random.default_rng(seed)
+    n = (g.exponential(mean, groups) * (g.random(groups) > 0.1)).astype(int)
+    return [int(v) for v in n]
+
+
+# Enough rows and groups for each of the tiles through LDS.
+LARGE = {
+    "short groups": (_lengths(45, 30, 1), 3, 2),
+    "long groups": (_lengths(8, 330, 2), 1, 5),
+    "very long groups": (_lengths(5, 3600, 3), 0, 7),
+}
+GROUPS_AND_LARGE = {**GROUPS, **LARGE}
+
+
 def _run_rows(groups, N, K, tb, alpha=1.0, beta=0.0, pads=(0, 0, 0), shift=0, dist="uniform",
               share=False, seed=0):
     import torch
-    lengths, before, after = GROUPS[groups]
+    lengths, before, after = GROUPS_AND_LARGE[groups]
     G = len(lengths)
     at, d_at = _offsets(lengths, before)
     M = int(at[-1]) + after
@@ -135,9 +151,28 @@ def test_rows_exact_on_integers(groups, tb):
     assert np.array_equal(C, ref)
 
 
+@pytest.mark.parametrize("tb", [0, 1])
+@pytest.mark.parametrize("groups,N", [("short groups", 1000), ("short groups", 1001),
+                                      ("long groups", 1032), ("long groups", 1029),
+                                      ("very long groups", 2052), ("very long groups", 2049)])
+@pytest.mark.parametrize("K,alpha,beta,pads,shift", [
+    (64, 1.0, 0.0, (0, 0, 0), 0), (101, -0.5, 0.0, (0, 0, 0), 0), (3, 1.0, 0.0, (1, 3, 2), 1),
+    (130, 0.5, 2.0, (5, 1, 3), 3), (36, 1.0, 0.0, (0, 4, 0), 2)])
+def test_rows_of_many_tiles(groups, N, tb, K, alpha, beta, pads, shift):
+    _check(*_run_rows(groups, N, K, tb, alpha, beta, pads, shift))
+
+
+@pytest.mark.parametrize("tb", [0, 1])
+@pytest.mark.parametrize("groups,N", [("short groups", 1000), ("long groups", 1029),
+                                      ("very long groups", 2052)])
+def test_rows_of_many_tiles_exact_on_integers(groups, N, tb):
+    C, ref, _ = _run_rows(groups, N, 77, tb, dist="int8range")
+    assert np.array_equal(C, ref)
+
+
 def _run_k(groups, M, N, alpha=1.0, beta=0.0, pads=(0, 0, 0), shift=0, dist="uniform", seed=0):
     import torch
-    lengths, before, after = GROUPS[groups]
+    lengths, before, after = GROUPS_AND_LARGE[groups]
     G = len(lengths)
     at, d_at = _offsets(lengths, before)
     K = int(at[-1]) + after
@@ -191,6 +226,19 @@ def test_k_exact_on_integers(groups):
     assert np.array_equal(C, ref)
 
 
+@pytest.mark.parametrize("M,N", [(500, 520), (501, 520), (500, 517), (501, 517), (129, 640)])
+@pytest.mark.parametrize("alpha,beta,pads,shift", [(1.0, 0.0, (0, 0, 0), 0), (0.5, 2.0, (1, 3, 2), 1),
+                                                   (-1.0, 0.0, (4, 0, 1), 3)])
+@pytest.mark.parametrize("groups", ["short groups", "long groups"])
+def test_k_of_many_tiles(groups, M, N, alpha, beta, pads, shift):
+    _check(*_run_k(groups, M, N, alpha, beta, pads, shift))
+
+
+def test_k_of_many_tiles_exact_on_integers():
+    C, ref, _ = _run_k("short groups", 500, 520, dist="int8range")
+    assert np.array_equal(C, ref)
+
+
 @pytest.mark.parametrize("at", [[0, 40, 20, 50], [-7, 10, 60, 90], [50, 0, 50, 0],
                                 [2 ** 62, 3, -2 ** 63, 50]])
 def test_offsets_out_of_range_write_nothing_outside(at):
@@ -210,6 +258,22 @@ def test_offsets_out_of_range_write_nothing_outside(at):
     assert (C[:20] == 7).all() and (C[20 + M:] == 7).all()
     assert (D[0] == 7).all() and (D[-1] == 7).all()
     assert torch.isfinite(C).all() and torch.isfinite(D).all()
+
+
+@pytest.mark.parametrize("tb", [0, 1])
+def test_offsets_out_of_range_with_many_tiles(tb):
+    import torch
+    M, N, K, G = 1200, 1000, 40, 40
+    g = np.random.default_rng(6)
+    at = np.sort(g.integers(0, M + 1, G + 1))
+    at[5], at[11], at[20], at[30], at[40] = -3, 2 ** 40, 7, M + 9, 900
+    d_at = torch.from_numpy(at).cuda()
+    A = torch.randn(M, K, device="cuda")
+    B = torch.randn(G, K * N, device="cuda")
+    C = torch.full((M + 40, N), 7.0, device="cuda")
+    sg.sgemm_run_grouped(tb, G, M, N, K, 1.0, A, K, B, K if tb else N, K * N, 0.0, C[20:], N, d_at)
+    torch.cuda.synchronize()
+    assert (C[:20] == 7).all() and (C[20 + M:] == 7).all() and torch.isfinite(C).all()
 
 
 def test_rows_far_apart():
