@@ -59,18 +59,20 @@ __global__ void __launch_bounds__(256) quantize_transposed_kernel(CastArgs p) {
   const int row = tile * kWave + lane;
   const int k0 = g * kGranule + w * 32;
   const bool in = row < p.rows;
+  // Every lane loads, from the nearest element there is, so that the loads go
+  // out together; what lies past K is then dropped.
+  const int last = p.K - 1, col = min(row, p.rows - 1);
   float v[32];
 #pragma unroll
   for (int e = 0; e < 32; ++e) {
-    const long at = (long)(k0 + e) * p.ldx + row;
-    v[e] = 0.f;
-    if (in && k0 + e < p.K) {
-      if constexpr (BF16)
-        v[e] = __uint_as_float((unsigned)static_cast<const unsigned short *>(p.X)[at] << 16);
-      else
-        v[e] = static_cast<const float *>(p.X)[at];
-    }
+    const long at = (long)min(k0 + e, last) * p.ldx + col;
+    if constexpr (BF16)
+      v[e] = __uint_as_float((unsigned)static_cast<const unsigned short *>(p.X)[at] << 16);
+    else
+      v[e] = static_cast<const float *>(p.X)[at];
   }
+#pragma unroll
+  for (int e = 0; e < 32; ++e) v[e] = k0 + e < p.K ? v[e] : 0.f;
   unsigned top = 0;
 #pragma unroll
   for (int q = 0; q < 4; ++q) top = max(top, magnitude_bits(v + 8 * q));
@@ -111,6 +113,34 @@ __device__ __forceinline__ unsigned short to_bf16(float x) {
   return __builtin_bit_cast(unsigned short, (__bf16)x);
 }
 
+// The first n (at most 8) of eight values to consecutive elements.
+template <bool BF16>
+__device__ __forceinline__ void store8(void *x, int n, const float v[8]) {
+  if constexpr (BF16) {
+    unsigned short *p = static_cast<unsigned short *>(x);
+    if (n >= 8) {
+      u32x4_any t;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) t[e] = to_bf16(v[2 * e]) | (unsigned)to_bf16(v[2 * e + 1]) << 16;
+      *reinterpret_cast<u32x4_any *>(p) = t;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (e < n) p[e] = to_bf16(v[e]);
+    }
+  } else {
+    float *p = static_cast<float *>(x);
+    if (n >= 8) {
+      *reinterpret_cast<f32x4_any *>(p) = f32x4{v[0], v[1], v[2], v[3]};
+      *reinterpret_cast<f32x4_any *>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (e < n) p[e] = v[e];
+    }
+  }
+}
+
 template <bool BF16>
 __global__ void __launch_bounds__(256) dequantize_kernel(CastArgs p) {
   const int tid = threadIdx.x;
@@ -128,14 +158,7 @@ __global__ void __launch_bounds__(256) dequantize_kernel(CastArgs p) {
     decode8(codes, scale_value(s), v);
     char *x = static_cast<char *>(const_cast<void *>(p.X)) +
               ((long)row * p.ldx + k) * (BF16 ? 2 : 4);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      if (k + e >= p.K) break;
-      if constexpr (BF16)
-        reinterpret_cast<unsigned short *>(x)[e] = to_bf16(v[e]);
-      else
-        reinterpret_cast<float *>(x)[e] = v[e];
-    }
+    store8<BF16>(x, p.K - k, v);
   }
 }
 
