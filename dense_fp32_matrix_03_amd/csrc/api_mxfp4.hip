@@ -123,14 +123,20 @@ int run(int64_t groups, int64_t M, int64_t N, int64_t K, float alpha, int typeA,
   p.ldc = ldc;
   p.offsets = grouped ? offsets : nullptr;
   hipError_t err = hipSuccess;
+  int a_type = SGEMM_TYPE_MXFP4;
   if (reads_ab && !held) {
-    unsigned char *codes = static_cast<unsigned char *>(workspace);
-    unsigned char *scales = codes + codes_bytes(M, K);
-    err = sgemm::launch_mxfp4_quantize(false, typeA == SGEMM_TYPE_BF16,
-                                       cast_args(M, K, A, lda, codes, scales, M), s);
-    p.a = {codes, reinterpret_cast<unsigned *>(scales), (long)M};
+    if (sgemm::mxfp4_casts(p)) {
+      a_type = typeA;
+    } else {
+      unsigned char *codes = static_cast<unsigned char *>(workspace);
+      unsigned char *scales = codes + codes_bytes(M, K);
+      err = sgemm::launch_mxfp4_quantize(false, typeA == SGEMM_TYPE_BF16,
+                                         cast_args(M, K, A, lda, codes, scales, M), s);
+      p.a = {codes, reinterpret_cast<unsigned *>(scales), (long)M};
+    }
   }
-  if (err == hipSuccess) err = sgemm::launch_mxfp4_product(p, typeC == SGEMM_TYPE_BF16, cus, s);
+  if (err == hipSuccess)
+    err = sgemm::launch_mxfp4_product(p, a_type, typeC == SGEMM_TYPE_BF16, cus, s);
   return err == hipSuccess ? SGEMM_OK : SGEMM_ERR_LAUNCH;
 }
 

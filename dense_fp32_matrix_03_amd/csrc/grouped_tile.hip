@@ -66,12 +66,12 @@ grouped_tile_kernel(GroupedArgs p, int tiles_m, int tiles_n) {
     const int rank = blockIdx.x / per;
     const int t = xcd_contiguous_id(blockIdx.x % per, per);
     const int g = group_by_length(p.offsets, p.groups, p.K, rank);
-    long first, last;
+    int first, last;
     group_range(p.offsets, g, p.K, first, last);
     A += first * p.lda;
     B += first * p.ldb;
     C += (long)g * p.strideC;
-    K = (int)(last - first);
+    K = last - first;
     m0 = t / tiles_n * BM;
     n0 = t % tiles_n * BN;
     m_end = p.M;

@@ -31,8 +31,9 @@ struct CastArgs {
 hipError_t launch_mxfp4_quantize(bool trans, bool bf16, const CastArgs &p, hipStream_t s);
 hipError_t launch_mxfp4_dequantize(bool trans, bool bf16, const CastArgs &p, hipStream_t s);
 
-// C = alpha A B^T + beta C over held B; A held, or (a_type 0: FP32, 1:
-// bfloat16) cast by the kernel.  offsets: null, or the groups of sgemm_run_mxfp4_grouped.
+// C = alpha A B^T + beta C over held B; A held, or values that the kernel casts
+// (a.codes points to them and a.lds is their leading dimension).  offsets:
+// null, or the groups of sgemm_run_mxfp4_grouped.
 struct Mxfp4Args {
   int M, N, K, groups;
   float alpha, beta;
@@ -42,10 +43,14 @@ struct Mxfp4Args {
   const int64_t *offsets;
 };
 
+// Whether the product's kernel is to cast A itself: only then may a_type below
+// be other than SGEMM_TYPE_MXFP4.
+bool mxfp4_casts(const Mxfp4Args &p);
 // Picks the kernel for the product.
-hipError_t launch_mxfp4_product(const Mxfp4Args &p, bool c_bf16, int cus, hipStream_t s);
-// mxfp4_tile.hip: tiles of 256 x 256 or 128 x 128 through LDS.
-hipError_t launch_mxfp4_tile(int tile, const Mxfp4Args &p, bool c_bf16, hipStream_t s);
+hipError_t launch_mxfp4_product(const Mxfp4Args &p, int a_type, bool c_bf16, int cus,
+                                hipStream_t s);
+// mxfp4_tile.hip: tiles through LDS; A held.
+hipError_t launch_mxfp4_tile(const Mxfp4Args &p, bool c_bf16, int cus, hipStream_t s);
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
@@ -148,6 +153,20 @@ __device__ __forceinline__ unsigned magnitude_bits(const float v[8]) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
   return top;
+}
+
+// The cast of eight consecutive values, by 16 lanes that together have the 128
+// of a granule (lane % 16 its eighth of 16): returns the lane's codes and
+// gives every lane the granule's four scale bytes.
+__device__ __forceinline__ unsigned mxfp4_cast8(const float v[8], int lane, unsigned &scales) {
+  unsigned top = magnitude_bits(v);
+  top = max(top, (unsigned)__shfl_xor((int)top, 1));
+  top = max(top, (unsigned)__shfl_xor((int)top, 2));
+  const unsigned s = mxfp4_scale(top);
+  scales = s << (8 * (lane % 16 / 4));
+  scales |= (unsigned)__shfl_xor((int)scales, 4);
+  scales |= (unsigned)__shfl_xor((int)scales, 8);
+  return mxfp4_codes8(v, s);
 }
 
 }  // namespace sgemm

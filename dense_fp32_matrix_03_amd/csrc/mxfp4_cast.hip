@@ -36,15 +36,9 @@ __global__ void __launch_bounds__(256) quantize_kernel(CastArgs p) {
     float v[8];
     const char *x = static_cast<const char *>(p.X) + ((long)row * p.ldx + k) * (BF16 ? 2 : 4);
     load8<BF16>(x, in ? left : 0, v);
-    unsigned top = magnitude_bits(v);
-    top = max(top, (unsigned)__shfl_xor((int)top, 1));
-    top = max(top, (unsigned)__shfl_xor((int)top, 2));
-    const unsigned s = mxfp4_scale(top);
-    unsigned all = s << (8 * (l16 / 4));
-    all |= (unsigned)__shfl_xor((int)all, 4);
-    all |= (unsigned)__shfl_xor((int)all, 8);
+    unsigned all;
+    const unsigned codes = mxfp4_cast8(v, tid, all);
     if (in) {
-      const unsigned codes = mxfp4_codes8(v, s);
       reinterpret_cast<unsigned *>(p.codes)[(long)row * (p.granules * 16) + g * 16 + l16] = codes;
       if (l16 == 0) p.scales[(long)g * p.lds + row] = all;
     }

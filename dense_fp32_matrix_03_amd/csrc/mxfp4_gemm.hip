@@ -1,59 +1,60 @@
-// mxfp4_gemm.hip -- products of matrices held in microscaled 4-bit floating
-// point (include/sgemm_mxfp4.h), on v_mfma_scale_f32_16x16x128_f8f6f4.
+// mxfp4_gemm.hip -- products of few rows with a matrix held in microscaled
+// 4-bit floating point (include/sgemm_mxfp4.h), and the choice between this
+// kernel and the tiles of mxfp4_tile.hip.
 //
 // C(m, n) = alpha sum_b 2^(sa(m, b) + sb(n, b) - 254) sum_{k in b} a(m, k) b(n, k)
-// + beta C(m, n) over blocks b of 32 k.  The instruction multiplies 16 rows of
-// A by 16 rows of B over 128 k; lane quarter q supplies one block of 32 codes
-// (16 bytes) of row l % 16 of each operand, and that block's scale byte, which
-// op_sel picks from the four bytes of a register.
+// + beta C(m, n) over blocks b of 32 k, on v_mfma_scale_f32_16x16x128_f8f6f4.
+// The instruction multiplies 16 rows of A by 16 rows of B over 128 k; lane
+// quarter q supplies one block of 32 codes (16 bytes) of row l % 16 of each
+// operand, and that block's scale byte, which op_sel picks from the four bytes
+// of a register.
 //
-// The four blocks that an instruction covers need not be neighbours, as long
-// as A and B agree.  In a unit of 512 k (four granules of 128), quarter q has
-// granule q and instruction s its block s: a lane then reads 64 consecutive
-// bytes of codes and one dword of scales for four instructions, and the
-// scales of 16 rows are 64 consecutive bytes.
-#include "grouped_map.hpp"
-#include "mxfp4.hpp"
+// With few rows the time is that of reading B once, so B goes straight from
+// global memory into registers, and k is split over the waves of a work-group
+// to have enough of it in flight.  The four blocks that an instruction covers
+// need not be neighbours, as long as A and B agree.  In a unit of 512 k (four
+// granules of 128), quarter q has granule q and instruction s its block s: a
+// lane then reads 64 consecutive bytes of codes and one dword of scales for
+// four instructions, and the scales of 16 rows are 64 consecutive bytes.
+//
+// A of single precision or bfloat16 is cast by each wave as it needs it, a row
+// of a unit at a time: 8 values a lane, so 4 lanes have a block and 16 a
+// granule, as in the cast's own kernel.  The codes pass through LDS to the lanes
+// that multiply them.  That costs each work-group the cast of its rows again,
+// but no second launch: for one row by 8192 x 2048 it saves the cast's own 3
+// us, as long as the product takes.
 #include "mfma_dma.hpp"
+#include "mxfp4.hpp"
+#include "sgemm_mxfp4.h"
 
 namespace sgemm {
 
 namespace {
 
-// MT x NT blocks of 16 x 16 per wave; KS waves split k in units of 512.
-template <int MT, int NT, int KS, bool CBF16>
-__global__ void __launch_bounds__(KS *kWave) mxfp4_kernel(Mxfp4Args p, int tiles_m, int tiles_n) {
+// All of A's rows, MT blocks of 16, and NT blocks of 16 rows of B per work-group;
+// KS waves split k in units of 512.
+// TA: A's type (SGEMM_TYPE_*).
+template <int MT, int NT, int KS, int TA, bool CBF16>
+__global__ void __launch_bounds__(KS *kWave) mxfp4_kernel(Mxfp4Args p) {
+  static_assert(TA == SGEMM_TYPE_MXFP4 || MT == 1, "only 16 rows are cast on the way");
   const int lane = threadIdx.x % kWave;
   const int kq = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int r16 = lane % 16, q = lane / 16;
   const int granules = (p.K + 127) / 128;
-  long a_row = 0, b_row = 0;  // first row of the group in A (and C), and of its B
-  int m0, n0, m_end = p.M;
-  if (p.offsets) {
-    const GroupTile t = group_tile(p.offsets, p.groups, p.M, MT * 16, tiles_n, 8);
-    if (!t.valid) return;
-    a_row = t.row0;
-    b_row = (long)t.g * p.N;
-    m0 = t.tm * MT * 16;
-    n0 = t.tn * NT * 16;
-    m_end = t.rows;
-  } else {
-    m0 = (int)(blockIdx.x / tiles_n) * MT * 16;
-    n0 = (int)(blockIdx.x % tiles_n) * NT * 16;
-  }
+  const int n0 = blockIdx.x * NT * 16;
 
   // Rows past the end repeat the last one: what they give is not stored.
   const i32x4 *a_at[MT], *b_at[NT];
   const unsigned *as_at[MT], *bs_at[NT];
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
-    const long r = a_row + min(m0 + 16 * i + r16, m_end - 1);
+    const long r = min(16 * i + r16, p.M - 1);
     a_at[i] = reinterpret_cast<const i32x4 *>(p.a.codes) + r * granules * 4;
     as_at[i] = p.a.scales + r;
   }
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
-    const long r = b_row + min(n0 + 16 * j + r16, p.N - 1);
+    const long r = min(n0 + 16 * j + r16, p.N - 1);
     b_at[j] = reinterpret_cast<const i32x4 *>(p.b.codes) + r * granules * 4;
     bs_at[j] = p.b.scales + r;
   }
@@ -63,98 +64,160 @@ __global__ void __launch_bounds__(KS *kWave) mxfp4_kernel(Mxfp4Args p, int tiles
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  const int nk = p.alpha != 0.f ? granules : 0;
-  for (int g0 = 4 * kq; g0 < nk; g0 += 4 * KS) {
-    const int g = g0 + q;
-    const bool in = g < granules;
+  // The cast A of one unit per wave: rows of 256 bytes of codes, 272 apart so
+  // that 16 lanes' reads of a chunk fall on distinct banks, and their scales.
+  constexpr int kPitch = 272 / 4;
+  __shared__ __attribute__((aligned(16))) unsigned cast_codes[TA == SGEMM_TYPE_MXFP4 ? 4 : KS * 16 * kPitch];
+  __shared__ unsigned cast_scales[TA == SGEMM_TYPE_MXFP4 ? 1 : KS * 16 * 4];
+
+  struct Operand {
     i32x4 a[MT][4], b[NT][4];
     int as[MT], bs[NT];
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      as[i] = in ? (int)as_at[i][g * p.a.lds] : 0;
-#pragma unroll
-      for (int s = 0; s < 4; ++s) a[i][s] = in ? a_at[i][g * 4 + s] : i32x4{0, 0, 0, 0};
-    }
+  };
+  // Granules past the last one give zeros.
+  auto load = [&](int g0, Operand &o, auto whole) {
+    const int g = g0 + q;
+    const bool in = decltype(whole)::value || g < granules;
+    const i32x4 zero = {0, 0, 0, 0};
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      bs[j] = in ? (int)bs_at[j][g * p.b.lds] : 0;
 #pragma unroll
-      for (int s = 0; s < 4; ++s) b[j][s] = in ? b_at[j][g * 4 + s] : i32x4{0, 0, 0, 0};
+      for (int s = 0; s < 4; ++s) o.b[j][s] = in ? b_at[j][g * 4 + s] : zero;
+      o.bs[j] = in ? (int)bs_at[j][g * p.b.lds] : 0;
     }
+    if constexpr (TA == SGEMM_TYPE_MXFP4) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s) o.a[i][s] = in ? a_at[i][g * 4 + s] : zero;
+        o.as[i] = in ? (int)as_at[i][g * p.a.lds] : 0;
+      }
+    }
+  };
+  auto cast = [&](int g0, Operand &o) {
+    constexpr bool BF16 = TA == SGEMM_TYPE_BF16;
+    unsigned *codes = cast_codes + kq * 16 * kPitch, *scales = cast_scales + kq * 16 * 4;
+    const int k = g0 * 128 + lane * 8;
+    const char *x = reinterpret_cast<const char *>(p.a.codes) + (long)k * (BF16 ? 2 : 4);
+    const long row_bytes = p.a.lds * (BF16 ? 2 : 4);
+    for (int r = 0; r < p.M; r += 4) {  // four rows' loads go out together
+      float v[4][8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) load8<BF16>(x + min(r + i, p.M - 1) * row_bytes, p.K - k, v[i]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (r + i >= p.M) break;
+        unsigned all;
+        codes[(r + i) * kPitch + lane] = mxfp4_cast8(v[i], lane, all);
+        if (r16 == 0) scales[(r + i) * 4 + q] = all;
+      }
+    }
+    // The wave's own LDS accesses keep their order; the fence keeps the
+    // compiler's.
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    const int r = min(r16, p.M - 1);
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+      o.a[0][s] = *reinterpret_cast<const i32x4 *>(codes + r * kPitch + q * 16 + s * 4);
+    o.as[0] = (int)scales[r * 4 + q];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  };
+  auto mma = [&](const Operand &o) {
     static_for<4>([&](auto S) {
       constexpr int s = decltype(S)::value;
 #pragma unroll
       for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int j = 0; j < NT; ++j)
-          acc[i][j] = mfma_fp4_16x16x128<s>(a[i][s], b[j][s], acc[i][j], as[i], bs[j]);
+          acc[i][j] = mfma_fp4_16x16x128<s>(o.a[i][s], o.b[j][s], acc[i][j], o.as[i], o.bs[j]);
     });
+  };
+  auto load_any = [&](int g0, Operand &o) {
+    if (g0 + 4 <= granules)
+      load(g0, o, std::true_type());
+    else if (g0 < granules)
+      load(g0, o, std::false_type());
+  };
+  // The next unit's B (and held A) is on its way while this one is multiplied.
+  Operand cur, nxt;
+  load_any(4 * kq, cur);
+  for (int g0 = 4 * kq; g0 < granules; g0 += 4 * KS) {
+    load_any(g0 + 4 * KS, nxt);
+    if constexpr (TA != SGEMM_TYPE_MXFP4) cast(g0, cur);
+    mma(cur);
+    cur = nxt;
   }
 
-  if constexpr (KS > 1) {
-    __shared__ f32x4 red[(KS - 1) * MT * NT * kWave];
-    if (kq > 0) {
+  __shared__ f32x4 red[(KS - 1) * MT * NT * kWave];
+  if (kq > 0) {
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
+    for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
-          red[((kq - 1) * MT * NT + i * NT + j) * kWave + lane] = acc[i][j];
-    }
-    __syncthreads();
-    if (kq > 0) return;
-#pragma unroll
-    for (int s = 0; s < KS - 1; ++s)
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) acc[i][j] += red[(s * MT * NT + i * NT + j) * kWave + lane];
+      for (int j = 0; j < NT; ++j)
+        red[((kq - 1) * MT * NT + i * NT + j) * kWave + lane] = acc[i][j];
   }
+  __syncthreads();
+  if (kq > 0) return;
+#pragma unroll
+  for (int s = 0; s < KS - 1; ++s)
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) acc[i][j] += red[(s * MT * NT + i * NT + j) * kWave + lane];
 
   // Register e of lane l holds row 4 (l / 16) + e, column l % 16 of a block.
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int m = m0 + 16 * i + 4 * q + e;
-      if (m >= m_end) continue;
+      const int m = 16 * i + 4 * q + e;
+      if (m >= p.M) continue;
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         const int n = n0 + 16 * j + r16;
         if (n >= p.N) continue;
-        store_c<CBF16>(p, (a_row + m) * p.ldc + n, acc[i][j][e]);
+        store_c<CBF16>(p, m * p.ldc + n, acc[i][j][e]);
       }
     }
 }
 
-// The tile through LDS.  In units of a 256 x 256 tile's time, a compute unit
-// takes 0.56 for one tile of 128 x 128, 0.73 for two (they share it), and 0.29
-// a tile for more: measured on 256 compute units with bfloat16 C, 2048^3 24.0
-// us with 64 tiles of 256 x 256 and 13.5 with 256 of 128 x 128, 1024 x 8192 x
-// 8192 56.3 (128 tiles) and 40.8 (512), 4096^3 38.8 (256) and 42.9 (1024),
-// 8192^3 250 (1024) and 298 (4096).  Groups count with their mean length.
-int mxfp4_tile_size(const Mxfp4Args &p, int cus) {
-  const long groups = p.offsets ? p.groups : 1, mean = (p.M + groups - 1) / groups;
-  auto per_cu = [&](long t) {
-    const long tiles = groups * ((mean + t - 1) / t) * ((p.N + t - 1) / t);
-    return (double)((tiles + cus - 1) / cus);
-  };
-  const double n = per_cu(128);
-  return per_cu(256) <= (n == 1 ? 0.56 : n == 2 ? 0.73 : 0.29 * n) ? 256 : 128;
+template <int MT, int NT, int TA>
+hipError_t launch(const Mxfp4Args &p, bool c_bf16, hipStream_t s) {
+  const dim3 grid((unsigned)((p.N + NT * 16L - 1) / (NT * 16)));
+  // Eight waves from five units of k on: 16 x 8192 x 8192 takes 12.3 us with
+  // them and 13.8 with four, 16 x 2048 x 2048 3.6 with either.
+  if (p.K > 2048) {
+    if (c_bf16)
+      hipLaunchKernelGGL((mxfp4_kernel<MT, NT, 8, TA, true>), grid, dim3(8 * kWave), 0, s, p);
+    else
+      hipLaunchKernelGGL((mxfp4_kernel<MT, NT, 8, TA, false>), grid, dim3(8 * kWave), 0, s, p);
+  } else {
+    if (c_bf16)
+      hipLaunchKernelGGL((mxfp4_kernel<MT, NT, 4, TA, true>), grid, dim3(4 * kWave), 0, s, p);
+    else
+      hipLaunchKernelGGL((mxfp4_kernel<MT, NT, 4, TA, false>), grid, dim3(4 * kWave), 0, s, p);
+  }
+  return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_mxfp4_product(const Mxfp4Args &p, bool c_bf16, int cus, hipStream_t s) {
-  const long mean = p.M / (p.offsets ? p.groups : 1);
-  if (mean > 64) return launch_mxfp4_tile(mxfp4_tile_size(p, cus), p, c_bf16, s);
-  const int tiles_n = (p.N + 31) / 32, tiles_m = (p.M + 15) / 16;
-  const long rows = p.offsets ? group_tile_rows(p.M, p.groups, 16) : tiles_m;
-  const dim3 grid((unsigned)(rows * tiles_n)), block(4 * kWave);
-  if (c_bf16)
-    hipLaunchKernelGGL((mxfp4_kernel<1, 2, 4, true>), grid, block, 0, s, p, tiles_m, tiles_n);
-  else
-    hipLaunchKernelGGL((mxfp4_kernel<1, 2, 4, false>), grid, block, 0, s, p, tiles_m, tiles_n);
-  return hipGetLastError();
+// Casting M rows in every work-group beats a launch of the cast while the
+// rows are short and few: 1 x 8192 x 2048 4.8 us against 2.7 + 4.0, 2 x 8192 x
+// 8192 11.9 against 2.8 + 9.9; 4 x 8192 x 8192 13.9 against 2.6 + 10.2.
+bool mxfp4_casts(const Mxfp4Args &p) {
+  return !p.offsets && p.M <= 16 && (long)p.M * p.K <= 16384;
+}
+
+// Up to 32 rows this kernel: 16 x 8192 x 8192 12.3 us (64 x 64 tile 18.2), 32
+// rows 14.3 (18.5); 64 rows 21.4 (19.2).  Groups take the tiles.
+hipError_t launch_mxfp4_product(const Mxfp4Args &p, int a_type, bool c_bf16, int cus,
+                                hipStream_t s) {
+  if (a_type == SGEMM_TYPE_F32) return launch<1, 1, SGEMM_TYPE_F32>(p, c_bf16, s);
+  if (a_type == SGEMM_TYPE_BF16) return launch<1, 1, SGEMM_TYPE_BF16>(p, c_bf16, s);
+  if (p.offsets || p.M > 32) return launch_mxfp4_tile(p, c_bf16, cus, s);
+  return p.M <= 16 ? launch<1, 1, SGEMM_TYPE_MXFP4>(p, c_bf16, s)
+                   : launch<2, 2, SGEMM_TYPE_MXFP4>(p, c_bf16, s);
 }
 
 }  // namespace sgemm

@@ -18,6 +18,8 @@
 // whatever follows in memory, below that end (every code is finite), but both
 // operands' scales there read as 0: the products are at most 36 2^-254 and
 // vanish in single precision.
+#include <math.h>
+
 #include "grouped_map.hpp"
 #include "mfma_dma.hpp"
 #include "mxfp4.hpp"
@@ -28,10 +30,14 @@ namespace {
 
 constexpr int kSliceBytes = 128;  // codes of a row's slice
 
-template <int BM, int BN, int WM, int WN, int NST, bool CBF16>
-__global__ void __launch_bounds__(WM *WN *kWave, 2)
+// KS sets of WM x WN waves share a tile; set q takes slices q, q + KS, ..
+// through LDS stages of its own, and the sets' sums are added in order at the
+// end.  With few tiles the time is a chain of slices, each as long as its
+// loads take to arrive: the sets walk KS chains at once.
+template <int BM, int BN, int WM, int WN, int KS, int NST, bool CBF16>
+__global__ void __launch_bounds__(WM *WN *KS *kWave, 2)
 mxfp4_tile_kernel(Mxfp4Args p, TileMap tmap, int tiles_n) {
-  constexpr int NW = WM * WN;
+  constexpr int NW = WM * WN;  // waves of a set
   constexpr int WTM = BM / WM, WTN = BN / WN, FM = WTM / 32, FN = WTN / 32;
   constexpr int QA = BM * kSliceBytes / 1024 / NW, QB = BN * kSliceBytes / 1024 / NW;
   // Loads of 64 rows' scales of a granule.  Where they do not split evenly, some waves'
@@ -46,29 +52,31 @@ mxfp4_tile_kernel(Mxfp4Args p, TileMap tmap, int tiles_n) {
   // into one stage do not touch the one that is read (mfma_dma.hpp).
   static_assert(NST >= 2 && NST <= 4, "2 to 4 LDS stages");
   constexpr int SA = BM * kSliceBytes / 4, SB = BN * kSliceBytes / 4, SS = QS * NW * 64;
-  __shared__ __attribute__((aligned(1024))) float As0[SA], As1[SA], As2[NST > 2 ? SA : 1],
-      As3[NST > 3 ? SA : 1];
-  __shared__ __attribute__((aligned(1024))) float Bs0[SB], Bs1[SB], Bs2[NST > 2 ? SB : 1],
-      Bs3[NST > 3 ? SB : 1];
-  __shared__ __attribute__((aligned(1024))) float Ss0[SS], Ss1[SS], Ss2[NST > 2 ? SS : 1],
-      Ss3[NST > 3 ? SS : 1];  // scales: A's rows, then B's
+  __shared__ __attribute__((aligned(1024))) float As0[KS * SA], As1[KS * SA],
+      As2[NST > 2 ? KS * SA : 1], As3[NST > 3 ? KS * SA : 1];
+  __shared__ __attribute__((aligned(1024))) float Bs0[KS * SB], Bs1[KS * SB],
+      Bs2[NST > 2 ? KS * SB : 1], Bs3[NST > 3 ? KS * SB : 1];
+  __shared__ __attribute__((aligned(1024))) float Ss0[KS * SS], Ss1[KS * SS],
+      Ss2[NST > 2 ? KS * SS : 1], Ss3[NST > 3 ? KS * SS : 1];  // scales: A's rows, then B's
+
+  const int lane = threadIdx.x % kWave;
+  const int all_waves = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int kq = KS > 1 ? all_waves / NW : 0;
+  const int wave = KS > 1 ? all_waves % NW : all_waves;
+  const int wm = wave / WN, wn = wave % WN;
+  const int r32 = lane % 32, half = lane / 32;
   auto stage_a = [&](auto S) -> float * {
     constexpr int i = decltype(S)::value;
-    return i == 0 ? As0 : i == 1 ? As1 : i == 2 ? As2 : As3;
+    return (i == 0 ? As0 : i == 1 ? As1 : i == 2 ? As2 : As3) + kq * SA;
   };
   auto stage_b = [&](auto S) -> float * {
     constexpr int i = decltype(S)::value;
-    return i == 0 ? Bs0 : i == 1 ? Bs1 : i == 2 ? Bs2 : Bs3;
+    return (i == 0 ? Bs0 : i == 1 ? Bs1 : i == 2 ? Bs2 : Bs3) + kq * SB;
   };
   auto stage_s = [&](auto S) -> float * {
     constexpr int i = decltype(S)::value;
-    return i == 0 ? Ss0 : i == 1 ? Ss1 : i == 2 ? Ss2 : Ss3;
+    return (i == 0 ? Ss0 : i == 1 ? Ss1 : i == 2 ? Ss2 : Ss3) + kq * SS;
   };
-
-  const int lane = threadIdx.x % kWave;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int wm = wave / WN, wn = wave % WN;
-  const int r32 = lane % 32, half = lane / 32;
 
   long a_row = 0, b_row = 0;  // first row of the group in A (and C), and of its B
   int m0, n0, m_end = p.M;
@@ -109,28 +117,41 @@ mxfp4_tile_kernel(Mxfp4Args p, TileMap tmap, int tiles_n) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, records,
                                              kRawBufferWord3);
   };
-  // Slices at or past nk get descriptors without records: nothing is fetched.
-  // No branch depends on that, so that the loads can be scheduled between
-  // matrix-core instructions.
-  auto dma = [&](auto S, int t) {
-    const bool live = t < nk;
-    const long k0 = (long)t * kSliceBytes;
-    const __amdgpu_buffer_rsrc_t ra = rsrc(a0 + k0, live ? rows_a * pitch - (int)k0 : 0);
-    const __amdgpu_buffer_rsrc_t rb = rsrc(b0 + k0, live ? rows_b * pitch - (int)k0 : 0);
+  // Loads of the set's next slice into stage S.  Slices at or past nk get
+  // descriptors without records: nothing is fetched.  No branch depends on
+  // that, so that the loads can be scheduled between matrix-core instructions.
+  int k = kq;  // the slice
+  const unsigned *s_base[QS];
+  long s_lds[QS];
+  unsigned s_off[QS];
+  int s_records[QS], s_granule[QS];
+#pragma unroll
+  for (int q = 0; q < QS; ++q) {
+    const int u = wave + q * NW;  // uniform: which 64 rows of which granule
+    const bool of_a = u < BM / 32;
+    const int v = of_a ? u : u - BM / 32, per = of_a ? BM / 64 : BN / 64;
+    s_lds[q] = of_a ? p.a.lds : p.b.lds;
+    s_granule[q] = v / per;
+    s_base[q] = of_a ? sa0 : sb0;
+    s_off[q] = (unsigned)(v % per * 64 + lane) * 4u;
+    s_records[q] = u < US ? 4 * (of_a ? rows_a : rows_b) : 0;
+  }
+  auto dma = [&](auto S) {
+    const bool live = k < nk;
+    const int k0 = k * kSliceBytes;
+    const __amdgpu_buffer_rsrc_t ra = rsrc(a0 + k0, live ? rows_a * pitch - k0 : 0);
+    const __amdgpu_buffer_rsrc_t rb = rsrc(b0 + k0, live ? rows_b * pitch - k0 : 0);
 #pragma unroll
     for (int q = 0; q < QA; ++q) lds_dma<true>(ra, stage_a(S) + (wave + q * NW) * 256, off[q]);
 #pragma unroll
     for (int q = 0; q < QB; ++q) lds_dma<true>(rb, stage_b(S) + (wave + q * NW) * 256, off[q]);
 #pragma unroll
     for (int q = 0; q < QS; ++q) {
-      const int u = wave + q * NW;  // uniform: which 64 rows of which granule
-      const bool of_a = u < BM / 32;
-      const int v = of_a ? u : u - BM / 32, per = of_a ? BM / 64 : BN / 64;
-      const int g = 2 * t + v / per, r0 = v % per * 64;
-      const unsigned *base = (of_a ? sa0 : sb0) + g * (of_a ? p.a.lds : p.b.lds);
-      const int records = g < granules && u < US ? 4 * (of_a ? rows_a : rows_b) : 0;
-      lds_dma<false>(rsrc(base, records), stage_s(S) + u * 64, (unsigned)(r0 + lane) * 4u);
+      const int g = 2 * k + s_granule[q];
+      lds_dma<false>(rsrc(s_base[q] + g * s_lds[q], g < granules ? s_records[q] : 0),
+                     stage_s(S) + (wave + q * NW) * 64, s_off[q]);
     }
+    k += KS;
   };
 
   const int sw = kc_swizzle<32, true>(r32);
@@ -166,7 +187,6 @@ mxfp4_tile_kernel(Mxfp4Args p, TileMap tmap, int tiles_n) {
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
 
-  Ops cur, nxt;
   Scales sc, sn;
   auto mma = [&](auto STEP, const Ops &o) {
     constexpr int s = decltype(STEP)::value;
@@ -176,6 +196,7 @@ mxfp4_tile_kernel(Mxfp4Args p, TileMap tmap, int tiles_n) {
       for (int j = 0; j < FN; ++j)
         acc[i][j] = mfma_fp4_32x32x64<s>(o.a[i], o.b[j], acc[i][j], sc.a[i], sc.b[j]);
   };
+
   // A step's operand reads (and a slice's loads) are spread between its
   // matrix-core instructions.
   constexpr int kMfma = FM * FN, kReads = FM + FN;
@@ -192,44 +213,89 @@ mxfp4_tile_kernel(Mxfp4Args p, TileMap tmap, int tiles_n) {
     });
   };
   using S0 = std::integral_constant<int, 0>;
-  // Slice t is in stage S, slices t + 1 .. t + NST - 1 on their way to the
-  // others.  The last step waits for slice t + 1, and for every wave to be done
-  // with stage S, then sends slice t + NST there and reads slice t + 1's first
-  // operands.
-  auto slice = [&](auto S, int t) {
+  // The set's t-th slice is in stage S, the next NST - 1 on their way to the
+  // others.
+  // WHOLE: a wave with one block of 32 x 32 has too few matrix-core
+  // instructions in a step to cover the next one's reads, and registers to
+  // spare: it reads a whole slice's operands while it multiplies the one
+  // before.  The barrier waits for slice t + 1, and for every wave to have read
+  // slice t; then slice t + NST goes to stage S.
+  // Otherwise the operands are read a step ahead, and the last step of a slice
+  // waits for slice t + 1, and for every wave to be done with stage S, sends
+  // slice t + NST there and reads slice t + 1's first operands.
+  constexpr bool WHOLE = FM * FN == 1;
+  constexpr int kAhead = WHOLE ? 4 : 1;  // steps whose operands are held
+  Ops cur[kAhead], nxt[kAhead];
+  auto read_ahead = [&](auto S, Ops *o) {
+#pragma unroll
+    for (int s = 0; s < kAhead; ++s) read_ops(S, s, o[s]);
+  };
+  auto slice = [&](auto S) {
     using SN = std::integral_constant<int, (decltype(S)::value + 1) % NST>;
-    static_for<4>([&](auto STEP) {
-      constexpr int s = decltype(STEP)::value;
-      if constexpr (s < 3) {
-        read_ops(S, s + 1, nxt);
-        mma(STEP, cur);
-        interleave(std::false_type());
-      } else {
-        dma_barrier_keep<(NST - 2) * kLoads>();
-        dma(S, t + NST);
-        read_ops(SN(), 0, nxt);
-        read_scales(SN(), sn);
-        mma(STEP, cur);
-        interleave(std::true_type());
-      }
-      cur = nxt;
-    });
+    if constexpr (WHOLE) {
+      dma_barrier_keep<(NST - 2) * kLoads>();
+      dma(S);
+      read_ahead(SN(), nxt);
+      read_scales(SN(), sn);
+      static_for<4>([&](auto STEP) { mma(STEP, cur[decltype(STEP)::value]); });
+#pragma unroll
+      for (int s = 0; s < kAhead; ++s) cur[s] = nxt[s];
+    } else {
+      static_for<4>([&](auto STEP) {
+        constexpr int s = decltype(STEP)::value;
+        if constexpr (s < 3) {
+          read_ops(S, s + 1, nxt[0]);
+          mma(STEP, cur[0]);
+          interleave(std::false_type());
+        } else {
+          dma_barrier_keep<(NST - 2) * kLoads>();
+          dma(S);
+          read_ops(SN(), 0, nxt[0]);
+          read_scales(SN(), sn);
+          mma(STEP, cur[0]);
+          interleave(std::true_type());
+        }
+        cur[0] = nxt[0];
+      });
+    }
     sc = sn;
   };
 
   if (nk > 0) {
-    static_for<NST>([&](auto S) { dma(S, decltype(S)::value); });
+    const int turns = (nk + KS - 1) / KS;  // the same for all sets: they share the barriers
+    static_for<NST>([&](auto S) { dma(S); });
     dma_barrier_keep<(NST - 1) * kLoads>();
-    read_ops(S0(), 0, cur);
+    read_ahead(S0(), cur);
     read_scales(S0(), sc);
-    for (int t = 0; t < nk; t += NST) {
+    for (int t = 0; t < turns; t += NST) {
       static_for<NST>([&](auto S) {
-        if (decltype(S)::value == 0 || t + decltype(S)::value < nk) slice(S, t + decltype(S)::value);
+        if (decltype(S)::value == 0 || t + decltype(S)::value < turns) slice(S);
       });
     }
     // The last slices sent loads past K (no memory traffic): let them retire
     // before the work-group gives up its LDS.
     __builtin_amdgcn_s_waitcnt(0x0f70);
+  }
+
+  if constexpr (KS > 1) {
+    // The stages are free: every load has landed, every operand has been read.
+    // Set s > 0 leaves its sums at 4 KiFloat (s - 1) of As0, the last of four
+    // sets in Bs0.
+    static_assert(FM * FN * NW == 4 && (KS == 2 || KS == 4) && KS * SA == 2048 * KS &&
+                      SB == SA, "a set's sums are 16 KiB");
+    __syncthreads();
+    auto sums = [&](int set) { return (set == 3 ? Bs0 : As0 + (set - 1) * 4096) + wave * 1024 + lane; };
+    if (kq > 0) {
+      float *at = sums(kq);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) at[e * kWave] = acc[0][0][e];
+    }
+    __syncthreads();
+    if (kq > 0) return;
+#pragma unroll
+    for (int set = 1; set < KS; ++set)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[0][0][e] += sums(set)[e * kWave];
   }
 
   // Register e of lane l holds row acc32_row(l, e), column l % 32 of a block:
@@ -267,26 +333,52 @@ mxfp4_tile_kernel(Mxfp4Args p, TileMap tmap, int tiles_n) {
     store(std::false_type(), std::false_type());
 }
 
-template <int BM, int BN, int WM, int WN, int NST>
+template <int BM, int BN, int WM, int WN, int KS, int NST>
 hipError_t launch(const Mxfp4Args &p, bool c_bf16, hipStream_t s) {
   const int tiles_m = (p.M + BM - 1) / BM, tiles_n = (p.N + BN - 1) / BN;
   const long rows = p.offsets ? group_tile_rows(p.M, p.groups, BM) : tiles_m;
-  const dim3 grid((unsigned)(rows * tiles_n)), block(WM * WN * kWave);
+  const dim3 grid((unsigned)(rows * tiles_n)), block(WM * WN * KS * kWave);
   const TileMap tmap = make_tile_map(tiles_m, tiles_n, 8);
   if (c_bf16)
-    hipLaunchKernelGGL((mxfp4_tile_kernel<BM, BN, WM, WN, NST, true>), grid, block, 0, s, p, tmap,
+    hipLaunchKernelGGL((mxfp4_tile_kernel<BM, BN, WM, WN, KS, NST, true>), grid, block, 0, s, p, tmap,
                        tiles_n);
   else
-    hipLaunchKernelGGL((mxfp4_tile_kernel<BM, BN, WM, WN, NST, false>), grid, block, 0, s, p, tmap,
+    hipLaunchKernelGGL((mxfp4_tile_kernel<BM, BN, WM, WN, KS, NST, false>), grid, block, 0, s, p, tmap,
                        tiles_n);
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_mxfp4_tile(int tile, const Mxfp4Args &p, bool c_bf16, hipStream_t s) {
-  return tile == 256 ? launch<256, 256, 2, 4, 2>(p, c_bf16, s)
-                     : launch<128, 128, 2, 2, 2>(p, c_bf16, s);
+// Groups count with their mean length: the host does not know more.  In units
+// of a round of 256 x 256 tiles (one on each compute unit), a compute unit
+// takes for n tiles
+//   of 128 x 128   0.65 (n = 1), 0.77 (2), 0.29 n (more: two share the unit),
+//   of 64 x 64     0.35 (1), 0.42 (2), 0.16 n (more).
+// Measured on 256 compute units with bfloat16 C and K = 8192 (N = 8192), 64 x
+// 64 / 128 x 128 / 256 x 256: M = 128 25 / 39 / 64 us, 256 27 / 39 / 65, 512
+// 42 / 39 / 64, 1024 74 / 47 / 64, 8192 464 / 346 / 289; 2048 x 4096 x 4096
+// 39 / 24 / 33; 16 groups, 8192 rows by 2048 x 2048 53 / 43 / 46.  Groups of up
+// to 64 rows are bound by reading B, which the smallest tile does best: 32
+// groups, 48 rows by 4096 x 2048 27 / 31 / 42.  Two sets of waves on the 64 x
+// 64 tile take 19 us instead of 25 for 128 x 8192 x 8192 (24 for 27 at M =
+// 256), and nothing less where K is 2048 or tiles are many.
+hipError_t launch_mxfp4_tile(const Mxfp4Args &p, bool c_bf16, int cus, hipStream_t s) {
+  const long groups = !p.offsets ? 1 : p.groups < p.M ? p.groups : p.M;
+  const double mean = (double)p.M / groups;
+  auto per_cu = [&](long t) {
+    const double rows = p.offsets ? fmax(1.0, mean / t + 0.5) : ceil(mean / t);
+    return ceil(groups * rows * ((p.N + t - 1) / t) / cus);
+  };
+  const double n64 = per_cu(64), n128 = per_cu(128);
+  const double c64 = n64 == 1 ? 0.35 : n64 == 2 ? 0.42 : 0.16 * n64;
+  const double c128 = n128 == 1 ? 0.65 : n128 == 2 ? 0.77 : 0.29 * n128;
+  if ((p.offsets && mean <= 64) || (c64 <= c128 && c64 <= per_cu(256))) {
+    if (n64 <= 2 && p.K >= 4096) return launch<64, 64, 2, 2, 2, 2>(p, c_bf16, s);
+    return launch<64, 64, 2, 2, 1, 2>(p, c_bf16, s);
+  }
+  return c128 <= per_cu(256) ? launch<128, 128, 2, 2, 1, 2>(p, c_bf16, s)
+                             : launch<256, 256, 2, 4, 1, 2>(p, c_bf16, s);
 }
 
 }  // namespace sgemm

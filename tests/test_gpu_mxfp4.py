@@ -197,7 +197,8 @@ def _product(M, N, K, kind, out, alpha=1.0, beta=0.0, pads=(0, 0, 0), shift=0, s
 
 
 SIZES = [(1, 1, 1), (1, 64, 128), (5, 33, 45), (16, 128, 512), (17, 100, 700), (40, 129, 1000),
-         (70, 257, 333), (130, 300, 2050), (300, 520, 640)]
+         (70, 257, 333), (130, 300, 2050), (300, 520, 640), (1, 130, 9000), (2, 77, 2600),
+         (12, 200, 4500), (30, 333, 5000), (90, 200, 4200), (31, 65, 130)]
 
 
 @pytest.mark.parametrize("kind", ["f32", "bf16", "mxfp4"])
@@ -257,7 +258,8 @@ def test_product_without_k(out):
     _check(*_product(40, 50, 0, "f32", out, 1.0, -0.5), out)
 
 
-@pytest.mark.parametrize("M,N,K", [(4, 80, 400), (100, 200, 300), (300, 300, 600)])
+@pytest.mark.parametrize("M,N,K", [(4, 80, 400), (3, 50, 5000), (16, 70, 3000), (30, 90, 2500),
+                                   (100, 200, 300), (300, 300, 600), (70, 100, 4500)])
 def test_casting_on_the_way_gives_the_bits_of_the_cast(M, N, K):
     import torch
     for kind in ("f32", "bf16"):
