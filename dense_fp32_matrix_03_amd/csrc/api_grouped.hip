@@ -14,6 +14,7 @@ using sgemm_api::kMaxDim;
 using sgemm_api::kMaxWorkItems;
 
 constexpr int64_t kMaxLd = int64_t(1) << 22;   // offsets in a tile of 128 rows: below 2 GiB
+constexpr int64_t kMaxK = int64_t(1) << 30;    // rows of grouped_k: positions in K stay below 2^31
 constexpr int64_t kMaxLdc = int64_t(1) << 27;  // offsets in 8 rows of C: below 4 GiB
 
 int64_t tiles(int64_t n, int64_t t) { return (n + t - 1) / t; }
@@ -72,6 +73,7 @@ int sgemm_run_grouped_k(int64_t groups, int64_t M, int64_t N, int64_t K, float a
   if (groups > 1 && M > 0 && N > 0 && (__int128)(M - 1) * ldc + N > strideC)
     return SGEMM_ERR_INVALID_VALUE;
   if (rc != SGEMM_OK) return rc;
+  if (K > kMaxK) return SGEMM_ERR_TOO_LARGE;
   if (groups > 0 && tiles(M, 32) * tiles(N, 32) > kMaxWorkItems / 256 / groups)
     return SGEMM_ERR_TOO_LARGE;
   const bool writes = groups > 0 && M > 0 && N > 0, reads_ab = writes && K > 0 && alpha != 0.f;

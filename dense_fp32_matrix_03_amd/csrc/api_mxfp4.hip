@@ -115,7 +115,7 @@ int run(int64_t groups, int64_t M, int64_t N, int64_t K, float alpha, int typeA,
   p.N = (int)N;
   p.K = reads_ab ? (int)K : 0;
   p.groups = (int)b_groups;
-  p.alpha = alpha;
+  p.alpha = reads_ab ? alpha : 0.f;  // an empty sum is 0, whatever alpha is
   p.beta = beta;
   p.a = {static_cast<const unsigned char *>(A), static_cast<const unsigned *>(scalesA), lda};
   p.b = {static_cast<const unsigned char *>(B), static_cast<const unsigned *>(scalesB), ldsb};

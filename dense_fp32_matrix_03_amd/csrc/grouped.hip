@@ -56,6 +56,7 @@ __global__ void __launch_bounds__(kSets *kWave) grouped_kernel(GroupedArgs p, in
   const float *A = p.A + t.row0 * p.lda, *B = p.B + (long)t.g * p.strideB;
   float *C = p.C + t.row0 * p.ldc;
   const int K = p.alpha != 0.f ? p.K : 0;
+  const float alpha = K > 0 ? p.alpha : 0.f;  // an empty sum is 0, whatever alpha is
   const int m0 = t.tm * kRows, n0 = t.tn * kCols, m_end = t.rows;
 
   struct Ops {
@@ -116,7 +117,7 @@ __global__ void __launch_bounds__(kSets *kWave) grouped_kernel(GroupedArgs p, in
       const int n = TB ? n0 + 16 * j + c : n0 + 4 * c + j;
       if (n >= p.N) continue;
       float *at = C + (long)m * p.ldc + n;
-      *at = p.beta == 0.f ? p.alpha * acc[j][e] : fmaf(p.alpha, acc[j][e], p.beta * *at);
+      *at = p.beta == 0.f ? alpha * acc[j][e] : fmaf(alpha, acc[j][e], p.beta * *at);
     }
   }
 }

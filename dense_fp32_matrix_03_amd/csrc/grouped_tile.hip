@@ -87,6 +87,7 @@ grouped_tile_kernel(GroupedArgs p, int tiles_m, int tiles_n) {
     m_end = t.rows;
   }
   if (p.alpha == 0.f) K = 0;
+  const float alpha = K > 0 ? p.alpha : 0.f;  // an empty sum is 0, whatever alpha is
 
   unsigned offA[GA::NBW], offB[GB::NBW];
 #pragma unroll
@@ -276,9 +277,9 @@ grouped_tile_kernel(GroupedArgs p, int tiles_m, int tiles_n) {
               reinterpret_cast<float *>(reinterpret_cast<char *>(row + j * 32) + lane_at);
           const float v = acc[i][j][e];
           if constexpr (decltype(with_c)::value)
-            *at = fmaf(p.alpha, v, p.beta * *at);
+            *at = fmaf(alpha, v, p.beta * *at);
           else
-            __builtin_nontemporal_store(p.alpha * v, at);
+            __builtin_nontemporal_store(alpha * v, at);
         }
       }
   };

@@ -33,7 +33,7 @@
  * work-items at 256 for each 16 x 64 block (sgemm_run_grouped, counting
  * one partly filled row of blocks for each group) or 32 x 32 block
  * (sgemm_run_grouped_k) of C, lda and ldb below 2^22 where A and B are read,
- * and ldc below 2^27.
+ * ldc below 2^27, and K of sgemm_run_grouped_k at most 2^30.
  */
 #ifndef SGEMM_GROUPED_H_
 #define SGEMM_GROUPED_H_

@@ -59,7 +59,8 @@ def _grouped_k(**over):
     (dict(C=None), INVALID), (dict(offsets=None), INVALID), (dict(A=None), INVALID),
     (dict(A=None, B=None, K=0), READY), (dict(A=None, B=None, alpha=0.0), READY),
     (dict(offsets=20), INVALID), (dict(groups=4097), LARGE), (dict(lda=2 ** 22), LARGE),
-    (dict(ldc=2 ** 27, strideC=2 ** 30), LARGE),
+    (dict(ldc=2 ** 27, strideC=2 ** 30), LARGE), (dict(K=2 ** 30 + 1), LARGE),
+    (dict(K=2 ** 30), READY),
     (dict(groups=1024, M=4096, N=4096, lda=4096, ldb=4096, ldc=4096, strideC=2 ** 24), LARGE),
     (dict(groups=512, M=4096, N=4096, lda=4096, ldb=4096, ldc=4096, strideC=2 ** 24), READY),
 ])

@@ -276,6 +276,19 @@ def test_offsets_out_of_range_with_many_tiles(tb):
     assert (C[:20] == 7).all() and (C[20 + M:] == 7).all() and torch.isfinite(C).all()
 
 
+def test_empty_sums_do_not_multiply_alpha():
+    """An empty group's sum, or one over no k, is 0 even where alpha is infinite."""
+    import torch
+    at, d_at = _offsets([0, 3, 0])
+    A, B = torch.ones(3, 6, device="cuda"), torch.ones(3, 5, device="cuda")
+    D = torch.full((3, 6, 5), 2.0, device="cuda")
+    sg.sgemm_run_grouped_k(3, 6, 5, 3, float("inf"), A, 6, B, 5, 0.5, D, 5, 30, d_at)
+    assert (D[0] == 1).all() and (D[2] == 1).all() and torch.isinf(D[1]).all()
+    C = torch.full((3, 5), 2.0, device="cuda")
+    sg.sgemm_run_grouped(0, 3, 3, 5, 0, float("inf"), None, 1, None, 5, 0, 0.5, C, 5, d_at)
+    assert (C == 1).all()
+
+
 def test_rows_far_apart():
     """Offsets into A and C pass 2^31 elements: 1100 rows 2^21 floats apart."""
     import torch

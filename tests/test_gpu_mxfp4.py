@@ -258,6 +258,15 @@ def test_product_without_k(out):
     _check(*_product(40, 50, 0, "f32", out, 1.0, -0.5), out)
 
 
+def test_empty_sum_does_not_multiply_alpha():
+    import torch
+    for M in (3, 100):
+        C = torch.full((M, 5), 2.0, device="cuda")
+        sg.sgemm_run_mxfp4(M, 5, 0, float("inf"), "f32", None, 1, None, None, None, 5, 0.5, "f32",
+                           C, 5)
+        assert (C == 1).all()
+
+
 @pytest.mark.parametrize("M,N,K", [(4, 80, 400), (3, 50, 5000), (16, 70, 3000), (30, 90, 2500),
                                    (100, 200, 300), (300, 300, 600), (70, 100, 4500)])
 def test_casting_on_the_way_gives_the_bits_of_the_cast(M, N, K):
