@@ -46,12 +46,12 @@ __device__ __forceinline__ f32x4 load_some(const float *p, int n) {
 constexpr int kRows = 16, kCols = 64, kSets = 4;
 
 template <bool TB>
-__global__ void __launch_bounds__(kSets *kWave) grouped_kernel(GroupedArgs p, int tiles_n) {
+__global__ void __launch_bounds__(kSets *kWave) grouped_kernel(GroupedArgs p, GroupMap map) {
   const int lane = threadIdx.x % kWave;
   const int kq = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int c = lane % 16, h = lane / 16;
 
-  const GroupTile t = group_tile(p.offsets, p.groups, p.M, kRows, tiles_n, 8);
+  const GroupTile t = group_tile(p.offsets, p.groups, p.M, kRows, map);
   if (!t.valid) return;
   const float *A = p.A + t.row0 * p.lda, *B = p.B + (long)t.g * p.strideB;
   float *C = p.C + t.row0 * p.ldc;
@@ -145,9 +145,9 @@ hipError_t launch_grouped_rows(const GroupedArgs &p, bool tb, int cus, hipStream
   const dim3 grid((unsigned)(group_tile_rows(p.M, p.groups, kRows) * tiles_n)),
       block(kSets * kWave);
   if (tb)
-    hipLaunchKernelGGL(grouped_kernel<true>, grid, block, 0, s, p, tiles_n);
+    hipLaunchKernelGGL(grouped_kernel<true>, grid, block, 0, s, p, make_group_map(tiles_n));
   else
-    hipLaunchKernelGGL(grouped_kernel<false>, grid, block, 0, s, p, tiles_n);
+    hipLaunchKernelGGL(grouped_kernel<false>, grid, block, 0, s, p, make_group_map(tiles_n));
   return hipGetLastError();
 }
 

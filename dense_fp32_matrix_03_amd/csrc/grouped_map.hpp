@@ -17,6 +17,47 @@
 
 namespace sgemm {
 
+constexpr int kGroupRaster = 8;  // tile rows of a raster strip inside a group
+
+// What the host knows of the map: tiles across, and divisors by them.  Each
+// division in a work-group's prologue is a multiplication by a constant; the
+// compiler's sequences for three of them took 0.4 us of it.
+struct GroupMap {
+  int tiles_n;
+  FastDiv by_tiles_n, by_strip;  // strip: kGroupRaster tiles_n tiles
+};
+
+inline GroupMap make_group_map(int tiles_n) {  // host side
+  return GroupMap{tiles_n, make_fast_div(tiles_n), make_fast_div(kGroupRaster * tiles_n)};
+}
+
+// n / d for 1 <= d <= 8 and n < 2^29: with m = ceil(2^32 / d), m d exceeds 2^32
+// by less than d, so floor(n m / 2^32) is exact while n (m d - 2^32) < 2^32.
+__host__ __device__ __forceinline__ int div_up_to_8(int n, int d) {
+  const unsigned m = d == 2   ? 0x80000000u
+                     : d == 3 ? 0x55555556u
+                     : d == 4 ? 0x40000000u
+                     : d == 5 ? 0x33333334u
+                     : d == 6 ? 0x2aaaaaabu
+                     : d == 7 ? 0x24924925u
+                              : 0x20000000u;
+  return d == 1 ? n : (int)((unsigned long long)(unsigned)n * m >> 32);
+}
+
+// Tile `in` of a group with tiles_m rows of tiles: strips of kGroupRaster tile
+// rows walked column by column (TileMap's order).  False if it has no such
+// tile.
+__host__ __device__ __forceinline__ bool tile_in_group(const GroupMap &map, int in, int tiles_m,
+                                                       int &tm, int &tn) {
+  const int strip = map.by_strip(in), r = in - strip * (kGroupRaster * map.tiles_n);
+  const int left = tiles_m - strip * kGroupRaster;
+  const int high = left < kGroupRaster ? left : kGroupRaster;
+  if (high <= 0) return false;
+  tn = div_up_to_8(r, high);
+  tm = strip * kGroupRaster + (r - tn * high);
+  return tn < map.tiles_n && tm < tiles_m;
+}
+
 struct GroupTile {
   bool valid;
   int g;         // group
@@ -47,19 +88,19 @@ __device__ __forceinline__ int wave_scan(int v) {
   return v;
 }
 
-// The tile of work-group blockIdx.x: tiles of bm rows, tiles_n of them across,
-// group after group; inside a group a raster of group_m tile rows walked
-// column by column (TileMap's order).  All lanes of all waves get the same
+// The tile of work-group blockIdx.x: tiles of bm rows (a power of two), tiles_n
+// of them across, group after group, in tile_in_group's order.  All lanes of all waves get the same
 // answer.  Lane l sums `per` consecutive groups; where that is more than one,
 // the lane's groups are then told apart by a second sum over lanes.
 __device__ __forceinline__ GroupTile group_tile(const int64_t *offsets, int groups, int M, int bm,
-                                                int tiles_n, int group_m) {
+                                                const GroupMap &map) {
+  const int tiles_n = map.tiles_n;
   const int lane = threadIdx.x % kWave;
   const int per = (groups + kWave - 1) / kWave;
   auto tiles_of = [&](int g, int &first, int &last) {
     first = last = 0;
     if (g < groups) group_range(offsets, g, M, first, last);
-    return (last - first + bm - 1) / bm;
+    return (last - first + bm - 1) / bm;  // bm is a constant power of two
   };
   GroupTile t;
   t.valid = false;
@@ -75,7 +116,8 @@ __device__ __forceinline__ GroupTile group_tile(const int64_t *offsets, int grou
   const unsigned all = (unsigned)total * (unsigned)tiles_n;
   if (total <= 0 || blockIdx.x >= all) return t;
   const unsigned pos = (unsigned)xcd_contiguous_id(blockIdx.x, all);
-  const int q = (int)(pos / (unsigned)tiles_n);  // tile rows before this tile's row start
+  if (pos >= 1u << 29) return t;       // no launch has as many; keeps the divisions in range
+  const int q = map.by_tiles_n((int)pos);  // tile rows before this tile's row start
   // Offsets that decrease can make these sums meaningless: whatever group and
   // tile come out are checked against the group's own range at the end.
   unsigned long long after = __ballot(scan > q);
@@ -97,33 +139,33 @@ __device__ __forceinline__ GroupTile group_tile(const int64_t *offsets, int grou
   t.row0 = __builtin_amdgcn_readlane(first, l);
   t.rows = __builtin_amdgcn_readlane(last, l) - (int)t.row0;
   const int tiles_m = (t.rows + bm - 1) / bm;
-  const unsigned in = pos - (unsigned)before * (unsigned)tiles_n;
-  const unsigned per_raster = (unsigned)group_m * (unsigned)tiles_n;
-  const int first_row = (int)(in / per_raster) * group_m;
-  const unsigned r = in % per_raster;
-  const int high = min(group_m, tiles_m - first_row);
-  if (first_row < 0 || high <= 0) return t;
-  t.tn = (int)(r / (unsigned)high);
-  t.tm = first_row + (int)(r % (unsigned)high);
-  t.valid = t.tn < tiles_n && t.tm < tiles_m;
+  const int in = (int)(pos - (unsigned)before * (unsigned)tiles_n);
+  if (in < 0 || in >= 1 << 29) return t;
+  t.valid = tile_in_group(map, in, tiles_m, t.tm, t.tn);
   return t;
 }
 
 // The group with `rank` longer ones before it (equal ones in their order),
-// among up to 64 groups; with more groups, group `rank`.
-__device__ __forceinline__ int group_by_length(const int64_t *offsets, int groups, int M,
-                                               int rank) {
-  if (groups > kWave) return rank;
+// among up to 64 groups; with more groups, group `rank`.  And its rows.
+__device__ __forceinline__ int group_by_length(const int64_t *offsets, int groups, int M, int rank,
+                                               int &first, int &last) {
+  if (groups > kWave) {
+    group_range(offsets, rank, M, first, last);
+    return rank;
+  }
   const int lane = threadIdx.x % kWave;
-  int first = 0, last = -1;
-  if (lane < groups) group_range(offsets, lane, M, first, last);
-  const int mine = last - first;  // -1 past the last group
+  int f = 0, l = -1;
+  if (lane < groups) group_range(offsets, lane, M, f, l);
+  const int mine = l - f;  // -1 past the last group
   int before = 0;
   for (int g = 0; g < groups; ++g) {
     const int other = __builtin_amdgcn_readlane(mine, g);
     before += other > mine || (other == mine && g < lane);
   }
-  return __builtin_ctzll(__ballot(before == rank && lane < groups));
+  const int g = __builtin_ctzll(__ballot(before == rank && lane < groups));
+  first = __builtin_amdgcn_readlane(f, g);
+  last = __builtin_amdgcn_readlane(l, g);
+  return g;
 }
 
 // Tile rows that a launch must provide for M rows in `groups` groups.

@@ -25,7 +25,7 @@ namespace {
 // transposed.  VA / VB: A / B take 16-byte loads.
 template <bool KFORM, bool TB, int BM, int BN, int BK, int WM, int WN, int NST, bool VA, bool VB>
 __global__ void __launch_bounds__(WM *WN *kWave, 2)
-grouped_tile_kernel(GroupedArgs p, int tiles_m, int tiles_n) {
+grouped_tile_kernel(GroupedArgs p, GroupMap map, FastDiv by_tiles, int tiles) {
   constexpr bool TA = KFORM;
   constexpr int NW = WM * WN;
   constexpr int WTM = BM / WM, WTN = BN / WN, FM = WTM / 32, FN = WTN / 32;
@@ -59,24 +59,23 @@ grouped_tile_kernel(GroupedArgs p, int tiles_m, int tiles_n) {
   float *C = p.C;
   int m0, n0, m_end, K;
   if constexpr (KFORM) {
-    const int per = tiles_m * tiles_n;
     // Each group's tiles are spread over the XCDs (a group of tiles per XCD
     // would leave the chip waiting for the XCD of the longest one), the longest
     // groups first.
-    const int rank = blockIdx.x / per;
-    const int t = xcd_contiguous_id(blockIdx.x % per, per);
-    const int g = group_by_length(p.offsets, p.groups, p.K, rank);
+    const int rank = by_tiles((int)blockIdx.x);
+    const int t = xcd_contiguous_id((int)blockIdx.x - rank * tiles, tiles);
     int first, last;
-    group_range(p.offsets, g, p.K, first, last);
+    const int g = group_by_length(p.offsets, p.groups, p.K, rank, first, last);
     A += first * p.lda;
     B += first * p.ldb;
     C += (long)g * p.strideC;
     K = last - first;
-    m0 = t / tiles_n * BM;
-    n0 = t % tiles_n * BN;
+    const int tm = map.by_tiles_n(t);
+    m0 = tm * BM;
+    n0 = (t - tm * map.tiles_n) * BN;
     m_end = p.M;
   } else {
-    const GroupTile t = group_tile(p.offsets, p.groups, p.M, BM, tiles_n, 8);
+    const GroupTile t = group_tile(p.offsets, p.groups, p.M, BM, map);
     if (!t.valid) return;
     A += t.row0 * p.lda;
     B += (long)t.g * p.strideB;
@@ -296,8 +295,8 @@ hipError_t launch(const GroupedArgs &p, hipStream_t s) {
   const int tiles_m = (p.M + BM - 1) / BM, tiles_n = (p.N + BN - 1) / BN;
   const long rows = KFORM ? (long)tiles_m * p.groups : group_tile_rows(p.M, p.groups, BM);
   hipLaunchKernelGGL((grouped_tile_kernel<KFORM, TB, BM, BN, BK, WM, WN, NST, VA, VB>),
-                     dim3((unsigned)(rows * tiles_n)), dim3(WM * WN * kWave), 0, s, p, tiles_m,
-                     tiles_n);
+                     dim3((unsigned)(rows * tiles_n)), dim3(WM * WN * kWave), 0, s, p,
+                     make_group_map(tiles_n), make_fast_div(tiles_m * tiles_n), tiles_m * tiles_n);
   return hipGetLastError();
 }
 

@@ -36,7 +36,7 @@ constexpr int kSliceBytes = 128;  // codes of a row's slice
 // loads take to arrive: the sets walk KS chains at once.
 template <int BM, int BN, int WM, int WN, int KS, int NST, bool CBF16>
 __global__ void __launch_bounds__(WM *WN *KS *kWave, 2)
-mxfp4_tile_kernel(Mxfp4Args p, TileMap tmap, int tiles_n) {
+mxfp4_tile_kernel(Mxfp4Args p, TileMap tmap, GroupMap map) {
   constexpr int NW = WM * WN;  // waves of a set
   constexpr int WTM = BM / WM, WTN = BN / WN, FM = WTM / 32, FN = WTN / 32;
   constexpr int QA = BM * kSliceBytes / 1024 / NW, QB = BN * kSliceBytes / 1024 / NW;
@@ -81,7 +81,7 @@ mxfp4_tile_kernel(Mxfp4Args p, TileMap tmap, int tiles_n) {
   long a_row = 0, b_row = 0;  // first row of the group in A (and C), and of its B
   int m0, n0, m_end = p.M;
   if (p.offsets) {
-    const GroupTile t = group_tile(p.offsets, p.groups, p.M, BM, tiles_n, 8);
+    const GroupTile t = group_tile(p.offsets, p.groups, p.M, BM, map);
     if (!t.valid) return;
     a_row = t.row0;
     b_row = (long)t.g * p.N;
@@ -338,13 +338,14 @@ hipError_t launch(const Mxfp4Args &p, bool c_bf16, hipStream_t s) {
   const int tiles_m = (p.M + BM - 1) / BM, tiles_n = (p.N + BN - 1) / BN;
   const long rows = p.offsets ? group_tile_rows(p.M, p.groups, BM) : tiles_m;
   const dim3 grid((unsigned)(rows * tiles_n)), block(WM * WN * KS * kWave);
-  const TileMap tmap = make_tile_map(tiles_m, tiles_n, 8);
+  const TileMap tmap = make_tile_map(tiles_m, tiles_n, kGroupRaster);
+  const GroupMap map = make_group_map(tiles_n);
   if (c_bf16)
     hipLaunchKernelGGL((mxfp4_tile_kernel<BM, BN, WM, WN, KS, NST, true>), grid, block, 0, s, p, tmap,
-                       tiles_n);
+                       map);
   else
     hipLaunchKernelGGL((mxfp4_tile_kernel<BM, BN, WM, WN, KS, NST, false>), grid, block, 0, s, p, tmap,
-                       tiles_n);
+                       map);
   return hipGetLastError();
 }
 

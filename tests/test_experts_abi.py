@@ -1,6 +1,8 @@
 """Entry points for products grouped by expert and for microscaled 4-bit
 operands: argument checks, which precede any runtime call (no GPU needed)."""
-import ctypes
+import os
+import shutil
+import subprocess
 
 import pytest
 
@@ -172,17 +174,23 @@ def _ranges(offsets, M):
     return out
 
 
-def test_launched_tile_rows_cover_any_groups():
-    """sum ceil(rows / bm) <= M / bm + min(groups, M) for every way to divide
-    M rows, the bound by which the host sizes a launch."""
-    import random
-    rng = random.Random(7)
-    for _ in range(3000):
-        M, groups = rng.randrange(1, 300), rng.randrange(1, 40)
-        cuts = sorted(rng.randrange(0, M + 1) for _ in range(groups + 1))
-        for bm in (16, 32, 64, 128):
-            tiles = sum((e - s + bm - 1) // bm for s, e in _ranges(cuts, M))
-            assert tiles <= M // bm + min(groups, M)
+HERE = os.path.dirname(os.path.abspath(__file__))
+CSRC = os.path.join(os.path.dirname(HERE), "dense_fp32_matrix_03_amd", "csrc")
+HIPCC = shutil.which("hipcc") or "/opt/rocm/bin/hipcc"
+
+
+@pytest.mark.skipif(not os.path.exists(HIPCC), reason="hipcc not installed")
+def test_map_of_tiles_inside_groups(tmp_path):
+    """tests/group_map_check.cpp, compiled for the host only: every tile of a
+    group is reached once, the divisions are exact, and the launched rows of
+    tiles cover any way to divide the rows."""
+    exe = tmp_path / "group_map_check"
+    subprocess.run([HIPCC, "-std=c++17", "-O2", "--cuda-host-only", "-x", "hip", "-I", CSRC,
+                    os.path.join(HERE, "group_map_check.cpp"), "-o", str(exe)],
+                   check=True, capture_output=True, timeout=300)
+    r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr
+    assert "failures 0" in r.stdout
 
 
 def test_clamped_groups_stay_inside():
