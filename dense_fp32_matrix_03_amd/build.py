@@ -38,7 +38,7 @@ SOURCES = ["api.hip", "mfma_kernels.hip", "mfma_layout_nn.hip", "mfma_layout_nn_
            "mfma_layout_nn_phases.hip", "mfma_layout_nn_serial.hip", "mfma_small.hip",
            "mfma_staged.hip",
            "valu_kernels.hip", "vector_add.hip", "bf16x3.hip", "ceiling.hip", "noalloc.hip",
-           "api_grouped.hip", "grouped.hip", "grouped_tile.hip",
+           "api_grouped.hip", "grouped.hip",
            "api_mxfp4.hip", "mxfp4_cast.hip", "mxfp4_gemm.hip", "mxfp4_tile.hip"]
 ARCH = "gfx950"
 BUNDLE_TARGET = f"hipv4-amdgcn-amd-amdhsa--{ARCH}"

@@ -44,7 +44,7 @@ int sgemm_run_grouped(int transB, int64_t groups, int64_t M, int64_t N, int64_t 
   int rc = check(groups, M, N, K, K, lda, transB ? K : N, ldb, ldc);
   if (rc == SGEMM_ERR_INVALID_VALUE || strideB < 0) return SGEMM_ERR_INVALID_VALUE;
   if (rc != SGEMM_OK) return rc;
-  if (sgemm::group_tile_rows(M, groups, 16) > kMaxWorkItems / 256 / (N ? tiles(N, 64) : 1))
+  if (sgemm::group_tile_rows(M, groups, 32) > kMaxWorkItems / 256 / (N ? tiles(N, 32) : 1))
     return SGEMM_ERR_TOO_LARGE;
   const bool writes = groups > 0 && M > 0 && N > 0, reads_ab = writes && K > 0 && alpha != 0.f;
   if (reads_ab && (lda >= kMaxLd || ldb >= kMaxLd)) return SGEMM_ERR_TOO_LARGE;

@@ -1,154 +1,413 @@
-// grouped.hip -- single-precision products of short groups of rows
-// (include/sgemm_grouped.h), and the choice between this kernel and the tiles
-// of grouped_tile.hip.
+// grouped.hip -- single-precision products of grouped rows
+// (include/sgemm_grouped.h) whose operand slices reach LDS by buffer-to-LDS
+// loads: the pipeline, LDS images and k order of mfma_dma.hpp, with a tile's
+// operands and limits found from the group lengths on the device.
 //
-// C(r, :) = alpha sum_k A(r, k) op(B_g)(k, :) + beta C(r, :) for the rows r of
-// group g, on v_mfma_f32_16x16x4_f32.  With a few rows a group the time is that
-// of reading the B_g once.  A work-group has 16 rows by 64 columns and splits k
-// over four waves, whose sums are added in order at the end, so that even one
-// short group spreads over the chip; its operands go straight from global
-// memory into registers.
+// C(r, :) = alpha sum_k A(r, k) op(B_g)(k, :) + beta C(r, :), or C_g = alpha
+// sum_r A(r, :)^T B(r, :) + beta C_g, on v_mfma_f32_32x32x2_f32.
 //
-// K is walked in groups of 16; in one, lane quarter h supplies k = 4 h + t to
-// instruction t, so an operand whose k runs along its stored rows takes its
-// four instructions' values in one 16-byte load.  B as given takes four 16-byte
-// loads, one of each k row, and its 64 columns are dealt to the four blocks
-// in turn: block j has column 4 c + j of lane c.
-//
-// 24 rows in 16 groups by 2048 x 2048: 31.5 us, 6.4 TB/s of the weights that
-// have rows (part of them stays in the Infinity Cache between calls).
-#include <type_traits>
-
-#include "common.hpp"
+// Edges.  An element outside op(A)'s rows or op(B)'s columns is fetched at an
+// offset past the descriptor's end and reads as zero.  A partial last slice
+// of k goes first, so that the main loop's loads need no test of k: an operand
+// whose k runs along its stored rows ends at the last valid row, the other
+// one compares each load's k (with 4-byte loads where K % 4 != 0, since a
+// 16-byte one would hold values past K).
 #include "grouped.hpp"
 #include "grouped_map.hpp"
+#include "mfma_dma.hpp"
 
 namespace sgemm {
 
 namespace {
 
-// Four floats at any 4-byte aligned address.
-typedef float f32x4_u __attribute__((ext_vector_type(4), aligned(4)));
+// KFORM: groups divide k (grouped_k; A^T and B as given); otherwise they
+// divide the rows of A and C, and TB tells whether the B_g are stored
+// transposed.  VA / VB: A / B take 16-byte loads.  KS sets of WM x WN waves
+// share a tile; set q takes slices q, q + KS, .. through LDS stages of its own,
+// and the sets' sums are added in order at the end.
+template <bool KFORM, bool TB, int BM, int BN, int BK, int WM, int WN, int KS, int NST, bool VA,
+          bool VB>
+__global__ void __launch_bounds__(WM *WN *KS *kWave, 2)
+grouped_kernel(GroupedArgs p, GroupMap map, FastDiv by_tiles, int tiles) {
+  constexpr bool TA = KFORM;
+  constexpr int NW = WM * WN;  // waves of a set
+  constexpr int WTM = BM / WM, WTN = BN / WN, FM = WTM / 32, FN = WTN / 32;
+  constexpr int KH = BK / 2, G = KH / 4;
+  using GA = SliceGeom<BM, BK, TA, VA, true, NW>;
+  using GB = SliceGeom<BN, BK, !TB, VB, true, NW>;
+  static_assert(!GA::SPARE && !GB::SPARE, "loads must split evenly over the waves");
+  constexpr int kLoads = GA::NBW + GB::NBW;
 
-// The first n (0..4) of four consecutive floats, zeros for the others.
-__device__ __forceinline__ f32x4 load_some(const float *p, int n) {
-  f32x4 v = {0.f, 0.f, 0.f, 0.f};
-  if (n >= 4) {
-    v = *reinterpret_cast<const f32x4_u *>(p);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 3; ++e)
-      if (e < n) v[e] = p[e];
-  }
-  return v;
-}
+  static_assert(NST >= 2 && NST <= 4, "2 to 4 LDS stages");
+  constexpr int SA = BM * BK, SB = BK * BN;
+  __shared__ __attribute__((aligned(1024))) float As0[KS * SA], As1[KS * SA],
+      As2[NST > 2 ? KS * SA : 1], As3[NST > 3 ? KS * SA : 1];
+  __shared__ __attribute__((aligned(1024))) float Bs0[KS * SB], Bs1[KS * SB],
+      Bs2[NST > 2 ? KS * SB : 1], Bs3[NST > 3 ? KS * SB : 1];
 
-constexpr int kRows = 16, kCols = 64, kSets = 4;
-
-template <bool TB>
-__global__ void __launch_bounds__(kSets *kWave) grouped_kernel(GroupedArgs p, GroupMap map) {
   const int lane = threadIdx.x % kWave;
-  const int kq = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int c = lane % 16, h = lane / 16;
-
-  const GroupTile t = group_tile(p.offsets, p.groups, p.M, kRows, map);
-  if (!t.valid) return;
-  const float *A = p.A + t.row0 * p.lda, *B = p.B + (long)t.g * p.strideB;
-  float *C = p.C + t.row0 * p.ldc;
-  const int K = p.alpha != 0.f ? p.K : 0;
-  const float alpha = K > 0 ? p.alpha : 0.f;  // an empty sum is 0, whatever alpha is
-  const int m0 = t.tm * kRows, n0 = t.tn * kCols, m_end = t.rows;
-
-  struct Ops {
-    f32x4 a, b[4];
+  const int all_waves = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int kq = KS > 1 ? all_waves / NW : 0;
+  const int wave = KS > 1 ? all_waves % NW : all_waves;
+  const int wm = wave / WN, wn = wave % WN;
+  const int r32 = lane % 32, half = lane / 32;
+  auto stage_a = [&](auto S) -> float * {
+    constexpr int i = decltype(S)::value;
+    return (i == 0 ? As0 : i == 1 ? As1 : i == 2 ? As2 : As3) + kq * SA;
   };
-  // Rows past the end repeat the last one: what they give is not stored.
-  const float *const a_row = A + (long)min(m0 + c, m_end - 1) * p.lda;
-  auto load = [&](int k, Ops &o, auto whole) {
-    constexpr bool WHOLE = decltype(whole)::value;
-    o.a = load_some(a_row + k + 4 * h, WHOLE ? 4 : K - k - 4 * h);
+  auto stage_b = [&](auto S) -> float * {
+    constexpr int i = decltype(S)::value;
+    return (i == 0 ? Bs0 : i == 1 ? Bs1 : i == 2 ? Bs2 : Bs3) + kq * SB;
+  };
+
+  const float *A = p.A, *B = p.B;
+  float *C = p.C;
+  int m0, n0, m_end, K;
+  if constexpr (KFORM) {
+    // Each group's tiles are spread over the XCDs (a group of tiles per XCD
+    // would leave the chip waiting for the XCD of the longest one), the longest
+    // groups first.
+    const int rank = by_tiles((int)blockIdx.x);
+    const int t = xcd_contiguous_id((int)blockIdx.x - rank * tiles, tiles);
+    int first, last;
+    const int g = group_by_length(p.offsets, p.groups, p.K, rank, first, last);
+    A += first * p.lda;
+    B += first * p.ldb;
+    C += (long)g * p.strideC;
+    K = last - first;
+    const int tm = map.by_tiles_n(t);
+    m0 = tm * BM;
+    n0 = (t - tm * map.tiles_n) * BN;
+    m_end = p.M;
+  } else {
+    const GroupTile t = group_tile(p.offsets, p.groups, p.M, BM, map);
+    if (!t.valid) return;
+    A += t.row0 * p.lda;
+    B += (long)t.g * p.strideB;
+    C += t.row0 * p.ldc;
+    K = p.K;
+    m0 = t.tm * BM;
+    n0 = t.tn * BN;
+    m_end = t.rows;
+  }
+  if (p.alpha == 0.f) K = 0;
+  const float alpha = K > 0 ? p.alpha : 0.f;  // an empty sum is 0, whatever alpha is
+
+  unsigned offA[GA::NBW], offB[GB::NBW];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if constexpr (TB) {
-        const int n = min(n0 + 16 * j + c, p.N - 1), kk = k + 4 * h;
-        o.b[j] = load_some(B + (long)n * p.ldb + kk, WHOLE ? 4 : K - kk);
+  for (int q = 0; q < GA::NBW; ++q) {
+    int row, col;
+    GA::elem(wave, lane, q, row, col);
+    offA[q] = m0 + GA::mnof(row, col) < m_end ? (unsigned)(row * p.lda + col) * 4u : kOutOfRange;
+  }
+#pragma unroll
+  for (int q = 0; q < GB::NBW; ++q) {
+    int row, col;
+    GB::elem(wave, lane, q, row, col);
+    offB[q] = n0 + GB::mnof(row, col) < p.N ? (unsigned)(row * p.ldb + col) * 4u : kOutOfRange;
+  }
+  auto rsrc = [](const float *base, int records) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<float *>(base), 0, records,
+                                             kRawBufferWord3);
+  };
+  auto origin_a = [&](int k0) { return TA ? A + (long)k0 * p.lda + m0 : A + (long)m0 * p.lda + k0; };
+  auto origin_b = [&](int k0) { return TB ? B + (long)n0 * p.ldb + k0 : B + (long)k0 * p.ldb + n0; };
+
+  // Position u of the slice order: with a ragged K the partial slice first,
+  // then slice u - 1.  Positions at or past nk get descriptors without
+  // records: nothing is fetched.
+  const int nk = (K + BK - 1) / BK, ragged = K % BK != 0;
+  auto dma = [&](auto S, int u) {
+    const int records = u < nk ? kBufferRecords : 0;
+    const int k0 = u < nk ? (u - ragged) * BK : 0;
+    const __amdgpu_buffer_rsrc_t ra = rsrc(origin_a(k0), records);
+    const __amdgpu_buffer_rsrc_t rb = rsrc(origin_b(k0), records);
+#pragma unroll
+    for (int q = 0; q < GA::NBW; ++q)
+      lds_dma<VA>(ra, stage_a(S) + (wave + q * NW) * GA::FPB, offA[q]);
+#pragma unroll
+    for (int q = 0; q < GB::NBW; ++q)
+      lds_dma<VB>(rb, stage_b(S) + (wave + q * NW) * GB::FPB, offB[q]);
+  };
+  // The partial slice, kl values of k, into stage 0.
+  auto dma_tail = [&](auto geom, float *stage, const float *origin, long ld, int mn_left, int kl) {
+    using Gm = decltype(geom);
+    const __amdgpu_buffer_rsrc_t r = rsrc(origin, Gm::KR ? kl * (int)ld * 4 : kBufferRecords);
+#pragma unroll
+    for (int q = 0; q < Gm::NBW; ++q) {
+      int row, col;
+      Gm::elem(wave, lane, q, row, col);
+      const bool in = Gm::mnof(row, col) < mn_left && (Gm::KR || Gm::kof(row, col) < kl);
+      lds_dma<Gm::E == 4>(r, stage + (wave + q * NW) * Gm::FPB,
+                          in ? (unsigned)(row * ld + col) * 4u : kOutOfRange);
+    }
+  };
+
+  const int sw = kc_swizzle<BK, true>(r32);
+  int a_off[G], b_off[G];
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    a_off[g] = TA ? (half * KH + g * 4) * BM + wm * WTM + r32
+                  : (wm * WTM + r32) * BK + 4 * ((half * (KH / 4) + g) ^ sw);
+    b_off[g] = TB ? (wn * WTN + r32) * BK + 4 * ((half * (KH / 4) + g) ^ sw)
+                  : (half * KH + g * 4) * BN + wn * WTN + r32;
+  }
+  struct Ops {
+    f32x4 a[FM], b[FN];
+  };
+  auto read_ops = [&](auto S, int g, Ops &o) {
+    const float *as = stage_a(S), *bs = stage_b(S);
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      if constexpr (TA) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) o.a[i][t] = as[a_off[g] + t * BM + i * 32];
       } else {
-        const int kk = k + 4 * h + j, n = n0 + 4 * c;
-        o.b[j] = load_some(B + (long)kk * p.ldb + n, WHOLE ? 4 : (kk < K ? p.N - n : 0));
+        o.a[i] = *reinterpret_cast<const f32x4 *>(as + a_off[g] + i * 32 * BK);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      if constexpr (TB) {
+        o.b[j] = *reinterpret_cast<const f32x4 *>(bs + b_off[g] + j * 32 * BK);
+      } else {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) o.b[j][t] = bs[b_off[g] + t * BN + j * 32];
       }
     }
   };
-  f32x4 acc[4];
+  f32x16 acc[FM][FN];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const bool inside = TB || n0 + kCols <= p.N;
-  for (int k = 16 * kq; k < K; k += 16 * kSets) {
-    Ops o;
-    if (inside && k + 16 <= K)
-      load(k, o, std::true_type());
-    else
-      load(k, o, std::false_type());
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+  auto mma = [&](const Ops &o) {
 #pragma unroll
     for (int t = 0; t < 4; ++t)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        acc[j] = mfma16x16x4(o.a[t], TB ? o.b[j][t] : o.b[t][j], acc[j]);
-  }
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) acc[i][j] = mfma32x32x2(o.a[i][t], o.b[j][t], acc[i][j]);
+  };
 
-  __shared__ f32x4 red[(kSets - 1) * 4 * kWave];
-  if (kq > 0) {
+  // As in mfma_dma.hpp: one matrix-core instruction per load in the last group
+  // of a slice, then two per operand read.
+  constexpr int kMfma = 4 * FM * FN;
+  constexpr int kReads = (TA ? 2 * FM : FM) + (TB ? FN : 2 * FN);
+  auto interleave = [&](auto last) {
+    constexpr int loads = decltype(last)::value ? kLoads : 0;
+    static_for<kMfma>([&](auto I) {
+      constexpr int i = decltype(I)::value;
+      constexpr int d = kReads * (i + 1) / kMfma - kReads * i / kMfma;
+      constexpr int v = loads * (i + 1) / kMfma - loads * i / kMfma;
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      if constexpr (d > 0) __builtin_amdgcn_sched_group_barrier(0x100, d, 0);
+      if constexpr (v > 0) __builtin_amdgcn_sched_group_barrier(0x020, v, 0);
+    });
+  };
+  using S0 = std::integral_constant<int, 0>;
+  Ops cur, nxt;
+  auto slice = [&](auto S, int t) {  // the set's t-th slice
+    using SN = std::integral_constant<int, (decltype(S)::value + 1) % NST>;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) red[((kq - 1) * 4 + j) * kWave + lane] = acc[j];
-  }
-  __syncthreads();
-  if (kq > 0) return;
-#pragma unroll
-  for (int s = 0; s < kSets - 1; ++s)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[j] += red[(s * 4 + j) * kWave + lane];
-
-  // Register e of lane l holds row 4 (l / 16) + e, column l % 16 of a block.
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const int m = m0 + 4 * h + e;
-    if (m >= m_end) continue;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int n = TB ? n0 + 16 * j + c : n0 + 4 * c + j;
-      if (n >= p.N) continue;
-      float *at = C + (long)m * p.ldc + n;
-      *at = p.beta == 0.f ? alpha * acc[j][e] : fmaf(alpha, acc[j][e], p.beta * *at);
+    for (int g = 0; g < G; ++g) {
+      if (g + 1 < G) {
+        read_ops(S, g + 1, nxt);
+        mma(cur);
+        interleave(std::false_type());
+      } else {
+        dma_barrier_keep<(NST - 2) * kLoads>();
+        dma(S, kq + (t + NST) * KS);
+        read_ops(SN(), 0, nxt);
+        mma(cur);
+        interleave(std::true_type());
+      }
+      cur = nxt;
     }
+  };
+
+  if (nk > 0) {
+    const int turns = (nk + KS - 1) / KS;  // the same for all sets: they share the barriers
+    if (ragged && kq == 0) {
+      const int k0 = (nk - 1) * BK, kl = K - k0;
+      using GAn = SliceGeom<BM, BK, TA, false, true, NW>;
+      using GBn = SliceGeom<BN, BK, !TB, false, true, NW>;
+      if (!TA && K % 4 != 0)
+        dma_tail(GAn(), stage_a(S0()), origin_a(k0), p.lda, m_end - m0, kl);
+      else
+        dma_tail(GA(), stage_a(S0()), origin_a(k0), p.lda, m_end - m0, kl);
+      if (TB && K % 4 != 0)
+        dma_tail(GBn(), stage_b(S0()), origin_b(k0), p.ldb, p.N - n0, kl);
+      else
+        dma_tail(GB(), stage_b(S0()), origin_b(k0), p.ldb, p.N - n0, kl);
+    } else {
+      dma(S0(), kq);
+    }
+    static_for<NST - 1>([&](auto I) {
+      using S = std::integral_constant<int, decltype(I)::value + 1>;
+      dma(S(), kq + (decltype(I)::value + 1) * KS);
+    });
+    dma_barrier_keep<(NST - 1) * kLoads>();
+    read_ops(S0(), 0, cur);
+    for (int t = 0; t < turns; t += NST) {
+      static_for<NST>([&](auto S) {
+        if (decltype(S)::value == 0 || t + decltype(S)::value < turns)
+          slice(S, t + decltype(S)::value);
+      });
+    }
+    // The last slices sent loads past K (no memory traffic): let them retire
+    // before the work-group gives up its LDS.
+    __builtin_amdgcn_s_waitcnt(0x0f70);
   }
+
+  if constexpr (KS > 1) {
+    // The stages are free: every load has landed, every operand has been read.
+    // Set s > 0 leaves its sums in As0, those that do not fit there in Bs0.
+    constexpr int kSums = NW * FM * FN * 16 * kWave, kInA = KS * SA / kSums;
+    static_assert(kInA + KS * SB / kSums >= KS - 1, "the sets' sums fit the first stages");
+    __syncthreads();
+    auto sums = [&](int set, int i, int j) {
+      float *const at = set - 1 < kInA ? As0 + (set - 1) * kSums : Bs0 + (set - 1 - kInA) * kSums;
+      return at + ((wave * FM + i) * FN + j) * 16 * kWave + lane;
+    };
+    if (kq > 0) {
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) sums(kq, i, j)[e * kWave] = acc[i][j][e];
+    }
+    __syncthreads();
+    if (kq > 0) return;
+#pragma unroll
+    for (int set = 1; set < KS; ++set)
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) acc[i][j][e] += sums(set, i, j)[e * kWave];
+  }
+
+  // Register e of lane l holds row acc32_row(l, e), column l % 32 of a block:
+  // row 4 (l / 32) of a uniform base and a constant number of rows past it.
+  const bool full = m0 + BM <= m_end && n0 + BN <= p.N;
+  const int mw = m0 + wm * WTM, nw = n0 + wn * WTN;
+  float *const origin = C + (long)mw * p.ldc + nw;
+  const unsigned lane_at = (unsigned)(4 * half * p.ldc + r32) * 4u;
+  const int rows = m_end - mw - 4 * half, cols = p.N - nw - r32;
+  auto store = [&](auto whole, auto with_c) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int r = i * 32 + 8 * (e >> 2) + (e & 3);
+        float *const row = origin + r * p.ldc;
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+          if (!decltype(whole)::value && (r >= rows || j * 32 >= cols)) continue;
+          float *const at =
+              reinterpret_cast<float *>(reinterpret_cast<char *>(row + j * 32) + lane_at);
+          const float v = acc[i][j][e];
+          if constexpr (decltype(with_c)::value)
+            *at = fmaf(alpha, v, p.beta * *at);
+          else
+            __builtin_nontemporal_store(alpha * v, at);
+        }
+      }
+  };
+  if (p.beta != 0.f)
+    store(std::false_type(), std::true_type());
+  else if (full)
+    store(std::true_type(), std::false_type());
+  else
+    store(std::false_type(), std::false_type());
+}
+
+template <bool KFORM, bool TB, int BM, int BN, int BK, int WM, int WN, int KS, bool VA, bool VB>
+hipError_t launch(const GroupedArgs &p, hipStream_t s) {
+  const int tiles_m = (p.M + BM - 1) / BM, tiles_n = (p.N + BN - 1) / BN;
+  const long rows = KFORM ? (long)tiles_m * p.groups : group_tile_rows(p.M, p.groups, BM);
+  hipLaunchKernelGGL((grouped_kernel<KFORM, TB, BM, BN, BK, WM, WN, KS, 2, VA, VB>),
+                     dim3((unsigned)(rows * tiles_n)), dim3(WM * WN * KS * kWave), 0, s, p,
+                     make_group_map(tiles_n), make_fast_div(tiles_m * tiles_n), tiles_m * tiles_n);
+  return hipGetLastError();
+}
+
+// B as given is read along n: 16-byte loads need N to be a multiple of 4.
+template <int BM, int BN, int BK, int WM, int WN, int KS>
+hipError_t launch_rows(const GroupedArgs &p, bool tb, hipStream_t s) {
+  if (tb) return launch<false, true, BM, BN, BK, WM, WN, KS, true, true>(p, s);
+  if (p.N % 4 == 0) return launch<false, false, BM, BN, BK, WM, WN, KS, true, true>(p, s);
+  return launch<false, false, BM, BN, BK, WM, WN, KS, true, false>(p, s);
+}
+
+// Both operands of grouped_k are read along their rows.
+template <int BM, int BN, int WM, int WN, int KS>
+hipError_t launch_k(const GroupedArgs &p, hipStream_t s) {
+  const bool va = p.M % 4 == 0, vb = p.N % 4 == 0;
+  if (va && vb) return launch<true, false, BM, BN, 32, WM, WN, KS, true, true>(p, s);
+  if (va) return launch<true, false, BM, BN, 32, WM, WN, KS, true, false>(p, s);
+  if (vb) return launch<true, false, BM, BN, 32, WM, WN, KS, false, true>(p, s);
+  return launch<true, false, BM, BN, 32, WM, WN, KS, false, false>(p, s);
 }
 
 }  // namespace
 
-// This kernel or a tile of 32 x 128 through LDS, whichever the rounds of
-// work-groups on the compute units make faster.  A round of the tile takes as
-// long as 2.4 rounds of this kernel, 1.6 where B is transposed or its loads are
-// narrow.  Measured, this kernel first: 1 group of 64 rows by 4096 x 4096 42 us
-// and 75; 16 groups, 24 rows by 2048 x 2048 31.5 and 42.5, 512 rows 61 and 67,
-// 1024 rows 108 and 102; 64 groups, 2048 rows by 1024 x 1024 63 and 45; B
-// transposed 16 groups, 384 rows by 2048 x 2048 96 and 79.  The host knows the
-// number of tiles to within the groups' lengths.
+// Four tiles; `small` is the number of 32 x 32 ones, as far as the host knows
+// it (to within the groups' lengths).
+//  - 32 x 32, 4 sets of waves over k in slices of 32: where few work-groups
+//    each have a long sum, latency bounds them, and more waves on a sum hide it.
+//  - the same in slices of 16 for groups of less than 16 rows: reading B bounds
+//    them, and 32 KiB of LDS for 64 let twice as many work-groups read.
+//  - 32 x 64, 2 sets: groups that would leave much of a 64-row tile empty, and
+//    products whose 64 x 64 tiles would be few.
+//  - 64 x 64: the least LDS traffic per product of the four.
+// Measured in that order (us; B as given, groups of unequal length):
+//    1 group of 1 row by 8192 x 8192       49   59   80    -
+//    1 of 64 by 4096 x 4096                27   31   42    -
+//    16 groups, 24 rows by 2048 x 2048     41   33   39    -
+//    16 groups, 512 rows by 2048 x 2048    62   62   53    -
+//    4 groups, 1024 rows by 512 x 4096     55    -   66   72
+//    4 groups, 2048 rows by 1024 x 1024    50    -   44   49
+//    8 groups, 4096 rows by 1024 x 2048   164    -  146  151
+//    8 groups, 8192 rows by 2048 x 1024   337    -  272  260
 hipError_t launch_grouped_rows(const GroupedArgs &p, bool tb, int cus, hipStream_t s) {
-  const long groups = p.groups < p.M ? p.groups : p.M;
-  auto rounds = [&](long bm, long bn) {
-    const long most = p.M / bm + groups / 2;
-    return ((most > groups ? most : groups) * ((p.N + bn - 1) / bn) + cus - 1) / cus;
-  };
-  const double per_round = tb || p.N % 4 != 0 ? 0.625 : 0.42;
-  if (rounds(kRows, kCols) * per_round > rounds(32, 128))
-    return launch_grouped_tile(p, tb, cus, s);
-  const int tiles_n = (p.N + kCols - 1) / kCols;
-  const dim3 grid((unsigned)(group_tile_rows(p.M, p.groups, kRows) * tiles_n)),
-      block(kSets * kWave);
-  if (tb)
-    hipLaunchKernelGGL(grouped_kernel<true>, grid, block, 0, s, p, make_group_map(tiles_n));
-  else
-    hipLaunchKernelGGL(grouped_kernel<false>, grid, block, 0, s, p, make_group_map(tiles_n));
-  return hipGetLastError();
+  const long groups = p.groups < p.M ? p.groups : p.M, most = p.M / 32 + groups / 2;
+  const long small = (most > groups ? most : groups) * ((p.N + 31) / 32);
+  const long mean = p.M / p.groups;
+  if (small <= cus || (mean >= 16 && 2 * small <= 5L * cus))
+    return launch_rows<32, 32, 32, 1, 1, 4>(p, tb, s);
+  if (mean < 16) return launch_rows<32, 32, 16, 1, 1, 4>(p, tb, s);
+  if (mean < 192 || small < 12L * cus) return launch_rows<32, 64, 32, 1, 2, 2>(p, tb, s);
+  return launch_rows<64, 64, 32, 2, 2, 1>(p, tb, s);
+}
+
+// Tiles of 128 x 128 where they give every compute unit at least 4 and pad C
+// by at most 1/16 more than 64 x 128 does; else 64 x 128 where those give every
+// compute unit 4; else 64 x 64, but 32 x 32 with 4 sets of waves over the rows
+// where that leaves compute units without a tile and the groups are long.
+// Measured in that order (us):
+//    8 groups of 512 rows by 2048 x 2048        246   253    -     -
+//    8 groups of 1024 rows by 1024 x 2048       252   258  263   390
+//    8 groups, 4096 rows by 1024 x 1024          89    74   70   123
+//    32 groups, 1500 rows by 257 x 1000          27    23   25   100
+//    12 groups, 4096 rows by 512 x 1024           -    56   41    76
+//    8 groups, 1024 rows by 256 x 512             -    15    9    11
+//    3 groups, 4096 rows by 512 x 512             -    84   50    25
+//    1 group of 16384 rows by 64 x 64             -   473  268    73
+hipError_t launch_grouped_k(const GroupedArgs &p, int cus, hipStream_t s) {
+  const long m128 = (p.M + 127) / 128, m64 = (p.M + 63) / 64;
+  const long n128 = (p.N + 127) / 128, n64 = (p.N + 63) / 64;
+  if (p.M % 4 == 0 && p.N % 4 == 0 && m128 * n128 * p.groups >= 4L * cus &&
+      16 * 2 * m128 <= 17 * m64)
+    return launch<true, false, 128, 128, 32, 4, 2, 1, true, true>(p, s);
+  if (m64 * n128 * p.groups >= 4L * cus) return launch_k<64, 128, 2, 2, 1>(p, s);
+  if (m64 * n64 * p.groups > cus || p.K < 192L * p.groups) return launch_k<64, 64, 2, 2, 1>(p, s);
+  return launch_k<32, 32, 1, 1, 4>(p, s);
 }
 
 }  // namespace sgemm

@@ -19,11 +19,8 @@ struct GroupedArgs {
   const int64_t *offsets;  // device: groups + 1 values
 };
 
-// Rows of C by group: C(r, :) = alpha A(r, :) op(B_g) + beta C(r, :), on the
-// kernel for short groups or on a tile through LDS.
+// Rows of C by group: C(r, :) = alpha A(r, :) op(B_g) + beta C(r, :).
 hipError_t launch_grouped_rows(const GroupedArgs &p, bool tb, int cus, hipStream_t s);
-
-hipError_t launch_grouped_tile(const GroupedArgs &p, bool tb, int cus, hipStream_t s);
 
 // C_g = alpha A_g^T B_g + beta C_g over the rows (k) of group g.
 hipError_t launch_grouped_k(const GroupedArgs &p, int cus, hipStream_t s);

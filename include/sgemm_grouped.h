@@ -30,10 +30,10 @@
  * (SGEMM_ERR_INVALID_VALUE).  The calls allocate nothing, use no workspace
  * and are asynchronous on `stream`.  Limits (SGEMM_ERR_TOO_LARGE): sizes
  * below 2^31, groups <= SGEMM_GROUPED_MAX_GROUPS, one launch below 2^32
- * work-items at 256 for each 16 x 64 block (sgemm_run_grouped, counting
- * one partly filled row of blocks for each group) or 32 x 32 block
- * (sgemm_run_grouped_k) of C, lda and ldb below 2^22 where A and B are read,
- * ldc below 2^27, and K of sgemm_run_grouped_k at most 2^30.
+ * work-items at 256 for each 32 x 32 block of C (sgemm_run_grouped counts
+ * one partly filled row of blocks for each group), lda and ldb below 2^22
+ * where A and B are read, ldc below 2^27, and K of sgemm_run_grouped_k at
+ * most 2^30.
  */
 #ifndef SGEMM_GROUPED_H_
 #define SGEMM_GROUPED_H_

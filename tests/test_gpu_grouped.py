@@ -170,6 +170,25 @@ def test_rows_of_many_tiles_exact_on_integers(groups, N, tb):
     assert np.array_equal(C, ref)
 
 
+@pytest.mark.parametrize("tb", [0, 1])
+@pytest.mark.parametrize("groups", ["one group", "several tiles", "two hundred", "short groups"])
+@pytest.mark.parametrize("K", [15, 16, 17, 31, 32, 33, 63, 64, 65, 96, 127, 128, 129, 255, 257,
+                               384, 385])
+def test_rows_around_whole_turns_of_the_sets(groups, K, tb):
+    """Sets of waves take slices of k in turn: a last turn of 1 to all of them,
+    whole and partial slices."""
+    _check(*_run_rows(groups, 1001 if groups == "short groups" else 90, K, tb))
+
+
+@pytest.mark.parametrize("tb", [0, 1])
+@pytest.mark.parametrize("groups,N", [("one group", 256), ("several tiles", 255),
+                                      ("two hundred", 300)])
+@pytest.mark.parametrize("K,alpha,beta,pads,shift", [
+    (4100, 1.0, 0.0, (0, 0, 0), 0), (2047, -0.5, 2.0, (1, 3, 2), 1), (1030, 1.0, 1.0, (2, 2, 0), 2)])
+def test_rows_of_long_sums(groups, N, tb, K, alpha, beta, pads, shift):
+    _check(*_run_rows(groups, N, K, tb, alpha, beta, pads, shift))
+
+
 def _run_k(groups, M, N, alpha=1.0, beta=0.0, pads=(0, 0, 0), shift=0, dist="uniform", seed=0):
     import torch
     lengths, before, after = GROUPS_AND_LARGE[groups]
@@ -234,9 +253,27 @@ def test_k_of_many_tiles(groups, M, N, alpha, beta, pads, shift):
     _check(*_run_k(groups, M, N, alpha, beta, pads, shift))
 
 
-def test_k_of_many_tiles_exact_on_integers():
-    C, ref, _ = _run_k("short groups", 500, 520, dist="int8range")
+@pytest.mark.parametrize("M,N", [(500, 520), (600, 640)])
+def test_k_of_many_tiles_exact_on_integers(M, N):
+    C, ref, _ = _run_k("short groups", M, N, dist="int8range")
     assert np.array_equal(C, ref)
+
+
+@pytest.mark.parametrize("groups", ["long groups", "very long groups"])
+@pytest.mark.parametrize("M,N", [(64, 64), (1, 1), (33, 45), (130, 68), (36, 131)])
+@pytest.mark.parametrize("alpha,beta,pads,shift", [(1.0, 0.0, (0, 0, 0), 0), (0.5, 2.0, (1, 3, 2), 1)])
+def test_k_of_few_tiles_and_long_groups(groups, M, N, alpha, beta, pads, shift):
+    _check(*_run_k(groups, M, N, alpha, beta, pads, shift))
+
+
+def test_k_of_few_tiles_exact_on_integers():
+    C, ref, _ = _run_k("long groups", 70, 45, dist="int8range")
+    assert np.array_equal(C, ref)
+
+
+@pytest.mark.parametrize("alpha,beta,pads,shift", [(1.0, 0.0, (0, 0, 0), 0), (0.5, 2.0, (4, 3, 2), 1)])
+def test_k_of_large_tiles(alpha, beta, pads, shift):
+    _check(*_run_k("short groups", 600, 640, alpha, beta, pads, shift))
 
 
 @pytest.mark.parametrize("at", [[0, 40, 20, 50], [-7, 10, 60, 90], [50, 0, 50, 0],
