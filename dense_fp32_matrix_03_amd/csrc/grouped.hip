@@ -11,7 +11,14 @@
 // of k goes first, so that the main loop's loads need no test of k: an operand
 // whose k runs along its stored rows ends at the last valid row, the other
 // one compares each load's k (with 4-byte loads where K % 4 != 0, since a
-// 16-byte one would hold values past K).
+// 16-byte one would hold values past K).  An operand with k down its columns
+// and a width w that is no multiple of 4 has 16-byte loads whose last elements
+// lie up to 3 past the width: they belong to rows or columns of the product
+// that are not stored.  Such a load of row r reaches element 2 of row r + 1 at
+// most (element 1 where w = 2), inside the operand for all rows but the last;
+// so the last slice, partial or not, goes first with 4-byte loads.  (Width 1
+// takes 4-byte loads throughout.)  63 groups, 3351 rows by 913 x 896: 110 us
+// with 4-byte loads throughout, 102 so (tiles of 64 x 128, slices of 32).
 #include "grouped.hpp"
 #include "grouped_map.hpp"
 #include "mfma_dma.hpp"
@@ -113,10 +120,11 @@ grouped_kernel(GroupedArgs p, GroupMap map, FastDiv by_tiles, int tiles) {
   auto origin_a = [&](int k0) { return TA ? A + (long)k0 * p.lda + m0 : A + (long)m0 * p.lda + k0; };
   auto origin_b = [&](int k0) { return TB ? B + (long)n0 * p.ldb + k0 : B + (long)k0 * p.ldb + n0; };
 
-  // Position u of the slice order: with a ragged K the partial slice first,
+  // Position u of the slice order: with a ragged K or edge the last slice first,
   // then slice u - 1.  Positions at or past nk get descriptors without
   // records: nothing is fetched.
-  const int nk = (K + BK - 1) / BK, ragged = K % BK != 0;
+  const bool wide_edge = (TA && VA && p.M % 4 != 0) || (!TB && VB && p.N % 4 != 0);
+  const int nk = (K + BK - 1) / BK, ragged = K % BK != 0 || wide_edge;
   auto dma = [&](auto S, int u) {
     const int records = u < nk ? kBufferRecords : 0;
     const int k0 = u < nk ? (u - ragged) * BK : 0;
@@ -129,7 +137,7 @@ grouped_kernel(GroupedArgs p, GroupMap map, FastDiv by_tiles, int tiles) {
     for (int q = 0; q < GB::NBW; ++q)
       lds_dma<VB>(rb, stage_b(S) + (wave + q * NW) * GB::FPB, offB[q]);
   };
-  // The partial slice, kl values of k, into stage 0.
+  // The last slice, kl values of k, into stage 0.
   auto dma_tail = [&](auto geom, float *stage, const float *origin, long ld, int mn_left, int kl) {
     using Gm = decltype(geom);
     const __amdgpu_buffer_rsrc_t r = rsrc(origin, Gm::KR ? kl * (int)ld * 4 : kBufferRecords);
@@ -234,11 +242,11 @@ grouped_kernel(GroupedArgs p, GroupMap map, FastDiv by_tiles, int tiles) {
       const int k0 = (nk - 1) * BK, kl = K - k0;
       using GAn = SliceGeom<BM, BK, TA, false, true, NW>;
       using GBn = SliceGeom<BN, BK, !TB, false, true, NW>;
-      if (!TA && K % 4 != 0)
+      if (TA ? p.M % 4 != 0 : K % 4 != 0)
         dma_tail(GAn(), stage_a(S0()), origin_a(k0), p.lda, m_end - m0, kl);
       else
         dma_tail(GA(), stage_a(S0()), origin_a(k0), p.lda, m_end - m0, kl);
-      if (TB && K % 4 != 0)
+      if (TB ? K % 4 != 0 : p.N % 4 != 0)
         dma_tail(GBn(), stage_b(S0()), origin_b(k0), p.ldb, p.N - n0, kl);
       else
         dma_tail(GB(), stage_b(S0()), origin_b(k0), p.ldb, p.N - n0, kl);
@@ -337,22 +345,17 @@ hipError_t launch(const GroupedArgs &p, hipStream_t s) {
   return hipGetLastError();
 }
 
-// B as given is read along n: 16-byte loads need N to be a multiple of 4.
 template <int BM, int BN, int BK, int WM, int WN, int KS>
 hipError_t launch_rows(const GroupedArgs &p, bool tb, hipStream_t s) {
   if (tb) return launch<false, true, BM, BN, BK, WM, WN, KS, true, true>(p, s);
-  if (p.N % 4 == 0) return launch<false, false, BM, BN, BK, WM, WN, KS, true, true>(p, s);
-  return launch<false, false, BM, BN, BK, WM, WN, KS, true, false>(p, s);
+  if (p.N > 1) return launch<false, false, BM, BN, BK, WM, WN, KS, true, true>(p, s);
+  return launch<false, false, 32, 32, 32, 1, 1, 4, true, false>(p, s);
 }
 
-// Both operands of grouped_k are read along their rows.
-template <int BM, int BN, int WM, int WN, int KS>
+template <int BM, int BN, int BK, int WM, int WN, int KS>
 hipError_t launch_k(const GroupedArgs &p, hipStream_t s) {
-  const bool va = p.M % 4 == 0, vb = p.N % 4 == 0;
-  if (va && vb) return launch<true, false, BM, BN, 32, WM, WN, KS, true, true>(p, s);
-  if (va) return launch<true, false, BM, BN, 32, WM, WN, KS, true, false>(p, s);
-  if (vb) return launch<true, false, BM, BN, 32, WM, WN, KS, false, true>(p, s);
-  return launch<true, false, BM, BN, 32, WM, WN, KS, false, false>(p, s);
+  if (p.M > 1 && p.N > 1) return launch<true, false, BM, BN, BK, WM, WN, KS, true, true>(p, s);
+  return launch<true, false, 32, 32, 32, 1, 1, 4, false, false>(p, s);
 }
 
 }  // namespace
@@ -386,28 +389,24 @@ hipError_t launch_grouped_rows(const GroupedArgs &p, bool tb, int cus, hipStream
   return launch_rows<64, 64, 32, 2, 2, 1>(p, tb, s);
 }
 
-// Tiles of 128 x 128 where they give every compute unit at least 4 and pad C
-// by at most 1/16 more than 64 x 128 does; else 64 x 128 where those give every
-// compute unit 4; else 64 x 64, but 32 x 32 with 4 sets of waves over the rows
-// where that leaves compute units without a tile and the groups are long.
-// Measured in that order (us):
-//    8 groups of 512 rows by 2048 x 2048        246   253    -     -
-//    8 groups of 1024 rows by 1024 x 2048       252   258  263   390
-//    8 groups, 4096 rows by 1024 x 1024          89    74   70   123
-//    32 groups, 1500 rows by 257 x 1000          27    23   25   100
-//    12 groups, 4096 rows by 512 x 1024           -    56   41    76
-//    8 groups, 1024 rows by 256 x 512             -    15    9    11
-//    3 groups, 4096 rows by 512 x 512             -    84   50    25
-//    1 group of 16384 rows by 64 x 64             -   473  268    73
+// Tiles of 64 x 128 in slices of 16 rows (24 KiB of LDS: six work-groups of a
+// compute unit hide each other's start and end, and groups are padded less)
+// where there are 4 for every compute unit; else 64 x 64, but 32 x 32 with 4
+// sets of waves over the rows where those leave compute units without a tile
+// and the groups are long.  Measured in that order (us):
+//    8 groups, 8192 rows by 1024 x 2048         245   258   396
+//    63 groups, 3351 rows by 913 x 896           71    99   384
+//    32 groups, 1500 rows by 257 x 1000          19    22    77
+//    12 groups, 4096 rows by 512 x 1024          53    40    76
+//    8 groups, 1024 rows by 256 x 512            15     9    11
+//    3 groups, 4096 rows by 512 x 512            84    50    25
+//    1 group of 16384 rows by 64 x 64           473   268    73
 hipError_t launch_grouped_k(const GroupedArgs &p, int cus, hipStream_t s) {
-  const long m128 = (p.M + 127) / 128, m64 = (p.M + 63) / 64;
-  const long n128 = (p.N + 127) / 128, n64 = (p.N + 63) / 64;
-  if (p.M % 4 == 0 && p.N % 4 == 0 && m128 * n128 * p.groups >= 4L * cus &&
-      16 * 2 * m128 <= 17 * m64)
-    return launch<true, false, 128, 128, 32, 4, 2, 1, true, true>(p, s);
-  if (m64 * n128 * p.groups >= 4L * cus) return launch_k<64, 128, 2, 2, 1>(p, s);
-  if (m64 * n64 * p.groups > cus || p.K < 192L * p.groups) return launch_k<64, 64, 2, 2, 1>(p, s);
-  return launch_k<32, 32, 1, 1, 4>(p, s);
+  const long m64 = (p.M + 63) / 64, n128 = (p.N + 127) / 128, n64 = (p.N + 63) / 64;
+  if (m64 * n128 * p.groups >= 4L * cus) return launch_k<64, 128, 16, 2, 2, 1>(p, s);
+  if (2 * m64 * n64 * p.groups > 3L * cus || p.K < 192L * p.groups)
+    return launch_k<64, 64, 32, 2, 2, 1>(p, s);
+  return launch_k<32, 32, 32, 1, 1, 4>(p, s);
 }
 
 }  // namespace sgemm

@@ -153,15 +153,20 @@ __device__ __forceinline__ int group_by_length(const int64_t *offsets, int group
     return rank;
   }
   const int lane = threadIdx.x % kWave;
-  int f = 0, l = -1;
+  int f = 0, l = 0;
   if (lane < groups) group_range(offsets, lane, M, f, l);
-  const int mine = l - f;  // -1 past the last group
-  int before = 0;
-  for (int g = 0; g < groups; ++g) {
-    const int other = __builtin_amdgcn_readlane(mine, g);
-    before += other > mine || (other == mine && g < lane);
+  // Bit by bit from the highest: the lanes of `same` agree with the group sought
+  // in the bits seen so far.
+  unsigned long long same = __ballot(lane < groups);
+  for (int bit = 31 - __builtin_clz(M | 1); bit >= 0; --bit) {
+    const unsigned long long ones = same & __ballot(((l - f) >> bit & 1) != 0);
+    const int longer = __builtin_popcountll(ones);
+    same = rank < longer ? ones : same & ~ones;
+    rank = rank < longer ? rank : rank - longer;
   }
-  const int g = __builtin_ctzll(__ballot(before == rank && lane < groups));
+  const int at = __builtin_amdgcn_mbcnt_hi((unsigned)(same >> 32),
+                                           __builtin_amdgcn_mbcnt_lo((unsigned)same, 0));
+  const int g = __builtin_ctzll(same & __ballot(at == rank));
   first = __builtin_amdgcn_readlane(f, g);
   last = __builtin_amdgcn_readlane(l, g);
   return g;

@@ -189,6 +189,14 @@ def test_rows_of_long_sums(groups, N, tb, K, alpha, beta, pads, shift):
     _check(*_run_rows(groups, N, K, tb, alpha, beta, pads, shift))
 
 
+@pytest.mark.parametrize("N", [1, 2, 3, 5, 6, 7, 9, 34, 63])
+@pytest.mark.parametrize("K", [1, 31, 32, 64, 65, 300])
+@pytest.mark.parametrize("groups", ["rows outside", "two hundred", "long groups"])
+def test_rows_of_widths_that_are_no_multiple_of_four(groups, N, K):
+    """The last row of each B_g is the end of its buffer (no padding)."""
+    _check(*_run_rows(groups, N, K, 0))
+
+
 def _run_k(groups, M, N, alpha=1.0, beta=0.0, pads=(0, 0, 0), shift=0, dist="uniform", seed=0):
     import torch
     lengths, before, after = GROUPS_AND_LARGE[groups]
@@ -264,6 +272,14 @@ def test_k_of_many_tiles_exact_on_integers(M, N):
 @pytest.mark.parametrize("alpha,beta,pads,shift", [(1.0, 0.0, (0, 0, 0), 0), (0.5, 2.0, (1, 3, 2), 1)])
 def test_k_of_few_tiles_and_long_groups(groups, M, N, alpha, beta, pads, shift):
     _check(*_run_k(groups, M, N, alpha, beta, pads, shift))
+
+
+@pytest.mark.parametrize("M,N", [(1, 5), (5, 1), (2, 2), (3, 3), (5, 6), (7, 9), (34, 65), (1, 64),
+                                 (64, 1), (2, 68), (66, 4)])
+@pytest.mark.parametrize("groups", ["one row", "one group", "empty ones", "rows outside",
+                                    "long groups"])
+def test_k_of_widths_that_are_no_multiple_of_four(groups, M, N):
+    _check(*_run_k(groups, M, N))
 
 
 def test_k_of_few_tiles_exact_on_integers():
