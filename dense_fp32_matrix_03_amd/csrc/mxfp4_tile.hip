@@ -368,9 +368,10 @@ hipError_t launch(const Mxfp4Args &p, bool c_bf16, hipStream_t s) {
 // 42 / 39 / 64, 1024 74 / 47 / 64, 8192 464 / 346 / 289; 2048 x 4096 x 4096
 // 39 / 24 / 33; 16 groups, 8192 rows by 2048 x 2048 53 / 43 / 46.  Groups of up
 // to 64 rows are bound by reading B, which the smallest tile does best: 32
-// groups, 48 rows by 4096 x 2048 27 / 31 / 42.  Two sets of waves on the 64 x
-// 64 tile take 19 us instead of 25 for 128 x 8192 x 8192 (24 for 27 at M =
-// 256), and nothing less where K is 2048 or tiles are many.
+// groups, 48 rows by 4096 x 2048 27 / 31 / 42.  Sets of waves on the 64 x 64
+// tile, 1 / 2 / 4 of them: 128 x 8192 x 8192 17.5 / 14.7 / 13.2 us, 64 x 4096 x
+// 14336 21.7 / 17.9 / 15.6, 117 x 1785 x 5632 8.5 / 8.4 / 9.1; 256 x 8192 x 8192
+// 27 / 24, with four one work-group fills a compute unit.
 hipError_t launch_mxfp4_tile(const Mxfp4Args &p, bool c_bf16, int cus, hipStream_t s) {
   const long groups = !p.offsets ? 1 : p.groups < p.M ? p.groups : p.M;
   const double mean = (double)p.M / groups;
@@ -382,7 +383,8 @@ hipError_t launch_mxfp4_tile(const Mxfp4Args &p, bool c_bf16, int cus, hipStream
   const double c64 = n64 == 1 ? 0.35 : n64 == 2 ? 0.42 : 0.16 * n64;
   const double c128 = n128 == 1 ? 0.65 : n128 == 2 ? 0.77 : 0.29 * n128;
   if ((p.offsets && mean <= 64) || (c64 <= c128 && c64 <= per_cu(256))) {
-    if (n64 <= 2 && p.K >= 4096) return launch<64, 64, 2, 2, 2, 2>(p, c_bf16, s);
+    if (n64 == 1 && p.K >= 6144) return launch<64, 64, 2, 2, 4, 2>(p, c_bf16, s);
+    if (n64 == 2 && p.K >= 6144) return launch<64, 64, 2, 2, 2, 2>(p, c_bf16, s);
     return launch<64, 64, 2, 2, 1, 2>(p, c_bf16, s);
   }
   return c128 <= per_cu(256) ? launch<128, 128, 2, 2, 1, 2>(p, c_bf16, s)

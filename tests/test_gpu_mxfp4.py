@@ -216,6 +216,46 @@ def test_product_of_many_tiles(K, kind, out, alpha, beta):
     _check(*_product(4120, 3990, K, kind, out, alpha, beta, pads=(3, 2, 1)), out)
 
 
+@pytest.mark.parametrize("M,N,K", [(65, 130, 8320), (40, 129, 6150), (250, 8190, 6150),
+                                   (33, 300, 20000)])
+@pytest.mark.parametrize("kind,out,alpha,beta", [("f32", "f32", 1.0, 0.0), ("mxfp4", "bf16", 0.5, 2.0)])
+def test_product_of_few_tiles_and_long_sums(M, N, K, kind, out, alpha, beta):
+    _check(*_product(M, N, K, kind, out, alpha, beta, pads=(1, 2, 3)), out)
+
+
+@pytest.mark.parametrize("rows", [3, 90])
+def test_rows_of_b_past_four_gigabytes(rows):
+    """Two groups' B of 2.5 GB each: all zero but for the last rows of either."""
+    import torch
+    N, K, some = 150000, 32768, 40
+    g = np.random.default_rng(rows)
+    codes = torch.zeros(2 * N * (K // 2), dtype=torch.uint8, device="cuda").view(2 * N, K // 2)
+    scales = torch.zeros(K // 128, 2 * N, 4, dtype=torch.uint8, device="cuda")
+    pb, sb = mx.quantize(_values(rows, (2 * some, K)))
+    pa, sa = mx.quantize(_values(rows + 1, (rows, K)))
+    for n in (0, 1):
+        end = (n + 1) * N
+        codes[end - some:end] = _cuda(pb[n * some:(n + 1) * some])
+        scales[:, end - some:end] = _cuda(np.ascontiguousarray(sb[:, n * some:(n + 1) * some]))
+    at = np.array([0, rows // 3, rows], np.int64)
+    C = torch.full((rows, N), 7.0, device="cuda")
+    sg.sgemm_run_mxfp4_grouped(2, rows, N, K, 1.0, "mxfp4", _cuda(pa), rows, _cuda(sa), codes,
+                               scales, 2 * N, 0.0, "f32", C, N, _cuda(at))
+    assert (C[:, :N - some] == 0).all()
+    a, b = mx.values(pa, sa, K), mx.values(pb, sb, K)
+    for n in (0, 1):
+        i, j, bn = at[n], at[n + 1], b[n * some:(n + 1) * some]
+        _check(C[i:j, N - some:].cpu().numpy(), a[i:j] @ bn.T, np.abs(a[i:j]) @ np.abs(bn).T, "f32")
+    # both groups' rows as one matrix, by the kernel for few rows
+    few = min(rows, 20)
+    D = torch.full((few, 2 * N), 7.0, device="cuda")
+    sg.sgemm_run_mxfp4(few, 2 * N - 1, K, 1.0, "mxfp4", _cuda(pa), rows, _cuda(sa), codes, scales,
+                       2 * N, 0.0, "f32", D, 2 * N)
+    assert (D[:, 2 * N - 1] == 7).all() and (D[:, N:2 * N - some] == 0).all()
+    _check(D[:, 2 * N - some:2 * N - 1].cpu().numpy(), a[:few] @ b[some:2 * some - 1].T,
+           np.abs(a[:few]) @ np.abs(b[some:2 * some - 1]).T, "f32")
+
+
 def test_product_exact_on_many_tiles():
     """Values of the format itself under one scale: every sum is exact."""
     import torch
