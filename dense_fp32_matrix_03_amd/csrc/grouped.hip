@@ -367,10 +367,7 @@ hipError_t launch_k(const GroupedArgs &p, hipStream_t s) {
 //  - the same in slices of 16 for groups of less than 16 rows: reading B bounds
 //    them, and 32 KiB of LDS for 64 let twice as many work-groups read.
 //  - 32 x 64, 2 sets: groups that would leave much of a 64-row tile empty, and
-//    products whose 64 x 64 tiles would be few.  In slices of 16 where k is
-//    short, for the work-groups that then share a compute unit: 27 groups, 1536
-//    rows by 2341 x 225 26 us against 31, 64 groups, 4099 rows by 1000 x 777 75
-//    against 80; 16 groups, 512 rows by 2048 x 2048 56 against 53.
+//    products whose 64 x 64 tiles would be few.
 //  - 64 x 64: the least LDS traffic per product of the four.
 // Measured in that order (us; B as given, groups of unequal length):
 //    1 group of 1 row by 8192 x 8192       49   59   80    -
@@ -388,9 +385,7 @@ hipError_t launch_grouped_rows(const GroupedArgs &p, bool tb, int cus, hipStream
   if (small <= cus || (mean >= 16 && 2 * small <= 5L * cus))
     return launch_rows<32, 32, 32, 1, 1, 4>(p, tb, s);
   if (mean < 16) return launch_rows<32, 32, 16, 1, 1, 4>(p, tb, s);
-  if (mean < 192 || small < 12L * cus)
-    return p.K <= 1024 ? launch_rows<32, 64, 16, 1, 2, 2>(p, tb, s)
-                       : launch_rows<32, 64, 32, 1, 2, 2>(p, tb, s);
+  if (mean < 192 || small < 12L * cus) return launch_rows<32, 64, 32, 1, 2, 2>(p, tb, s);
   return launch_rows<64, 64, 32, 2, 2, 1>(p, tb, s);
 }
 
