@@ -364,27 +364,31 @@ hipError_t launch_k(const GroupedArgs &p, hipStream_t s) {
 // it (to within the groups' lengths).
 //  - 32 x 32, 4 sets of waves over k in slices of 32: where few work-groups
 //    each have a long sum, latency bounds them, and more waves on a sum hide it.
-//  - the same in slices of 16 for groups of less than 16 rows: reading B bounds
-//    them, and 32 KiB of LDS for 64 let twice as many work-groups read.
+//  - the same in slices of 16 for groups of a few rows, some of them empty:
+//    reading B bounds them, and 32 KiB of LDS for 64 let twice as many
+//    work-groups read.
 //  - 32 x 64, 2 sets: groups that would leave much of a 64-row tile empty, and
 //    products whose 64 x 64 tiles would be few.
 //  - 64 x 64: the least LDS traffic per product of the four.
-// Measured in that order (us; B as given, groups of unequal length):
-//    1 group of 1 row by 8192 x 8192       49   59   80    -
-//    1 of 64 by 4096 x 4096                27   31   42    -
-//    16 groups, 24 rows by 2048 x 2048     41   33   39    -
-//    16 groups, 512 rows by 2048 x 2048    62   62   53    -
-//    4 groups, 1024 rows by 512 x 4096     55    -   66   72
-//    4 groups, 2048 rows by 1024 x 1024    50    -   44   49
-//    8 groups, 4096 rows by 1024 x 2048   164    -  146  151
-//    8 groups, 8192 rows by 2048 x 1024   337    -  272  260
+// Measured in that order (us; B as given and not in the caches, groups of
+// unequal length):
+//    1 group of 1 row by 8192 x 8192       66   89  110  189
+//    1 of 64 by 4096 x 4096                34   45   56   96
+//    16 groups, 24 rows by 2048 x 2048     50   39   44   74
+//    32 groups, 24 rows by 1024 x 2048     42   34   42   73
+//    64 groups, 512 rows by 1024 x 1024    62   56   61   70
+//    16 groups, 128 rows by 2048 x 2048    52   54   44   75
+//    16 groups, 512 rows by 2048 x 2048    78   80   62  103
+//    4 groups, 200 rows by 2000 x 4000     51   54   60  100
+//    8 groups, 2048 rows by 2048 x 1024   105   85   81   92
+//    8 groups, 8192 rows by 2048 x 1024   357  302  273  258
 hipError_t launch_grouped_rows(const GroupedArgs &p, bool tb, int cus, hipStream_t s) {
   const long groups = p.groups < p.M ? p.groups : p.M, most = p.M / 32 + groups / 2;
   const long small = (most > groups ? most : groups) * ((p.N + 31) / 32);
   const long mean = p.M / p.groups;
-  if (small <= cus || (mean >= 16 && 2 * small <= 5L * cus))
+  if (small <= cus || (mean >= 8 && 2 * small <= 5L * cus))
     return launch_rows<32, 32, 32, 1, 1, 4>(p, tb, s);
-  if (mean < 16) return launch_rows<32, 32, 16, 1, 1, 4>(p, tb, s);
+  if (mean < 8 || (mean < 16 && small > 6L * cus)) return launch_rows<32, 32, 16, 1, 1, 4>(p, tb, s);
   if (mean < 192 || small < 12L * cus) return launch_rows<32, 64, 32, 1, 2, 2>(p, tb, s);
   return launch_rows<64, 64, 32, 2, 2, 1>(p, tb, s);
 }

@@ -182,7 +182,8 @@ def test_rows_around_whole_turns_of_the_sets(groups, K, tb):
 
 @pytest.mark.parametrize("tb", [0, 1])
 @pytest.mark.parametrize("groups,N", [("one group", 256), ("several tiles", 255),
-                                      ("two hundred", 300)])
+                                      ("two hundred", 300), ("short groups", 1001),
+                                      ("long groups", 1032)])
 @pytest.mark.parametrize("K,alpha,beta,pads,shift", [
     (4100, 1.0, 0.0, (0, 0, 0), 0), (2047, -0.5, 2.0, (1, 3, 2), 1), (1030, 1.0, 1.0, (2, 2, 0), 2)])
 def test_rows_of_long_sums(groups, N, tb, K, alpha, beta, pads, shift):
