@@ -3,7 +3,8 @@
     python bench.py [--gpus 1] [--steps K] [--warmup W] [--workload NAME]
                     [--variant V] [--no-cpu-baseline] [--no-secondary]
     python bench.py --table | --general | --small | --shards | --ladder
-                    | --vector-add | --bf16x3 | --bf16x3-general | --copy-calibration
+                    | --vector-add | --bf16x3 | --bf16x3-general | --experts
+                    | --copy-calibration
 
 One step is one call of sgemm_run on the 8192^3 workload (uniform[-1, 1)
 inputs from seed 4, already resident in HBM).  W untimed calls, then exactly
@@ -17,8 +18,9 @@ times (--table), the general form and strided batches (--general), small
 products with sgemm_run's tile and every forced tile (--small), one
 GPU's share of 8192^3 split by rows over 1-8 GPUs (--shards), the pages'
 progression (--ladder), the vector add (--vector-add), the bfloat16 split
-path (--bf16x3, --bf16x3-general), and the copy that calibrates the HBM
-counters (--copy-calibration).
+path (--bf16x3, --bf16x3-general), products of grouped rows and of 4-bit
+operands (--experts), and the copy that calibrates the HBM counters
+(--copy-calibration).
 
 The CPU baseline is the oracle (double-precision triple loop) timed on the
 host cores on a bounded sample of the same workload: the first R rows of C,
@@ -457,6 +459,51 @@ def general_table(settle: float) -> list[dict]:
         print(json.dumps(r), flush=True)
         rows.append(r)
         del dA, dB, dC
+        torch.cuda.empty_cache()
+    return rows
+
+
+def experts_table(settle: float) -> list[dict]:
+    """Time the calls of perf/operators.py's cases (products of grouped rows,
+    casts to 4-bit floats and products of them), one JSON line each.  Several
+    sets of operands are used in turn, more of them than the caches hold."""
+    import importlib.util
+
+    import torch
+
+    spec = importlib.util.spec_from_file_location("operators",
+                                                  os.path.join(ROOT, "perf", "operators.py"))
+    ops = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ops)
+    ops.own = True
+    rows = []
+    stream = torch.cuda.current_stream()
+    for case in ops.listed():
+        need = ops.work(case)
+        sets = [ops.prepare(case, i) for i in range(max(2, min(8, int(8e8 / need["bytes"]) + 1)))]
+        for st in sets:
+            ops.run(st)
+        torch.cuda.synchronize()
+        steps, t_end = 0, time.perf_counter() + settle
+        while time.perf_counter() < t_end or steps < 20:
+            for st in sets:
+                ops.run(st)
+            torch.cuda.synchronize()
+            steps += len(sets)
+        steps = max(20, min(400, steps)) // len(sets) * len(sets)
+        t0 = torch.cuda.Event(enable_timing=True)
+        t1 = torch.cuda.Event(enable_timing=True)
+        t0.record(stream)
+        for i in range(steps):
+            ops.run(sets[i % len(sets)])
+        t1.record(stream)
+        torch.cuda.synchronize()
+        us = t0.elapsed_time(t1) / steps * 1e3
+        r = {"case": case["name"], "us": round(us, 2), "gb_per_s": round(need["bytes"] / us / 1e3),
+             "tflops": round(need["flops"] / us / 1e6, 2)}
+        print(json.dumps(r), flush=True)
+        rows.append(r)
+        del sets, st
         torch.cuda.empty_cache()
     return rows
 
@@ -922,6 +969,9 @@ def main(argv=None) -> int:
     ap.add_argument("--bf16x3-general", action="store_true",
                     help="time sgemm_run_bf16x3_ex (stored transposes; alpha/beta) at "
                          "2048^3 and 8192^3, one JSON line each")
+    ap.add_argument("--experts", action="store_true",
+                    help="time products of grouped rows, casts to 4-bit floats and products of "
+                         "them on the cases of perf/operators.py, one JSON line each")
     ap.add_argument("--kscan", action="store_true",
                     help="time sgemm_run at M = N = 256 and 1024 over K = 32 .. 4096, two "
                          "floor cases and the five workloads, one JSON line each (with the "
@@ -986,6 +1036,10 @@ def main(argv=None) -> int:
         return 0
     if a.bf16x3 or a.bf16x3_general:
         bf16x3_table(a.steps, a.warmup, a.settle, general=a.bf16x3_general)
+        sg.sgemm_destroy()
+        return 0
+    if a.experts:
+        experts_table(a.settle)
         sg.sgemm_destroy()
         return 0
     if a.vector_add:
