@@ -21,7 +21,8 @@ namespace {
 constexpr int kGranule = 128;
 constexpr int kRowsPerGroup = 32;  // rows of a work-group, not transposed
 
-// One granule of 32 rows per work-group of 4 waves: 16 lanes a row.
+// One granule of 32 rows per work-group of 4 waves: 16 lanes a row.  8192 x
+// 8192: 53 us from single precision (5.7 TB/s), 30 from bfloat16 (5.7).
 template <bool BF16>
 __global__ void __launch_bounds__(256) quantize_kernel(CastArgs p) {
   const int tid = threadIdx.x;
@@ -35,7 +36,7 @@ __global__ void __launch_bounds__(256) quantize_kernel(CastArgs p) {
     const bool in = row < p.rows;
     float v[8];
     const char *x = static_cast<const char *>(p.X) + ((long)row * p.ldx + k) * (BF16 ? 2 : 4);
-    load8<BF16>(x, in ? left : 0, v);
+    load8<BF16, true>(x, in ? left : 0, v);
     unsigned all;
     const unsigned codes = mxfp4_cast8(v, tid, all);
     if (in) {
@@ -91,11 +92,12 @@ __device__ __forceinline__ float scale_value(unsigned s) {
   return __uint_as_float(s == 255u ? 0x7fc00000u : (s ? s << 23 : 0x00400000u));
 }
 
-// The eight values of a dword of codes.
-__device__ __forceinline__ void decode8(unsigned codes, float scale, float v[8]) {
+// The first N (at most 8) values of a dword of codes.
+template <int N = 8>
+__device__ __forceinline__ void decode(unsigned codes, float scale, float v[N]) {
   constexpr unsigned kGrid = 0xc8643210u;  // twice the magnitudes 0, .5, 1, 1.5, 2, 3, 4, 6
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
+  for (int e = 0; e < N; ++e) {
     const unsigned c = codes >> (4 * e) & 15u;
     const float m = 0.5f * (float)(kGrid >> (4 * (c & 7u)) & 15u);
     v[e] = (c & 8u ? -m : m) * scale;
@@ -107,52 +109,51 @@ __device__ __forceinline__ unsigned short to_bf16(float x) {
   return __builtin_bit_cast(unsigned short, (__bf16)x);
 }
 
-// The first n (at most 8) of eight values to consecutive elements.
-template <bool BF16>
-__device__ __forceinline__ void store8(void *x, int n, const float v[8]) {
-  if constexpr (BF16) {
-    unsigned short *p = static_cast<unsigned short *>(x);
-    if (n >= 8) {
-      u32x4_any t;
+// The first n (at most 16 bytes) of a lane's values to consecutive elements.
+__device__ __forceinline__ void store(unsigned short *x, int n, const float v[8]) {
+  if (n >= 8) {
+    u32x4_any t;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) t[e] = to_bf16(v[2 * e]) | (unsigned)to_bf16(v[2 * e + 1]) << 16;
-      *reinterpret_cast<u32x4_any *>(p) = t;
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (e < n) p[e] = to_bf16(v[e]);
-    }
+    for (int e = 0; e < 4; ++e) t[e] = to_bf16(v[2 * e]) | (unsigned)to_bf16(v[2 * e + 1]) << 16;
+    __builtin_nontemporal_store(t, reinterpret_cast<u32x4_any *>(x));
   } else {
-    float *p = static_cast<float *>(x);
-    if (n >= 8) {
-      *reinterpret_cast<f32x4_any *>(p) = f32x4{v[0], v[1], v[2], v[3]};
-      *reinterpret_cast<f32x4_any *>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
-    } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (e < n) p[e] = v[e];
-    }
+    for (int e = 0; e < 8; ++e)
+      if (e < n) x[e] = to_bf16(v[e]);
+  }
+}
+__device__ __forceinline__ void store(float *x, int n, const float v[4]) {
+  if (n >= 4) {
+    const f32x4_any t = {v[0], v[1], v[2], v[3]};
+    __builtin_nontemporal_store(t, reinterpret_cast<f32x4_any *>(x));
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < n) x[e] = v[e];
   }
 }
 
+// A granule of 32 rows per work-group; a lane writes 16 bytes, so that a wave's
+// store is of whole rows of the granule.  8192 x 8192: 30 us to bfloat16 (5.6
+// TB/s), 51 to single precision (5.9); 80 with eight floats a lane in two stores.
 template <bool BF16>
 __global__ void __launch_bounds__(256) dequantize_kernel(CastArgs p) {
-  const int tid = threadIdx.x;
+  using T = std::conditional_t<BF16, unsigned short, float>;
+  using Codes = std::conditional_t<BF16, unsigned, unsigned short>;
+  constexpr int V = 16 / sizeof(T), kLanes = kGranule / V, kPass = 256 / kLanes;
   const int g = blockIdx.x % p.granules, tile = blockIdx.x / p.granules;
-  const int l16 = tid % 16;
-  const int k = g * kGranule + l16 * 8;
+  const int l = threadIdx.x % kLanes;
+  const int k = g * kGranule + l * V;
 #pragma unroll
-  for (int i = 0; i < kRowsPerGroup / 16; ++i) {
-    const int row = tile * kRowsPerGroup + i * 16 + tid / 16;
+  for (int i = 0; i < kRowsPerGroup / kPass; ++i) {
+    const int row = tile * kRowsPerGroup + i * kPass + threadIdx.x / kLanes;
     if (row >= p.rows) break;
     const unsigned codes =
-        reinterpret_cast<const unsigned *>(p.codes)[(long)row * (p.granules * 16) + g * 16 + l16];
-    const unsigned s = p.scales[(long)g * p.lds + row] >> (8 * (l16 / 4)) & 255u;
-    float v[8];
-    decode8(codes, scale_value(s), v);
-    char *x = static_cast<char *>(const_cast<void *>(p.X)) +
-              ((long)row * p.ldx + k) * (BF16 ? 2 : 4);
-    store8<BF16>(x, p.K - k, v);
+        static_cast<const Codes *>(p.codes)[((long)row * p.granules + g) * kLanes + l];
+    const unsigned s = p.scales[(long)g * p.lds + row] >> (8 * (l * V / 32)) & 255u;
+    float v[V];
+    decode<V>(codes, scale_value(s), v);
+    store(static_cast<T *>(const_cast<void *>(p.X)) + (long)row * p.ldx + k, p.K - k, v);
   }
 }
 
@@ -166,10 +167,10 @@ __global__ void __launch_bounds__(256) dequantize_transposed_kernel(CastArgs p) 
   const uint4 c = reinterpret_cast<const uint4 *>(p.codes)[(long)row * (p.granules * 4) + g * 4 + w];
   const float scale = scale_value(p.scales[(long)g * p.lds + row] >> (8 * w) & 255u);
   float v[32];
-  decode8(c.x, scale, v);
-  decode8(c.y, scale, v + 8);
-  decode8(c.z, scale, v + 16);
-  decode8(c.w, scale, v + 24);
+  decode(c.x, scale, v);
+  decode(c.y, scale, v + 8);
+  decode(c.z, scale, v + 16);
+  decode(c.w, scale, v + 24);
 #pragma unroll
   for (int e = 0; e < 32; ++e) {
     if (k0 + e >= p.K) break;
