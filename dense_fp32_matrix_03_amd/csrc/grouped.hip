@@ -6,6 +6,12 @@
 // C(r, :) = alpha sum_k A(r, k) op(B_g)(k, :) + beta C(r, :), or C_g = alpha
 // sum_r A(r, :)^T B(r, :) + beta C_g, on v_mfma_f32_32x32x2_f32.
 //
+// Long groups are bound by the matrix cores (8 groups, 8192 rows by 2048 x 1024
+// 133 TFLOP/s, the same rows as k of 1024 x 2048 138, the pipes 87-89% busy),
+// short ones by reading B (16 groups, 24 rows by 2048 x 2048 5.2 TB/s), and
+// what lies between by the rows that tiles pad to (64 groups of 64 rows on
+// average by 1000 x 777 67 TFLOP/s, 80 with the padding).
+//
 // Edges.  An element outside op(A)'s rows or op(B)'s columns is fetched at an
 // offset past the descriptor's end and reads as zero.  A partial last slice
 // of k goes first, so that the main loop's loads need no test of k: an operand

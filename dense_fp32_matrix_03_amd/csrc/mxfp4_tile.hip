@@ -13,6 +13,13 @@
 // LDS image is [row][8 chunks of 16 bytes], chunk c at c ^ kc_swizzle
 // (mfma_dma.hpp), the scales' [granule][row].
 //
+// 8192^3 with bfloat16 C takes 260-290 us, 3.8-4.2 PFLOP/s at an engine clock of
+// 1.85-2.1 GHz.  The main loop runs at 5 PFLOP/s, what the 4-bit instructions
+// alone sustain on such data (5.0-5.8, at 1.5 GHz: power decides); the rest
+// is the burst of C's stores, in which the matrix cores idle.  Smaller products
+// are bound by the first loads and the stores of a tile, and short groups by
+// reading B (32 groups, 48 rows by 4096 x 2048 4.1 TB/s).
+//
 // Edges.  The descriptors end at the last row's last byte, so rows past it
 // read as zeros.  Where K ends inside a slice the second granule's codes are
 // whatever follows in memory, below that end (every code is finite), but both
