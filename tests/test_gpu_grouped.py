@@ -495,3 +495,93 @@ def test_on_another_stream():
         a, b = A[at[n]:at[n + 1]].astype(np.float64), B[n].astype(np.float64)
         if len(a):
             _check(C.cpu().numpy()[at[n]:at[n + 1]], a @ b, np.abs(a) @ np.abs(b))
+
+
+@pytest.mark.parametrize("tb", [0, 1])
+@pytest.mark.parametrize("K,N,lengths", [(50, 45, [17, 20, 33]), (1100, 34, [40, 1, 90]),
+                                         (33, 1001, [700, 350, 900])])
+def test_what_is_not_finite_stays_in_its_row(K, N, lengths, tb):
+    """One row of A is NaN and one B_g infinite: the other groups' rows, and the
+    NaN row's neighbours, are what they are without them."""
+    import torch
+    at, d_at = _offsets(lengths)
+    M, G = int(at[-1]), len(lengths)
+    g = np.random.default_rng(K + N)
+    A, B = inputs.uniform(g, (M, K)), inputs.uniform(g, (G, N, K) if tb else (G, K, N))
+    out = []
+    for spoilt in (False, True):
+        if spoilt:
+            A[at[1]] = np.nan        # the first row of the second group
+            B[2] = np.inf
+        C = torch.full((M, N), 3.0, device="cuda")
+        sg.sgemm_run_grouped(tb, G, M, N, K, 1.0, _dev(A), K, _dev(B), K if tb else N, K * N, 0.0,
+                             C, N, d_at)
+        out.append(C.cpu().numpy())
+    same = np.ones(M, bool)
+    same[at[1]] = same[at[2]:] = False
+    assert np.array_equal(out[0][same], out[1][same])
+    assert np.isnan(out[1][at[1]]).all() and not np.isfinite(out[1][at[2]:]).any()
+
+
+@pytest.mark.parametrize("M,N,lengths", [(37, 45, [17, 20, 33]), (64, 130, [300, 500, 700]),
+                                         (601, 999, [30, 2, 64] + [9] * 20)])
+def test_what_is_not_finite_stays_in_its_group(M, N, lengths):
+    import torch
+    at, d_at = _offsets(lengths)
+    K, G = int(at[-1]), len(lengths)
+    g = np.random.default_rng(M + N)
+    A, B = inputs.uniform(g, (K, M)), inputs.uniform(g, (K, N))
+    out = []
+    for spoilt in (False, True):
+        if spoilt:
+            A[at[1]:at[2]] = np.nan
+            B[at[1]:at[2]] = np.inf
+        C = torch.full((G, M, N), 3.0, device="cuda")
+        sg.sgemm_run_grouped_k(G, M, N, K, 1.0, _dev(A), M, _dev(B), N, 0.0, C, N, M * N, d_at)
+        out.append(C.cpu().numpy())
+    others = [n for n in range(G) if n != 1]
+    assert np.array_equal(out[0][others], out[1][others]) and np.isnan(out[1][1]).all()
+
+
+def test_the_most_groups():
+    """4096 groups, most of them empty or of one row; the last one long."""
+    import torch
+    lengths = [(n * 7) % 3 // 2 for n in range(4095)] + [300]
+    at, d_at = _offsets(lengths)
+    M, G, K, N = int(at[-1]), 4096, 24, 20
+    g = np.random.default_rng(2)
+    A, B = inputs.uniform(g, (M, K)), inputs.uniform(g, (G, K, N))
+    E = inputs.uniform(g, (M, N))
+    C, D = torch.empty(M, N, device="cuda"), torch.empty(G, K, N, device="cuda")
+    sg.sgemm_run_grouped(0, G, M, N, K, 1.0, _dev(A), K, _dev(B), N, K * N, 0.0, C, N, d_at)
+    sg.sgemm_run_grouped_k(G, K, N, M, 1.0, _dev(A), K, _dev(E), N, 0.0, D, N, K * N, d_at)
+    of = np.repeat(np.arange(G), lengths)
+    a, b, e = A.astype(np.float64), B.astype(np.float64)[of], E.astype(np.float64)
+    _check(C.cpu().numpy(), np.einsum("mk,mkn->mn", a, b),
+           np.einsum("mk,mkn->mn", np.abs(a), np.abs(b)))
+    ref, mag = np.zeros((G, K, N)), np.zeros((G, K, N))
+    np.add.at(ref, of, a[:, :, None] * e[:, None, :])
+    np.add.at(mag, of, np.abs(a[:, :, None] * e[:, None, :]))
+    _check(D.cpu().numpy(), ref, mag)
+
+
+def test_two_streams_at_once():
+    """Two calls in flight share nothing."""
+    import torch
+    G, M, N, K = 6, 900, 500, 400
+    g = np.random.default_rng(4)
+    at, d_at = _offsets([100, 250, 0, 300, 50, 200])
+    A = [_dev(inputs.uniform(g, (M, K))) for _ in range(2)]
+    B = [_dev(inputs.uniform(g, (G, K, N))) for _ in range(2)]
+    C = [torch.zeros(M, N, device="cuda") for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(8):
+        for i in range(2):
+            sg.sgemm_run_grouped(0, G, M, N, K, 1.0, A[i], K, B[i], N, K * N, 0.0, C[i], N, d_at,
+                                 stream=streams[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        alone = torch.zeros(M, N, device="cuda")
+        sg.sgemm_run_grouped(0, G, M, N, K, 1.0, A[i], K, B[i], N, K * N, 0.0, alone, N, d_at)
+        assert torch.equal(alone, C[i])

@@ -521,3 +521,34 @@ def test_an_expert_layer_with_4_bit_weights():
         if j > i:
             _check(hidden[i:j], 0.1 * (xv[i:j] @ b1), 0.1 * (np.abs(xv[i:j]) @ np.abs(b1)), "bf16")
             _check(y.cpu().numpy()[i:j], hv[i:j] @ b2, np.abs(hv[i:j]) @ np.abs(b2), "f32")
+
+
+def test_two_streams_with_a_workspace_each():
+    import torch
+    M, N, K = 70, 520, 900
+    w = torch.randn(N, K, device="cuda")
+    codes = torch.empty(N, mx.padded(K) // 2, dtype=torch.uint8, device="cuda")
+    scales = torch.empty(mx.padded(K) // 128, N, 4, dtype=torch.uint8, device="cuda")
+    sg.sgemm_mxfp4_quantize(0, N, K, "f32", w, K, codes, scales, N)
+    X = [torch.randn(M, K, device="cuda") for _ in range(2)]
+    C = [torch.zeros(M, N, device="cuda") for _ in range(2)]
+    n = sg.sgemm_mxfp4_workspace_size("f32", M, K)
+    ws = [torch.empty(n, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(8):
+        for i in range(2):
+            sg.sgemm_run_mxfp4(M, N, K, 1.0, "f32", X[i], K, None, codes, scales, N, 0.0, "f32",
+                               C[i], N, ws[i], n, stream=streams[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        alone = torch.zeros(M, N, device="cuda")
+        sg.sgemm_run_mxfp4(M, N, K, 1.0, "f32", X[i], K, None, codes, scales, N, 0.0, "f32", alone,
+                           N, ws[0], n)
+        assert torch.equal(alone, C[i])
+
+
+def test_the_most_groups():
+    lengths = [n % 5 // 4 for n in range(4095)] + [200]
+    for kind, out in (("f32", "f32"), ("mxfp4", "bf16")):
+        _check(*_product(sum(lengths), 33, 150, kind, out, lengths=lengths), out)
