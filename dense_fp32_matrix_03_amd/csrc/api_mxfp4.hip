@@ -125,7 +125,7 @@ int run(int64_t groups, int64_t M, int64_t N, int64_t K, float alpha, int typeA,
   hipError_t err = hipSuccess;
   int a_type = SGEMM_TYPE_MXFP4;
   if (reads_ab && !held) {
-    if (sgemm::mxfp4_casts(p)) {
+    if (sgemm::mxfp4_casts(p, cus)) {
       a_type = typeA;
     } else {
       unsigned char *codes = static_cast<unsigned char *>(workspace);

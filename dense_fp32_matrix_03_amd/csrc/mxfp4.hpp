@@ -45,7 +45,7 @@ struct Mxfp4Args {
 
 // Whether the product's kernel is to cast A itself: only then may a_type below
 // be other than SGEMM_TYPE_MXFP4.
-bool mxfp4_casts(const Mxfp4Args &p);
+bool mxfp4_casts(const Mxfp4Args &p, int cus);
 // Picks the kernel for the product.
 hipError_t launch_mxfp4_product(const Mxfp4Args &p, int a_type, bool c_bf16, int cus,
                                 hipStream_t s);

@@ -223,6 +223,27 @@ def test_product_of_few_tiles_and_long_sums(M, N, K, kind, out, alpha, beta):
     _check(*_product(M, N, K, kind, out, alpha, beta, pads=(1, 2, 3)), out)
 
 
+SPREAD = {"one each": [1, 0, 0, 2, 1, 0, 0, 1], "two tiles in one": [18] + [0] * 15,
+          "all in the last": [0] * 7 + [13], "seventy": [(n * 3) % 4 // 3 for n in range(70)],
+          "none": [0, 0]}
+
+
+@pytest.mark.parametrize("groups", SPREAD)
+@pytest.mark.parametrize("N,K", [(1, 32), (33, 129), (150, 700), (40, 2050)])
+@pytest.mark.parametrize("kind,out", [("f32", "f32"), ("bf16", "bf16"), ("mxfp4", "f32")])
+def test_grouped_rows_spread_thin(groups, N, K, kind, out):
+    _check(*_product(sum(SPREAD[groups]) + 3, N, K, kind, out, lengths=SPREAD[groups], before=1), out)
+
+
+@pytest.mark.parametrize("kind", ["f32", "mxfp4"])
+@pytest.mark.parametrize("alpha,beta,pads,shift", [(0.5, 2.0, (1, 2, 3), 1), (1.0, 1.0, (0, 0, 1), 0),
+                                                   (0.0, 0.5, (0, 0, 0), 0)])
+def test_grouped_rows_spread_thin_strides_alpha_beta(kind, alpha, beta, pads, shift):
+    lengths = SPREAD["one each"]
+    _check(*_product(sum(lengths), 75, 600, kind, "f32", alpha, beta, pads, shift, lengths=lengths),
+           "f32")
+
+
 @pytest.mark.parametrize("rows", [3, 90])
 def test_rows_of_b_past_four_gigabytes(rows):
     """Two groups' B of 2.5 GB each: all zero but for the last rows of either."""
