@@ -37,9 +37,10 @@ namespace {
 // divide the rows of A and C, and TB tells whether the B_g are stored
 // transposed.  VA / VB: A / B take 16-byte loads.  KS sets of WM x WN waves
 // share a tile; set q takes slices q, q + KS, .. through LDS stages of its own,
-// and the sets' sums are added in order at the end.
+// and the sets' sums are added in order at the end.  STREAM: stores of C are
+// non-temporal.
 template <bool KFORM, bool TB, int BM, int BN, int BK, int WM, int WN, int KS, int NST, bool VA,
-          bool VB>
+          bool VB, bool STREAM>
 __global__ void __launch_bounds__(WM *WN *KS *kWave, 2)
 grouped_kernel(GroupedArgs p, GroupMap map, FastDiv by_tiles, int tiles) {
   constexpr bool TA = KFORM;
@@ -328,8 +329,10 @@ grouped_kernel(GroupedArgs p, GroupMap map, FastDiv by_tiles, int tiles) {
           const float v = acc[i][j][e];
           if constexpr (decltype(with_c)::value)
             *at = fmaf(alpha, v, p.beta * *at);
-          else
+          else if constexpr (STREAM)
             __builtin_nontemporal_store(alpha * v, at);
+          else
+            *at = alpha * v;
         }
       }
   };
@@ -341,11 +344,12 @@ grouped_kernel(GroupedArgs p, GroupMap map, FastDiv by_tiles, int tiles) {
     store(std::false_type(), std::false_type());
 }
 
-template <bool KFORM, bool TB, int BM, int BN, int BK, int WM, int WN, int KS, bool VA, bool VB>
+template <bool KFORM, bool TB, int BM, int BN, int BK, int WM, int WN, int KS, bool VA, bool VB,
+          bool STREAM = true>
 hipError_t launch(const GroupedArgs &p, hipStream_t s) {
   const int tiles_m = (p.M + BM - 1) / BM, tiles_n = (p.N + BN - 1) / BN;
   const long rows = KFORM ? (long)tiles_m * p.groups : group_tile_rows(p.M, p.groups, BM);
-  hipLaunchKernelGGL((grouped_kernel<KFORM, TB, BM, BN, BK, WM, WN, KS, 2, VA, VB>),
+  hipLaunchKernelGGL((grouped_kernel<KFORM, TB, BM, BN, BK, WM, WN, KS, 2, VA, VB, STREAM>),
                      dim3((unsigned)(rows * tiles_n)), dim3(WM * WN * KS * kWave), 0, s, p,
                      make_group_map(tiles_n), make_fast_div(tiles_m * tiles_n), tiles_m * tiles_n);
   return hipGetLastError();
@@ -358,9 +362,10 @@ hipError_t launch_rows(const GroupedArgs &p, bool tb, hipStream_t s) {
   return launch<false, false, 32, 32, 32, 1, 1, 4, true, false>(p, s);
 }
 
-template <int BM, int BN, int BK, int WM, int WN, int KS>
+template <int BM, int BN, int BK, int WM, int WN, int KS, bool STREAM = true>
 hipError_t launch_k(const GroupedArgs &p, hipStream_t s) {
-  if (p.M > 1 && p.N > 1) return launch<true, false, BM, BN, BK, WM, WN, KS, true, true>(p, s);
+  if (p.M > 1 && p.N > 1)
+    return launch<true, false, BM, BN, BK, WM, WN, KS, true, true, STREAM>(p, s);
   return launch<true, false, 32, 32, 32, 1, 1, 4, false, false>(p, s);
 }
 
@@ -413,7 +418,14 @@ hipError_t launch_grouped_rows(const GroupedArgs &p, bool tb, int cus, hipStream
 //    1 group of 16384 rows by 64 x 64           473   268    73
 hipError_t launch_grouped_k(const GroupedArgs &p, int cus, hipStream_t s) {
   const long m64 = (p.M + 63) / 64, n128 = (p.N + 127) / 128, n64 = (p.N + 63) / 64;
-  if (m64 * n128 * p.groups >= 4L * cus) return launch_k<64, 128, 16, 2, 2, 1>(p, s);
+  // Groups of a few rows leave little but the writing of C.  Rows of C that start
+  // inside a cache line are then better not streamed: parts of a line meet in
+  // L2 (49 groups, 99 rows by 192 x 2667 32 us against 49; by 192 x 2688 23
+  // against 21; 24 groups, 800 rows by 512 x 1544 33 against 28).
+  const bool stream = p.ldc % 32 == 0 || p.K > 24L * p.groups;
+  if (m64 * n128 * p.groups >= 4L * cus)
+    return stream ? launch_k<64, 128, 16, 2, 2, 1>(p, s)
+                  : launch_k<64, 128, 16, 2, 2, 1, false>(p, s);
   if (2 * m64 * n64 * p.groups > 3L * cus || p.K < 192L * p.groups)
     return launch_k<64, 64, 32, 2, 2, 1>(p, s);
   return launch_k<32, 32, 32, 1, 1, 4>(p, s);
