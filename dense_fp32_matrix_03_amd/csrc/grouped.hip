@@ -33,6 +33,15 @@ namespace sgemm {
 
 namespace {
 
+// Roundings of products of one sign add up along a chain of fused multiply-adds:
+// u = 2^-24 of their sum for each.  So a chain has 128 k.  Up to 4096 k of a set
+// of waves the chains are simply added: at most 128 + 31 u, and 3 for four sets,
+// together 9.7e-6.  Beyond, what each addition rounds off goes into the next
+// chain, whose 128 roundings see it: 134 u + K u^2, below 1e-5 up to K = 2^29.
+// 8 groups, 8192 rows by 2048 x 1024: 260 us with one chain for a sum, 264 with
+// chains added, 272 with the carry.
+constexpr int kChain = 128, kPlain = 4096;
+
 // KFORM: groups divide k (grouped_k; A^T and B as given); otherwise they
 // divide the rows of A and C, and TB tells whether the B_g are stored
 // transposed.  VA / VB: A / B take 16-byte loads.  KS sets of WM x WN waves
@@ -191,13 +200,13 @@ grouped_kernel(GroupedArgs p, GroupMap map, FastDiv by_tiles, int tiles) {
       }
     }
   };
-  f32x16 acc[FM][FN];
+  f32x16 acc[FM][FN], sum[FM][FN];
 #pragma unroll
   for (int i = 0; i < FM; ++i)
 #pragma unroll
     for (int j = 0; j < FN; ++j)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = sum[i][j][e] = 0.f;
   auto mma = [&](const Ops &o) {
 #pragma unroll
     for (int t = 0; t < 4; ++t)
@@ -205,6 +214,24 @@ grouped_kernel(GroupedArgs p, GroupMap map, FastDiv by_tiles, int tiles) {
       for (int i = 0; i < FM; ++i)
 #pragma unroll
         for (int j = 0; j < FN; ++j) acc[i][j] = mfma32x32x2(o.a[i][t], o.b[j][t], acc[i][j]);
+  };
+  // A chain ends in `sum`; the next one begins with 0, or, with CARRY, with what
+  // the addition rounded off (once it is not finite, 0: an infinity stays one).
+  auto end_chain = [&](auto CARRY) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float before = sum[i][j][e];
+          sum[i][j][e] += acc[i][j][e];
+          if constexpr (decltype(CARRY)::value)
+            acc[i][j][e] = __builtin_isfinite(sum[i][j][e])
+                               ? acc[i][j][e] - (sum[i][j][e] - before) : 0.f;
+          else
+            acc[i][j][e] = 0.f;
+        }
   };
 
   // As in mfma_dma.hpp: one matrix-core instruction per load in the last group
@@ -266,11 +293,25 @@ grouped_kernel(GroupedArgs p, GroupMap map, FastDiv by_tiles, int tiles) {
     });
     dma_barrier_keep<(NST - 1) * kLoads>();
     read_ops(S0(), 0, cur);
-    for (int t = 0; t < turns; t += NST) {
-      static_for<NST>([&](auto S) {
-        if (decltype(S)::value == 0 || t + decltype(S)::value < turns)
-          slice(S, t + decltype(S)::value);
-      });
+    constexpr int kTurns = kChain / BK;  // of a chain
+    static_assert(kTurns % NST == 0, "a chain begins with stage 0");
+    auto chains = [&](auto CARRY) __attribute__((always_inline)) {
+      for (int t = 0; t < turns;) {
+        const int end = min(t + kTurns, turns);
+        for (; t < end; t += NST) {
+          static_for<NST>([&](auto S) {
+            if (decltype(S)::value == 0 || t + decltype(S)::value < end)
+              slice(S, t + decltype(S)::value);
+          });
+        }
+        end_chain(CARRY);
+      }
+    };
+    if (turns <= kPlain / BK) {
+      chains(std::false_type());
+    } else {
+      chains(std::true_type());
+      end_chain(std::false_type());
     }
     // The last slices sent loads past K (no memory traffic): let them retire
     // before the work-group gives up its LDS.
@@ -293,7 +334,7 @@ grouped_kernel(GroupedArgs p, GroupMap map, FastDiv by_tiles, int tiles) {
 #pragma unroll
         for (int j = 0; j < FN; ++j)
 #pragma unroll
-          for (int e = 0; e < 16; ++e) sums(kq, i, j)[e * kWave] = acc[i][j][e];
+          for (int e = 0; e < 16; ++e) sums(kq, i, j)[e * kWave] = sum[i][j][e];
     }
     __syncthreads();
     if (kq > 0) return;
@@ -304,7 +345,7 @@ grouped_kernel(GroupedArgs p, GroupMap map, FastDiv by_tiles, int tiles) {
 #pragma unroll
         for (int j = 0; j < FN; ++j)
 #pragma unroll
-          for (int e = 0; e < 16; ++e) acc[i][j][e] += sums(set, i, j)[e * kWave];
+          for (int e = 0; e < 16; ++e) sum[i][j][e] += sums(set, i, j)[e * kWave];
   }
 
   // Register e of lane l holds row acc32_row(l, e), column l % 32 of a block:
@@ -326,7 +367,7 @@ grouped_kernel(GroupedArgs p, GroupMap map, FastDiv by_tiles, int tiles) {
           if (!decltype(whole)::value && (r >= rows || j * 32 >= cols)) continue;
           float *const at =
               reinterpret_cast<float *>(reinterpret_cast<char *>(row + j * 32) + lane_at);
-          const float v = acc[i][j][e];
+          const float v = sum[i][j][e];
           if constexpr (decltype(with_c)::value)
             *at = fmaf(alpha, v, p.beta * *at);
           else if constexpr (STREAM)

@@ -25,7 +25,9 @@
  * |C(i,j) - exact| <= 1e-5 * sum |products| + 1e-6 for the sum, the order
  * of summation fixed for a given call and group lengths (repeated calls give
  * identical bits), results rounded once after beta * C, C not read when
- * beta == 0, A and B not read when alpha == 0.  Any 4-byte alignment of A, B
+ * beta == 0, A and B not read when alpha == 0.  The contract holds whatever
+ * the products' signs, for sums over up to 2^29 (long sums are added up in
+ * parts, so that their roundings do not pile up).  Any 4-byte alignment of A, B
  * and C is accepted; offsets must be 8-byte aligned
  * (SGEMM_ERR_INVALID_VALUE).  The calls allocate nothing, use no workspace
  * and are asynchronous on `stream`.  Limits (SGEMM_ERR_TOO_LARGE): sizes
