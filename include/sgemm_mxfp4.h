@@ -90,9 +90,14 @@ int sgemm_mxfp4_dequantize(int trans, int64_t rows, int64_t K, const void *codes
  * SGEMM_TYPE_BF16), ldc >= max(1, N).  Products of elements are exact; sums
  * are single precision in an order that is fixed for a given call, alpha *
  * sum + beta * C is rounded once to single precision and, for bfloat16,
- * once more, to the nearest, ties to even.  |C - exact| <= 1e-5 * sum
- * |products| + 1e-6 before that last rounding.  C is not read when beta ==
- * 0; A and B are not read when alpha == 0 or K == 0.
+ * once more, to the nearest, ties to even.  Before that last rounding
+ *   |C - exact| <= max(1e-5, (K / 7 + 16) 2^-24) * sum |products| + 1e-6.
+ * The second term, past 1e-5 from K = 1057 on, is for operands whose blocks
+ * spread widely: a matrix instruction adds 64 or 128 products at once and
+ * drops those below 2^-27 of the largest addend (K / 8 of the bound).  Sums
+ * of normally distributed values, with their magnitudes too, stay within 1e-5
+ * up to K = 2^21.  C is not read when beta == 0; A and B are not read when
+ * alpha == 0 or K == 0.
  *
  * Workspace: device memory of at least sgemm_mxfp4_workspace_size(typeA, M,
  * K) bytes (0 for SGEMM_TYPE_MXFP4), 16-byte aligned, in which a call keeps
