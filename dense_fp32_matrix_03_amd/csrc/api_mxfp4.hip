@@ -83,10 +83,13 @@ int run(int64_t groups, int64_t M, int64_t N, int64_t K, float alpha, int typeA,
   if (M > kMaxDim || N > kMaxDim || K > kMaxK || lda > kMaxDim || ldsb > kMaxDim ||
       ldc >= kMaxLdc || b_groups > SGEMM_GROUPED_MAX_GROUPS)
     return SGEMM_ERR_TOO_LARGE;
-  const int64_t rows = grouped ? sgemm::group_tile_rows(M, groups, 16) : tiles(M, 16);
-  if (rows > kMaxWorkItems / 256 / (N ? tiles(N, 16) : 1)) return SGEMM_ERR_TOO_LARGE;
   const bool writes = M > 0 && N > 0 && b_groups > 0;
   const bool reads_ab = writes && K > 0 && alpha != 0.f;
+  // Work-items for a block of 16 x 16: 256 at the most, but 512 with eight waves to it.
+  const int64_t block =
+      !grouped && M <= 16 && sgemm::mxfp4_eight_sets(reads_ab ? K : 0) ? 512 : 256;
+  const int64_t rows = grouped ? sgemm::group_tile_rows(M, groups, 16) : tiles(M, 16);
+  if (rows > kMaxWorkItems / block / (N ? tiles(N, 16) : 1)) return SGEMM_ERR_TOO_LARGE;
   if (reads_ab && !held && !cast_fits(M, K)) return SGEMM_ERR_TOO_LARGE;
   if (writes && (!C || misaligned(C, typeC == SGEMM_TYPE_F32 ? 4 : 2) ||
                  (grouped && (!offsets || misaligned(offsets, 8)))))

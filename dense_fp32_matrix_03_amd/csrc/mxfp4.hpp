@@ -46,6 +46,10 @@ struct Mxfp4Args {
 // Whether the product's kernel is to cast A itself: only then may a_type below
 // be other than SGEMM_TYPE_MXFP4.
 bool mxfp4_casts(const Mxfp4Args &p, int cus);
+// Whether eight waves, not four, share the k of a few rows: from five units of
+// 512 k on.  16 x 8192 x 8192 takes 12.3 us with eight and 13.8 with four, 16 x
+// 2048 x 2048 3.6 with either.
+inline bool mxfp4_eight_sets(long K) { return K > 2048; }
 // Picks the kernel for the product.
 hipError_t launch_mxfp4_product(const Mxfp4Args &p, int a_type, bool c_bf16, int cus,
                                 hipStream_t s);

@@ -205,12 +205,10 @@ hipError_t launch_sets(const Mxfp4Args &p, bool c_bf16, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Eight waves from five units of k on: 16 x 8192 x 8192 takes 12.3 us with
-// them and 13.8 with four, 16 x 2048 x 2048 3.6 with either.
 template <int MT, int NT, int TA>
 hipError_t launch(const Mxfp4Args &p, bool c_bf16, hipStream_t s) {
-  return p.K > 2048 ? launch_sets<MT, NT, 8, TA, false>(p, c_bf16, s)
-                    : launch_sets<MT, NT, 4, TA, false>(p, c_bf16, s);
+  return mxfp4_eight_sets(p.K) ? launch_sets<MT, NT, 8, TA, false>(p, c_bf16, s)
+                               : launch_sets<MT, NT, 4, TA, false>(p, c_bf16, s);
 }
 
 template <int TA>

@@ -201,3 +201,16 @@ def test_clamped_groups_stay_inside():
         at = [rng.choice([-2 ** 63, -1, 0, rng.randrange(-60, 120), M, 2 ** 62]) for _ in range(9)]
         for s, e in _ranges(at, M):
             assert 0 <= s <= e <= M
+
+
+@pytest.mark.parametrize("over,status", [
+    # up to 16 rows over more than 2048 k: 512 work-items for 16 columns, so 2^23 blocks are 2^32
+    (dict(K=2049), LARGE), (dict(K=2 ** 21), LARGE), (dict(M=1, K=2049), LARGE),
+    (dict(K=2049, typeA=2, lda=16, scalesA=16), LARGE),
+    (dict(K=2049, N=2 ** 27 - 16), READY), (dict(K=2048), READY), (dict(K=2049, alpha=0.0), READY),
+])
+def test_mxfp4_work_items_of_few_rows(over, status):
+    a = dict(PRODUCT, workspace=256, workspace_bytes=2 ** 40, M=16, N=2 ** 27 - 15,
+             ldsb=2 ** 27 - 1, ldc=2 ** 27 - 1, lda=2 ** 21)
+    a.update(over)
+    assert _name(sg.load_library().sgemm_run_mxfp4(*a.values(), None)) == status
