@@ -78,8 +78,8 @@ __device__ __forceinline__ f32x16 mfma_fp4_32x32x64(i32x4 a, i32x4 b, f32x16 c, 
                                                          kFormatFp4, S, sa, S, sb);
 }
 
-// C[at] = alpha sum + beta C[at], rounded to single precision once and then,
-// for bfloat16, to the nearest.  C is read only when beta != 0.
+// C[at] = alpha sum + beta C[at], rounded to single precision once after beta C[at]
+// and then, for bfloat16, to the nearest.  C is read only when beta != 0.
 template <bool CBF16>
 __device__ __forceinline__ void store_c(const Mxfp4Args &p, long at, float sum) {
   if constexpr (CBF16) {

@@ -88,11 +88,12 @@ int sgemm_mxfp4_dequantize(int trans, int64_t rows, int64_t K, const void *codes
  * Casting on the way gives the bits of sgemm_mxfp4_quantize followed by the
  * product of held matrices.  C is M x N of typeC (SGEMM_TYPE_F32 or
  * SGEMM_TYPE_BF16), ldc >= max(1, N).  Products of elements are exact; sums
- * are single precision in an order that is fixed for a given call, alpha *
- * sum + beta * C is rounded once to single precision and, for bfloat16,
- * once more, to the nearest, ties to even.  Before that last rounding
+ * are single precision in an order that is fixed for a given call.  The
+ * result is alpha * sum + beta * C, rounded to single precision once after
+ * beta * C (a fused multiply-add) and, for bfloat16, once more, to the
+ * nearest, ties to even.  Before that last rounding
  *   |C - exact| <= max(1e-5, (K / 7 + 16) 2^-24) * sum |products| + 1e-6.
- * The second term, past 1e-5 from K = 1057 on, is for operands whose blocks
+ * The second term, past 1e-5 from K = 1063 on, is for operands whose blocks
  * spread widely: a matrix instruction adds 64 or 128 products at once and
  * drops those below 2^-27 of the largest addend (K / 8 of the bound).  Sums
  * of normally distributed values, with their magnitudes too, stay within 1e-5

@@ -573,3 +573,29 @@ def test_the_most_groups():
     lengths = [n % 5 // 4 for n in range(4095)] + [200]
     for kind, out in (("f32", "f32"), ("mxfp4", "bf16")):
         _check(*_product(sum(lengths), 33, 150, kind, out, lengths=lengths), out)
+
+
+@pytest.mark.parametrize("M,N,K", [(5, 70, 300), (40, 70, 512), (200, 300, 256), (700, 8192, 256)])
+def test_beta_c_is_rounded_before_it_is_added(M, N, K):
+    """alpha sum + beta C is one fused multiply-add on beta C rounded to single
+    precision, bit for bit (the sums are exact: small integers)."""
+    import torch
+    g = np.random.default_rng(M)
+    a, b = (g.integers(-3, 4, (n, K)).astype(np.float32) for n in (M, N))
+    a[:, ::32], b[:, ::32] = 4, 4  # scales of 1: the values are held as they are
+    ca, sa, _ = _quantize(a, "f32", 0)
+    cb, sb, _ = _quantize(b, "f32", 0)
+    C0 = g.standard_normal((M, N)).astype(np.float32)
+    alpha, beta = np.float32(0.7), np.float32(-1 / 3)
+    C = _cuda(C0)
+    sg.sgemm_run_mxfp4(M, N, K, float(alpha), "mxfp4", ca, M, sa, cb, sb, N, float(beta), "f32", C, N)
+    sums = a.astype(np.float64) @ b.astype(np.float64).T
+    # 24 + 24 bits and an addend near them: rounded in 64 bits only where the last bit of 53 decides
+    want = (np.float64(alpha) * sums + (beta * C0).astype(np.float64)).astype(np.float32)
+    got = C.cpu().numpy()
+    assert np.array_equal(got, want)
+    # The other reading, one rounding in all, differs where beta C's (2^-26) moves a result of
+    # about 2^7 (spacing 2^-16) over a halfway point: in about M N / 2^9 places, too few at 5 x 70.
+    if M > 5:
+        once = (np.float64(alpha) * sums + np.float64(beta) * C0).astype(np.float32)
+        assert not np.array_equal(got, once)
