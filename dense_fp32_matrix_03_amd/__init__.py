@@ -172,13 +172,15 @@ def _type(t) -> int:
     return TYPES[t] if isinstance(t, str) else int(t)
 
 
-def _offsets(x):
-    """_ptr of group offsets, which the kernels read as 64-bit integers."""
+def _offsets(x, groups=0):
+    """_ptr of group offsets, which the kernels read as groups + 1 64-bit integers."""
     if hasattr(x, "dtype"):
         if x.element_size() != 8 or x.is_floating_point() or x.is_complex():
             raise TypeError("offsets must be int64")
         if not x.is_contiguous():
             raise ValueError("offsets must be contiguous")
+        if groups > 0 and x.numel() <= groups:
+            raise ValueError(f"offsets must hold groups + 1 = {groups + 1} values, not {x.numel()}")
     return _ptr(x)
 
 
@@ -278,7 +280,7 @@ def sgemm_run_grouped(transB, groups, M, N, K, alpha, A, lda, B, ldb, strideB, b
     group g (include/sgemm_grouped.h); offsets: groups + 1 int64 on the GPU."""
     _check("sgemm_run_grouped", load_library().sgemm_run_grouped(
         int(transB), groups, M, N, K, float(alpha), _ptr(A), lda, _ptr(B), ldb, strideB,
-        float(beta), _ptr(C), ldc, _offsets(offsets), _stream(stream)))
+        float(beta), _ptr(C), ldc, _offsets(offsets, groups), _stream(stream)))
 
 
 def sgemm_run_grouped_k(groups, M, N, K, alpha, A, lda, B, ldb, beta, C, ldc, strideC, offsets,
@@ -287,7 +289,7 @@ def sgemm_run_grouped_k(groups, M, N, K, alpha, A, lda, B, ldb, beta, C, ldc, st
     gradient of sgemm_run_grouped's B (include/sgemm_grouped.h)."""
     _check("sgemm_run_grouped_k", load_library().sgemm_run_grouped_k(
         groups, M, N, K, float(alpha), _ptr(A), lda, _ptr(B), ldb, float(beta), _ptr(C), ldc,
-        strideC, _offsets(offsets), _stream(stream)))
+        strideC, _offsets(offsets, groups), _stream(stream)))
 
 
 def sgemm_mxfp4_codes_size(rows, K) -> int:
@@ -336,7 +338,7 @@ def sgemm_run_mxfp4_grouped(groups, M, N, K, alpha, typeA, A, lda, scalesA, B, s
     """sgemm_run_mxfp4 for rows in groups, group g with rows g N .. of B."""
     _check("sgemm_run_mxfp4_grouped", load_library().sgemm_run_mxfp4_grouped(
         groups, M, N, K, float(alpha), _type(typeA), _ptr(A), lda, _ptr(scalesA), _ptr(B),
-        _ptr(scalesB), ldsb, float(beta), _type(typeC), _ptr(C), ldc, _offsets(offsets),
+        _ptr(scalesB), ldsb, float(beta), _type(typeC), _ptr(C), ldc, _offsets(offsets, groups),
         _ptr(workspace), workspace_bytes, _stream(stream)))
 
 

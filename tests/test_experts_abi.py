@@ -214,3 +214,23 @@ def test_mxfp4_work_items_of_few_rows(over, status):
              ldsb=2 ** 27 - 1, ldc=2 ** 27 - 1, lda=2 ** 21)
     a.update(over)
     assert _name(sg.load_library().sgemm_run_mxfp4(*a.values(), None)) == status
+
+
+def test_binding_checks_the_number_of_offsets():
+    """The kernels read groups + 1 values whatever the tensor holds."""
+    torch = pytest.importorskip("torch")
+    at = torch.zeros(4, dtype=torch.int64)
+    for groups in (4, 5, 4096):
+        with pytest.raises(ValueError, match=f"offsets must hold groups \\+ 1 = {groups + 1} values"):
+            sg._offsets(at, groups)
+        with pytest.raises(ValueError, match="groups"):
+            sg.sgemm_run_grouped(0, groups, 8, 5, 7, 1.0, 16, 7, 16, 5, 35, 0.0, 16, 5, at, 0)
+        with pytest.raises(ValueError, match="groups"):
+            sg.sgemm_run_grouped_k(groups, 8, 5, 7, 1.0, 16, 8, 16, 5, 0.0, 16, 5, 40, at, 0)
+        with pytest.raises(ValueError, match="groups"):
+            sg.sgemm_run_mxfp4_grouped(groups, 8, 5, 7, 1.0, "f32", 16, 7, None, 16, 16, 5 * groups,
+                                       0.0, "f32", 16, 5, at, 256, 8 * 68, 0)
+    for groups in (0, 1, 3):  # enough: the next check is the device's
+        with pytest.raises(ValueError, match="GPU"):
+            sg._offsets(at, groups)
+    assert sg._offsets(None, 0) is None and sg._offsets(4096, 4096) == 4096
