@@ -48,8 +48,8 @@ constexpr int kChain = 128, kPlain = 4096;
 // share a tile; set q takes slices q, q + KS, .. through LDS stages of its own,
 // and the sets' sums are added in order at the end.  STREAM: stores of C are
 // non-temporal.
-template <bool KFORM, bool TB, int BM, int BN, int BK, int WM, int WN, int KS, int NST, bool VA,
-          bool VB, bool STREAM>
+template <bool KFORM, bool TB, int BM, int BN, int BK, int WM, int WN, int KS, bool VA, bool VB,
+          bool STREAM>
 __global__ void __launch_bounds__(WM *WN *KS *kWave, 2)
 grouped_kernel(GroupedArgs p, GroupMap map, FastDiv by_tiles, int tiles) {
   constexpr bool TA = KFORM;
@@ -61,12 +61,9 @@ grouped_kernel(GroupedArgs p, GroupMap map, FastDiv by_tiles, int tiles) {
   static_assert(!GA::SPARE && !GB::SPARE, "loads must split evenly over the waves");
   constexpr int kLoads = GA::NBW + GB::NBW;
 
-  static_assert(NST >= 2 && NST <= 4, "2 to 4 LDS stages");
   constexpr int SA = BM * BK, SB = BK * BN;
-  __shared__ __attribute__((aligned(1024))) float As0[KS * SA], As1[KS * SA],
-      As2[NST > 2 ? KS * SA : 1], As3[NST > 3 ? KS * SA : 1];
-  __shared__ __attribute__((aligned(1024))) float Bs0[KS * SB], Bs1[KS * SB],
-      Bs2[NST > 2 ? KS * SB : 1], Bs3[NST > 3 ? KS * SB : 1];
+  __shared__ __attribute__((aligned(1024))) float As0[KS * SA], As1[KS * SA];
+  __shared__ __attribute__((aligned(1024))) float Bs0[KS * SB], Bs1[KS * SB];
 
   const int lane = threadIdx.x % kWave;
   const int all_waves = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -74,22 +71,16 @@ grouped_kernel(GroupedArgs p, GroupMap map, FastDiv by_tiles, int tiles) {
   const int wave = KS > 1 ? all_waves % NW : all_waves;
   const int wm = wave / WN, wn = wave % WN;
   const int r32 = lane % 32, half = lane / 32;
-  auto stage_a = [&](auto S) -> float * {
-    constexpr int i = decltype(S)::value;
-    return (i == 0 ? As0 : i == 1 ? As1 : i == 2 ? As2 : As3) + kq * SA;
-  };
-  auto stage_b = [&](auto S) -> float * {
-    constexpr int i = decltype(S)::value;
-    return (i == 0 ? Bs0 : i == 1 ? Bs1 : i == 2 ? Bs2 : Bs3) + kq * SB;
-  };
+  auto stage_a = [&](auto S) -> float * { return (decltype(S)::value ? As1 : As0) + kq * SA; };
+  auto stage_b = [&](auto S) -> float * { return (decltype(S)::value ? Bs1 : Bs0) + kq * SB; };
 
   const float *A = p.A, *B = p.B;
   float *C = p.C;
   int m0, n0, m_end, K;
   if constexpr (KFORM) {
     // Each group's tiles are spread over the XCDs (a group of tiles per XCD
-    // would leave the chip waiting for the XCD of the longest one), the longest
-    // groups first.
+    // would leave the chip waiting for the XCD of the longest one), of up to 64 groups the longest
+    // groups the longest first.
     const int rank = by_tiles((int)blockIdx.x);
     const int t = xcd_contiguous_id((int)blockIdx.x - rank * tiles, tiles);
     int first, last;
@@ -250,9 +241,10 @@ grouped_kernel(GroupedArgs p, GroupMap map, FastDiv by_tiles, int tiles) {
     });
   };
   using S0 = std::integral_constant<int, 0>;
+  using S1 = std::integral_constant<int, 1>;
   Ops cur, nxt;
   auto slice = [&](auto S, int t) {  // the set's t-th slice
-    using SN = std::integral_constant<int, (decltype(S)::value + 1) % NST>;
+    using SN = std::integral_constant<int, 1 - decltype(S)::value>;
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       if (g + 1 < G) {
@@ -260,8 +252,8 @@ grouped_kernel(GroupedArgs p, GroupMap map, FastDiv by_tiles, int tiles) {
         mma(cur);
         interleave(std::false_type());
       } else {
-        dma_barrier_keep<(NST - 2) * kLoads>();
-        dma(S, kq + (t + NST) * KS);
+        dma_barrier_keep<0>();
+        dma(S, kq + (t + 2) * KS);
         read_ops(SN(), 0, nxt);
         mma(cur);
         interleave(std::true_type());
@@ -287,22 +279,17 @@ grouped_kernel(GroupedArgs p, GroupMap map, FastDiv by_tiles, int tiles) {
     } else {
       dma(S0(), kq);
     }
-    static_for<NST - 1>([&](auto I) {
-      using S = std::integral_constant<int, decltype(I)::value + 1>;
-      dma(S(), kq + (decltype(I)::value + 1) * KS);
-    });
-    dma_barrier_keep<(NST - 1) * kLoads>();
+    dma(S1(), kq + KS);
+    dma_barrier_keep<kLoads>();
     read_ops(S0(), 0, cur);
     constexpr int kTurns = kChain / BK;  // of a chain
-    static_assert(kTurns % NST == 0, "a chain begins with stage 0");
+    static_assert(kTurns % 2 == 0, "a chain begins with stage 0");
     auto chains = [&](auto CARRY) __attribute__((always_inline)) {
       for (int t = 0; t < turns;) {
         const int end = min(t + kTurns, turns);
-        for (; t < end; t += NST) {
-          static_for<NST>([&](auto S) {
-            if (decltype(S)::value == 0 || t + decltype(S)::value < end)
-              slice(S, t + decltype(S)::value);
-          });
+        for (; t < end; t += 2) {
+          slice(S0(), t);
+          if (t + 1 < end) slice(S1(), t + 1);
         }
         end_chain(CARRY);
       }
@@ -390,7 +377,7 @@ template <bool KFORM, bool TB, int BM, int BN, int BK, int WM, int WN, int KS, b
 hipError_t launch(const GroupedArgs &p, hipStream_t s) {
   const int tiles_m = (p.M + BM - 1) / BM, tiles_n = (p.N + BN - 1) / BN;
   const long rows = KFORM ? (long)tiles_m * p.groups : group_tile_rows(p.M, p.groups, BM);
-  hipLaunchKernelGGL((grouped_kernel<KFORM, TB, BM, BN, BK, WM, WN, KS, 2, VA, VB, STREAM>),
+  hipLaunchKernelGGL((grouped_kernel<KFORM, TB, BM, BN, BK, WM, WN, KS, VA, VB, STREAM>),
                      dim3((unsigned)(rows * tiles_n)), dim3(WM * WN * KS * kWave), 0, s, p,
                      make_group_map(tiles_n), make_fast_div(tiles_m * tiles_n), tiles_m * tiles_n);
   return hipGetLastError();

@@ -49,7 +49,7 @@ constexpr int kSliceBytes = 128;  // codes of a row's slice
 // through LDS stages of its own, and the sets' sums are added in order at the
 // end.  With few tiles the time is a chain of slices, each as long as its
 // loads take to arrive: the sets walk KS chains at once.
-template <int BM, int BN, int WM, int WN, int KS, int NST, bool CBF16>
+template <int BM, int BN, int WM, int WN, int KS, bool CBF16>
 __global__ void __launch_bounds__(WM *WN *KS *kWave, 2)
 mxfp4_tile_kernel(Mxfp4Args p, TileMap tmap, GroupMap map) {
   constexpr int NW = WM * WN;  // waves of a set
@@ -65,14 +65,11 @@ mxfp4_tile_kernel(Mxfp4Args p, TileMap tmap, GroupMap map) {
 
   // One LDS array per stage and operand, so that the compiler sees that loads
   // into one stage do not touch the one that is read (mfma_dma.hpp).
-  static_assert(NST >= 2 && NST <= 4, "2 to 4 LDS stages");
   constexpr int SA = BM * kSliceBytes / 4, SB = BN * kSliceBytes / 4, SS = QS * NW * 64;
-  __shared__ __attribute__((aligned(1024))) float As0[KS * SA], As1[KS * SA],
-      As2[NST > 2 ? KS * SA : 1], As3[NST > 3 ? KS * SA : 1];
-  __shared__ __attribute__((aligned(1024))) float Bs0[KS * SB], Bs1[KS * SB],
-      Bs2[NST > 2 ? KS * SB : 1], Bs3[NST > 3 ? KS * SB : 1];
-  __shared__ __attribute__((aligned(1024))) float Ss0[KS * SS], Ss1[KS * SS],
-      Ss2[NST > 2 ? KS * SS : 1], Ss3[NST > 3 ? KS * SS : 1];  // scales: A's rows, then B's
+  __shared__ __attribute__((aligned(1024))) float As0[KS * SA], As1[KS * SA];
+  __shared__ __attribute__((aligned(1024))) float Bs0[KS * SB], Bs1[KS * SB];
+  // Scales: A's rows, then B's.
+  __shared__ __attribute__((aligned(1024))) float Ss0[KS * SS], Ss1[KS * SS];
 
   const int lane = threadIdx.x % kWave;
   const int all_waves = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -80,18 +77,9 @@ mxfp4_tile_kernel(Mxfp4Args p, TileMap tmap, GroupMap map) {
   const int wave = KS > 1 ? all_waves % NW : all_waves;
   const int wm = wave / WN, wn = wave % WN;
   const int r32 = lane % 32, half = lane / 32;
-  auto stage_a = [&](auto S) -> float * {
-    constexpr int i = decltype(S)::value;
-    return (i == 0 ? As0 : i == 1 ? As1 : i == 2 ? As2 : As3) + kq * SA;
-  };
-  auto stage_b = [&](auto S) -> float * {
-    constexpr int i = decltype(S)::value;
-    return (i == 0 ? Bs0 : i == 1 ? Bs1 : i == 2 ? Bs2 : Bs3) + kq * SB;
-  };
-  auto stage_s = [&](auto S) -> float * {
-    constexpr int i = decltype(S)::value;
-    return (i == 0 ? Ss0 : i == 1 ? Ss1 : i == 2 ? Ss2 : Ss3) + kq * SS;
-  };
+  auto stage_a = [&](auto S) -> float * { return (decltype(S)::value ? As1 : As0) + kq * SA; };
+  auto stage_b = [&](auto S) -> float * { return (decltype(S)::value ? Bs1 : Bs0) + kq * SB; };
+  auto stage_s = [&](auto S) -> float * { return (decltype(S)::value ? Ss1 : Ss0) + kq * SS; };
 
   long a_row = 0, b_row = 0;  // first row of the group in A (and C), and of its B
   int m0, n0, m_end = p.M;
@@ -228,16 +216,17 @@ mxfp4_tile_kernel(Mxfp4Args p, TileMap tmap, GroupMap map) {
     });
   };
   using S0 = std::integral_constant<int, 0>;
-  // The set's t-th slice is in stage S, the next NST - 1 on their way to the
-  // others.
+  using S1 = std::integral_constant<int, 1>;
+  // The set's t-th slice is in stage S, the next one on its way to the
+  // other.
   // WHOLE: a wave with one block of 32 x 32 has too few matrix-core
   // instructions in a step to cover the next one's reads, and registers to
   // spare: it reads a whole slice's operands while it multiplies the one
   // before.  The barrier waits for slice t + 1, and for every wave to have read
-  // slice t; then slice t + NST goes to stage S.
+  // slice t; then slice t + 2 goes to stage S.
   // Otherwise the operands are read a step ahead, and the last step of a slice
   // waits for slice t + 1, and for every wave to be done with stage S, sends
-  // slice t + NST there and reads slice t + 1's first operands.
+  // slice t + 2 there and reads slice t + 1's first operands.
   constexpr bool WHOLE = FM * FN == 1;
   constexpr int kAhead = WHOLE ? 4 : 1;  // steps whose operands are held
   Ops cur[kAhead], nxt[kAhead];
@@ -246,9 +235,9 @@ mxfp4_tile_kernel(Mxfp4Args p, TileMap tmap, GroupMap map) {
     for (int s = 0; s < kAhead; ++s) read_ops(S, s, o[s]);
   };
   auto slice = [&](auto S) {
-    using SN = std::integral_constant<int, (decltype(S)::value + 1) % NST>;
+    using SN = std::integral_constant<int, 1 - decltype(S)::value>;
     if constexpr (WHOLE) {
-      dma_barrier_keep<(NST - 2) * kLoads>();
+      dma_barrier_keep<0>();
       dma(S);
       read_ahead(SN(), nxt);
       read_scales(SN(), sn);
@@ -263,7 +252,7 @@ mxfp4_tile_kernel(Mxfp4Args p, TileMap tmap, GroupMap map) {
           mma(STEP, cur[0]);
           interleave(std::false_type());
         } else {
-          dma_barrier_keep<(NST - 2) * kLoads>();
+          dma_barrier_keep<0>();
           dma(S);
           read_ops(SN(), 0, nxt[0]);
           read_scales(SN(), sn);
@@ -278,14 +267,14 @@ mxfp4_tile_kernel(Mxfp4Args p, TileMap tmap, GroupMap map) {
 
   if (nk > 0) {
     const int turns = (nk + KS - 1) / KS;  // the same for all sets: they share the barriers
-    static_for<NST>([&](auto S) { dma(S); });
-    dma_barrier_keep<(NST - 1) * kLoads>();
+    dma(S0());
+    dma(S1());
+    dma_barrier_keep<kLoads>();
     read_ahead(S0(), cur);
     read_scales(S0(), sc);
-    for (int t = 0; t < turns; t += NST) {
-      static_for<NST>([&](auto S) {
-        if (decltype(S)::value == 0 || t + decltype(S)::value < turns) slice(S);
-      });
+    for (int t = 0; t < turns; t += 2) {
+      slice(S0());
+      if (t + 1 < turns) slice(S1());
     }
     // The last slices sent loads past K (no memory traffic): let them retire
     // before the work-group gives up its LDS.
@@ -355,7 +344,7 @@ mxfp4_tile_kernel(Mxfp4Args p, TileMap tmap, GroupMap map) {
     store(std::false_type(), std::false_type());
 }
 
-template <int BM, int BN, int WM, int WN, int KS, int NST>
+template <int BM, int BN, int WM, int WN, int KS>
 hipError_t launch(const Mxfp4Args &p, bool c_bf16, hipStream_t s) {
   const int tiles_m = (p.M + BM - 1) / BM, tiles_n = (p.N + BN - 1) / BN;
   const long rows = p.offsets ? group_tile_rows(p.M, p.groups, BM) : tiles_m;
@@ -363,10 +352,10 @@ hipError_t launch(const Mxfp4Args &p, bool c_bf16, hipStream_t s) {
   const TileMap tmap = make_tile_map(tiles_m, tiles_n, kGroupRaster);
   const GroupMap map = make_group_map(tiles_n);
   if (c_bf16)
-    hipLaunchKernelGGL((mxfp4_tile_kernel<BM, BN, WM, WN, KS, NST, true>), grid, block, 0, s, p, tmap,
+    hipLaunchKernelGGL((mxfp4_tile_kernel<BM, BN, WM, WN, KS, true>), grid, block, 0, s, p, tmap,
                        map);
   else
-    hipLaunchKernelGGL((mxfp4_tile_kernel<BM, BN, WM, WN, KS, NST, false>), grid, block, 0, s, p, tmap,
+    hipLaunchKernelGGL((mxfp4_tile_kernel<BM, BN, WM, WN, KS, false>), grid, block, 0, s, p, tmap,
                        map);
   return hipGetLastError();
 }
@@ -398,12 +387,12 @@ hipError_t launch_mxfp4_tile(const Mxfp4Args &p, bool c_bf16, int cus, hipStream
   const double c64 = n64 == 1 ? 0.35 : n64 == 2 ? 0.42 : 0.16 * n64;
   const double c128 = n128 == 1 ? 0.65 : n128 == 2 ? 0.77 : 0.29 * n128;
   if ((p.offsets && mean <= 64) || (c64 <= c128 && c64 <= per_cu(256))) {
-    if (n64 == 1 && p.K >= 6144) return launch<64, 64, 2, 2, 4, 2>(p, c_bf16, s);
-    if (n64 == 2 && p.K >= 6144) return launch<64, 64, 2, 2, 2, 2>(p, c_bf16, s);
-    return launch<64, 64, 2, 2, 1, 2>(p, c_bf16, s);
+    if (n64 == 1 && p.K >= 6144) return launch<64, 64, 2, 2, 4>(p, c_bf16, s);
+    if (n64 == 2 && p.K >= 6144) return launch<64, 64, 2, 2, 2>(p, c_bf16, s);
+    return launch<64, 64, 2, 2, 1>(p, c_bf16, s);
   }
-  return c128 <= per_cu(256) ? launch<128, 128, 2, 2, 1, 2>(p, c_bf16, s)
-                             : launch<256, 256, 2, 4, 1, 2>(p, c_bf16, s);
+  return c128 <= per_cu(256) ? launch<128, 128, 2, 2, 1>(p, c_bf16, s)
+                             : launch<256, 256, 2, 4, 1>(p, c_bf16, s);
 }
 
 }  // namespace sgemm
