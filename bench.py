@@ -463,24 +463,36 @@ def general_table(settle: float) -> list[dict]:
     return rows
 
 
-def experts_table(settle: float) -> list[dict]:
-    """Time the calls of perf/operators.py's cases (products of grouped rows,
-    casts to 4-bit floats and products of them), one JSON line each.  Several
-    sets of operands are used in turn, more of them than the caches hold."""
+def operators():
+    """perf/operators.py as a module."""
     import importlib.util
-
-    import torch
 
     spec = importlib.util.spec_from_file_location("operators",
                                                   os.path.join(ROOT, "perf", "operators.py"))
     ops = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(ops)
+    return ops
+
+
+def operand_sets(nbytes: int) -> int:
+    """Sets of operands of `nbytes` to use in turn so that none is still in the
+    256 MB Infinity Cache when its turn comes again."""
+    return max(2, int(8e8 / nbytes) + 1)
+
+
+def experts_table(settle: float) -> list[dict]:
+    """Time the calls of perf/operators.py's cases (products of grouped rows,
+    casts to 4-bit floats and products of them), one JSON line each.  Several
+    sets of operands are used in turn, more of them than the caches hold."""
+    import torch
+
+    ops = operators()
     ops.own = True
     rows = []
     stream = torch.cuda.current_stream()
     for case in ops.listed():
         need = ops.work(case)
-        sets = [ops.prepare(case, i) for i in range(max(2, min(8, int(8e8 / need["bytes"]) + 1)))]
+        sets = [ops.prepare(case, i) for i in range(operand_sets(need["bytes"]))]
         for st in sets:
             ops.run(st)
         torch.cuda.synchronize()
@@ -490,7 +502,7 @@ def experts_table(settle: float) -> list[dict]:
                 ops.run(st)
             torch.cuda.synchronize()
             steps += len(sets)
-        steps = max(20, min(400, steps)) // len(sets) * len(sets)
+        steps = max(1, min(400, steps) // len(sets)) * len(sets)
         t0 = torch.cuda.Event(enable_timing=True)
         t1 = torch.cuda.Event(enable_timing=True)
         t0.record(stream)

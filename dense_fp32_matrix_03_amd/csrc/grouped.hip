@@ -79,7 +79,7 @@ grouped_kernel(GroupedArgs p, GroupMap map, FastDiv by_tiles, int tiles) {
   int m0, n0, m_end, K;
   if constexpr (KFORM) {
     // Each group's tiles are spread over the XCDs (a group of tiles per XCD
-    // would leave the chip waiting for the XCD of the longest one), of up to 64 groups the longest
+    // would leave the chip waiting for the XCD of the longest one), of up to 64
     // groups the longest first.
     const int rank = by_tiles((int)blockIdx.x);
     const int t = xcd_contiguous_id((int)blockIdx.x - rank * tiles, tiles);

@@ -51,6 +51,15 @@ def test_committed_counters_follow_the_kernel_sources():
     assert t >= inputs.BY_NAME[bench.HEADLINE].min_bytes
 
 
+def test_operand_sets_of_the_experts_table_exceed_the_caches():
+    ops = bench.operators()
+    for case in ops.listed():
+        need = ops.work(case)["bytes"]
+        n = bench.operand_sets(need)
+        assert n >= 2 and n * need > 2 * 256e6, case["name"]
+        assert (n - 1) * need < 1e9 or n == 2, case["name"]  # and the card holds them
+
+
 @pytest.mark.gpu
 def test_headline_json_line():
     r = subprocess.run([sys.executable, os.path.join(ROOT, "bench.py"), "--steps", "2",
