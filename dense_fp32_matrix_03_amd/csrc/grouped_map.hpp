@@ -67,8 +67,8 @@ struct GroupTile {
 
 // Group g's rows, clamped so that they lie in [0, M] whatever the offsets are
 // (M < 2^31).
-__device__ __forceinline__ void group_range(const int64_t *offsets, int g, int M, int &first,
-                                            int &last) {
+__host__ __device__ __forceinline__ void group_range(const int64_t *offsets, int g, int M,
+                                                     int &first, int &last) {
   const int64_t s = offsets[g], e = offsets[g + 1];
   first = s < 0 ? 0 : (s > M ? M : (int)s);
   last = e < first ? first : (e > M ? M : (int)e);

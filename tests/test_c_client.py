@@ -76,3 +76,11 @@ def test_client_results_match_the_oracle(tmp_path):
     V = out("V.bin", (nv,))
     ref = oracle.vector_add(A.ravel()[:nv], B.ravel()[:nv])
     assert np.array_equal(V.view(np.uint32), ref.view(np.uint32))
+
+
+@pytest.mark.parametrize("header", sorted(f for f in os.listdir(os.path.join(HERE, "..", "include"))))
+def test_each_header_alone_is_strict_c99(header, tmp_path):
+    src = tmp_path / "one.c"
+    src.write_text(f'#include "{header}"\nint main(void) {{ return 0; }}\n')
+    subprocess.run(["gcc", "-std=c99", "-Wall", "-Wextra", "-Werror", "-pedantic", "-fsyntax-only",
+                    "-I" + os.path.join(HERE, "..", "include"), str(src)], check=True, timeout=60)

@@ -234,3 +234,15 @@ def test_binding_checks_the_number_of_offsets():
         with pytest.raises(ValueError, match="GPU"):
             sg._offsets(at, groups)
     assert sg._offsets(None, 0) is None and sg._offsets(4096, 4096) == 4096
+
+
+@pytest.mark.skipif(not os.path.exists(HIPCC), reason="hipcc not installed")
+def test_the_kernels_clamp_of_group_rows(tmp_path):
+    """tests/group_range_check.cpp, compiled for the host only."""
+    exe = tmp_path / "group_range_check"
+    subprocess.run([HIPCC, "-std=c++17", "-O2", "--cuda-host-only", "-x", "hip", "-I", CSRC,
+                    os.path.join(HERE, "group_range_check.cpp"), "-o", str(exe)],
+                   check=True, capture_output=True, timeout=300)
+    r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr
+    assert "failures 0" in r.stdout
