@@ -446,11 +446,17 @@ hipError_t launch_grouped_rows(const GroupedArgs &p, bool tb, int cus, hipStream
 //    1 group of 16384 rows by 64 x 64           473   268    73
 hipError_t launch_grouped_k(const GroupedArgs &p, int cus, hipStream_t s) {
   const long m64 = (p.M + 63) / 64, n128 = (p.N + 127) / 128, n64 = (p.N + 63) / 64;
-  // Groups of a few rows leave little but the writing of C.  Rows of C that start
-  // inside a cache line are then better not streamed: parts of a line meet in
-  // L2 (49 groups, 99 rows by 192 x 2667 32 us against 49; by 192 x 2688 23
-  // against 21; 24 groups, 800 rows by 512 x 1544 33 against 28).
-  const bool stream = p.ldc % 32 == 0 || p.K > 24L * p.groups;
+  // Groups of a few rows leave little but the writing of C.  Unless each row of C
+  // starts on 64 bytes, stores are then better not streamed: parts of a line
+  // meet in L2.  Streamed / plain at 2, 16, 24, 33 and 64 rows a group:
+  //    24 groups, 512 x 1544   27/21  28/25  29/28  30/31  38/40
+  //    49 groups, 192 x 2667   48/32  48/36  49/37  48/41  55/52
+  //    49 groups, 192 x 2688   21/23  23/29  25/31  29/37  40/48
+  //    the same, C 32 bytes on 46/30  47/34  48/37  49/41  55/51
+  //    32 groups, 257 x 1000   13/13  16/17  17/18  17/20  20/25
+  const bool lines =
+      ((reinterpret_cast<uintptr_t>(p.C) / 4 | p.ldc | (p.groups > 1 ? p.strideC : 0)) & 15) == 0;
+  const bool stream = lines || p.K > 32L * p.groups;
   if (m64 * n128 * p.groups >= 4L * cus)
     return stream ? launch_k<64, 128, 16, 2, 2, 1>(p, s)
                   : launch_k<64, 128, 16, 2, 2, 1, false>(p, s);

@@ -585,3 +585,10 @@ def test_two_streams_at_once():
         alone = torch.zeros(M, N, device="cuda")
         sg.sgemm_run_grouped(0, G, M, N, K, 1.0, A[i], K, B[i], N, K * N, 0.0, alone, N, d_at)
         assert torch.equal(alone, C[i])
+
+
+@pytest.mark.parametrize("N,pads,shift", [(512, (0, 0, 0), 0), (512, (0, 0, 0), 8), (528, (0, 0, 0), 16),
+                                          (512, (0, 0, 8), 0), (513, (0, 0, 15), 0), (517, (0, 0, 0), 3)])
+@pytest.mark.parametrize("alpha,beta", [(1.0, 0.0), (0.5, 2.0)])
+def test_k_of_short_groups_on_lines_of_c_and_off_them(N, pads, shift, alpha, beta):
+    _run_k("short groups", 500, N, alpha, beta, pads, shift)
