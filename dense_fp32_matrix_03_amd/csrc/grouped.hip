@@ -7,10 +7,10 @@
 // sum_r A(r, :)^T B(r, :) + beta C_g, on v_mfma_f32_32x32x2_f32.
 //
 // Long groups are bound by the matrix cores (8 groups, 8192 rows by 2048 x 1024
-// 133 TFLOP/s, the same rows as k of 1024 x 2048 138, the pipes 87-89% busy),
-// short ones by reading B (16 groups, 24 rows by 2048 x 2048 5.2 TB/s), and
-// what lies between by the rows that tiles pad to (64 groups of 64 rows on
-// average by 1000 x 777 67 TFLOP/s, 80 with the padding).
+// 130-132 TFLOP/s, the same rows as k of 1024 x 2048 134-136, the pipes 85-87%
+// busy), short ones by reading B (16 groups, 24 rows by 2048 x 2048 5.2 TB/s),
+// and what lies between partly by the rows that tiles pad to (64 groups of 64 rows
+// on average by 1000 x 777 68 TFLOP/s, 81 with the padding).
 //
 // Edges.  An element outside op(A)'s rows or op(B)'s columns is fetched at an
 // offset past the descriptor's end and reads as zero.  A partial last slice
@@ -411,16 +411,17 @@ hipError_t launch_k(const GroupedArgs &p, hipStream_t s) {
 //  - 64 x 64: the least LDS traffic per product of the four.
 // Measured in that order (us; B as given and not in the caches, groups of
 // unequal length):
-//    1 group of 1 row by 8192 x 8192       66   89  110  189
-//    1 of 64 by 4096 x 4096                34   45   56   96
-//    16 groups, 24 rows by 2048 x 2048     50   39   44   74
-//    32 groups, 24 rows by 1024 x 2048     42   34   42   73
-//    64 groups, 512 rows by 1024 x 1024    62   56   61   70
-//    16 groups, 128 rows by 2048 x 2048    52   54   44   75
-//    16 groups, 512 rows by 2048 x 2048    78   80   62  103
-//    4 groups, 200 rows by 2000 x 4000     51   54   60  100
-//    8 groups, 2048 rows by 2048 x 1024   105   85   81   92
-//    8 groups, 8192 rows by 2048 x 1024   357  302  273  258
+//    1 group of 1 row by 8192 x 8192       67   89  110  191
+//    1 of 64 by 4096 x 4096                35   46   55   97
+//    16 groups, 24 rows by 2048 x 2048     49   37   43   74
+//    32 groups, 24 rows by 1024 x 2048     44   34   42   74
+//    64 groups, 512 rows by 1024 x 1024    59   53   60   68
+//    16 groups, 128 rows by 2048 x 2048    53   53   45   75
+//    16 groups, 512 rows by 2048 x 2048    79   84   63  101
+//    4 groups, 200 rows by 2000 x 4000     52   53   60  100
+//    the same, other lengths               74   60   76   99
+//    8 groups, 2048 rows by 2048 x 1024   107   90   84   92
+//    8 groups, 8192 rows by 2048 x 1024   363  308  284  268
 hipError_t launch_grouped_rows(const GroupedArgs &p, bool tb, int cus, hipStream_t s) {
   const long groups = p.groups < p.M ? p.groups : p.M, most = p.M / 32 + groups / 2;
   const long small = (most > groups ? most : groups) * ((p.N + 31) / 32);
@@ -432,18 +433,19 @@ hipError_t launch_grouped_rows(const GroupedArgs &p, bool tb, int cus, hipStream
   return launch_rows<64, 64, 32, 2, 2, 1>(p, tb, s);
 }
 
-// Tiles of 64 x 128 in slices of 16 rows (24 KiB of LDS: six work-groups of a
-// compute unit hide each other's start and end, and groups are padded less)
+// Tiles of 64 x 128 in slices of 16 rows (24 KiB of LDS and 120 registers: four
+// work-groups of a compute unit hide each other's start and end, and groups are
+// padded less)
 // where there are 4 for every compute unit; else 64 x 64, but 32 x 32 with 4
 // sets of waves over the rows where those leave compute units without a tile
 // and the groups are long.  Measured in that order (us):
-//    8 groups, 8192 rows by 1024 x 2048         245   258   396
-//    63 groups, 3351 rows by 913 x 896           71    99   384
-//    32 groups, 1500 rows by 257 x 1000          19    22    77
-//    12 groups, 4096 rows by 512 x 1024          53    40    76
-//    8 groups, 1024 rows by 256 x 512            15     9    11
-//    3 groups, 4096 rows by 512 x 512            84    50    25
-//    1 group of 16384 rows by 64 x 64           473   268    73
+//    8 groups, 8192 rows by 1024 x 2048         261   278   423
+//    63 groups, 3351 rows by 913 x 896           82   111   411
+//    32 groups, 1500 rows by 257 x 1000          19    23    78
+//    12 groups, 4096 rows by 512 x 1024          51    43    83
+//    8 groups, 1024 rows by 256 x 512            16    10    12
+//    3 groups, 4096 rows by 512 x 512           107    56    30
+//    1 group of 16384 rows by 64 x 64           760   392   124
 hipError_t launch_grouped_k(const GroupedArgs &p, int cus, hipStream_t s) {
   const long m64 = (p.M + 63) / 64, n128 = (p.N + 127) / 128, n64 = (p.N + 63) / 64;
   // Groups of a few rows leave little but the writing of C.  Unless each row of C

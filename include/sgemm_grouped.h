@@ -70,8 +70,9 @@ int sgemm_run_grouped(int transB, int64_t groups, int64_t M, int64_t N, int64_t 
  * For every group g, over its rows r:
  *   C_g = alpha * sum_r A(r, :)^T B(r, :) + beta * C_g
  * A is K x M (lda >= max(1, M)), B is K x N (ldb >= max(1, N)); C_g is M x N
- * (ldc >= max(1, N)) and starts g * strideC floats after C, the matrices of
- * different groups disjoint (groups > 1: strideC >= (M - 1) * ldc + N).
+ * (ldc >= max(1, N)) and starts g * strideC floats after C (strideC >= 0),
+ * the matrices of different groups disjoint (groups > 1: strideC >=
+ * (M - 1) * ldc + N).
  * With A a layer's input and B its output's gradient this is the gradient of
  * each expert's weights.  An empty group leaves beta * C_g (zeros when
  * beta == 0).  M == 0, N == 0 or groups == 0 is a no-op.
