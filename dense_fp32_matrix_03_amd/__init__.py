@@ -20,6 +20,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libsgemm.so")
 HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "sgemm.h")
 MXFP4_HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "sgemm_mxfp4.h")
+INT8_HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "sgemm_int8.h")
 
 
 def _header_constants(path: str = HEADER_PATH) -> dict:
@@ -35,9 +36,9 @@ SGEMM_OK = _C["SGEMM_OK"]
 VARIANTS = {k[len("SGEMM_VARIANT_"):].lower(): v for k, v in _C.items()
             if k.startswith("SGEMM_VARIANT_")}
 NUM_VARIANTS = _C["SGEMM_NUM_VARIANTS"]
-# Element types of operands: "f32", "bf16", "mxfp4".
-TYPES = {k[len("SGEMM_TYPE_"):].lower(): v
-         for k, v in _header_constants(MXFP4_HEADER_PATH).items() if k.startswith("SGEMM_TYPE_")}
+# Element types of operands: "f32", "bf16", "mxfp4", "int8".
+TYPES = {k[len("SGEMM_TYPE_"):].lower(): v for path in (MXFP4_HEADER_PATH, INT8_HEADER_PATH)
+         for k, v in _header_constants(path).items() if k.startswith("SGEMM_TYPE_")}
 
 
 class SgemmError(RuntimeError):
@@ -105,6 +106,17 @@ def load_library(path: str = LIB_PATH):
     lib.sgemm_run_mxfp4.restype = ci
     lib.sgemm_run_mxfp4_grouped.argtypes = [i64] + mxfp4_args + [vp, vp, i64, vp]
     lib.sgemm_run_mxfp4_grouped.restype = ci
+    lib.sgemm_int8_codes_size.argtypes = [i64, i64]
+    lib.sgemm_int8_codes_size.restype = i64
+    lib.sgemm_int8_workspace_size.argtypes = [ci, i64, i64]
+    lib.sgemm_int8_workspace_size.restype = i64
+    lib.sgemm_int8_quantize.argtypes = [ci, i64, i64, ci, vp, i64, vp, i64, vp, vp]
+    lib.sgemm_int8_quantize.restype = ci
+    int8_args = [i64, i64, i64, f32, ci, vp, i64, vp, vp, i64, vp, f32, ci, vp, i64]
+    lib.sgemm_run_int8.argtypes = int8_args + [vp, i64, vp]
+    lib.sgemm_run_int8.restype = ci
+    lib.sgemm_run_int8_grouped.argtypes = [i64] + int8_args + [vp, vp, i64, vp]
+    lib.sgemm_run_int8_grouped.restype = ci
     lib.vector_add.argtypes = [i64, vp, vp, vp, vp]
     lib.vector_add.restype = ci
     lib.sgemm_mfma_ceiling.argtypes = [ci, ci, vp, i64, ctypes.POINTER(ctypes.c_double), vp]
@@ -339,6 +351,44 @@ def sgemm_run_mxfp4_grouped(groups, M, N, K, alpha, typeA, A, lda, scalesA, B, s
     _check("sgemm_run_mxfp4_grouped", load_library().sgemm_run_mxfp4_grouped(
         groups, M, N, K, float(alpha), _type(typeA), _ptr(A), lda, _ptr(scalesA), _ptr(B),
         _ptr(scalesB), ldsb, float(beta), _type(typeC), _ptr(C), ldc, _offsets(offsets, groups),
+        _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def sgemm_int8_codes_size(rows, K) -> int:
+    """Bytes of the codes of a held rows x K matrix, ldq = K padded to 128 (include/sgemm_int8.h)."""
+    return _size("sgemm_int8_codes_size", rows, K)
+
+
+def sgemm_int8_workspace_size(typeA, M, K) -> int:
+    """Workspace bytes of an 8-bit product whose A has type `typeA`."""
+    return _size("sgemm_int8_workspace_size", _type(typeA), M, K)
+
+
+def sgemm_int8_quantize(trans, rows, K, type, X, ldx, codes, ldq, scales, stream=None) -> None:
+    """Cast X (rows x K, or with trans stored K x rows; type "f32" or "bf16") to 8-bit integers
+    with a scale for each row."""
+    _check("sgemm_int8_quantize", load_library().sgemm_int8_quantize(
+        int(trans), rows, K, _type(type), _ptr(X), ldx, _ptr(codes), ldq, _ptr(scales),
+        _stream(stream)))
+
+
+def sgemm_run_int8(M, N, K, alpha, typeA, A, lda, scalesA, B, ldb, scalesB, beta, typeC, C, ldc,
+                   workspace=None, workspace_bytes=0, stream=None) -> None:
+    """C = alpha A B^T + beta C with B (and, for typeA "int8", A) held in 8-bit integers; an "f32"
+    or "bf16" A is cast on the way."""
+    _check("sgemm_run_int8", load_library().sgemm_run_int8(
+        M, N, K, float(alpha), _type(typeA), _ptr(A), lda, _ptr(scalesA), _ptr(B), ldb,
+        _ptr(scalesB), float(beta), _type(typeC), _ptr(C), ldc, _ptr(workspace), workspace_bytes,
+        _stream(stream)))
+
+
+def sgemm_run_int8_grouped(groups, M, N, K, alpha, typeA, A, lda, scalesA, B, ldb, scalesB, beta,
+                           typeC, C, ldc, offsets, workspace=None, workspace_bytes=0,
+                           stream=None) -> None:
+    """sgemm_run_int8 for rows in groups, group g with rows g N .. of B."""
+    _check("sgemm_run_int8_grouped", load_library().sgemm_run_int8_grouped(
+        groups, M, N, K, float(alpha), _type(typeA), _ptr(A), lda, _ptr(scalesA), _ptr(B), ldb,
+        _ptr(scalesB), float(beta), _type(typeC), _ptr(C), ldc, _offsets(offsets, groups),
         _ptr(workspace), workspace_bytes, _stream(stream)))
 
 

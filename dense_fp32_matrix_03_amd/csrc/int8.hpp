@@ -1,0 +1,94 @@
+// int8.hpp -- matrices held in 8-bit integers with a scale for each row
+// (include/sgemm_int8.h): device helpers and host-side launchers.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "common.hpp"
+#include "mxfp4.hpp"  // load8: eight values of either type
+
+namespace sgemm {
+
+inline long int8_kp(long K) { return (K + 127) / 128 * 128; }
+
+struct Int8CastArgs {
+  int rows, K;
+  long ldx;
+  const void *X;
+  char *codes;
+  long ldq;
+  float *scales;
+};
+
+hipError_t launch_int8_quantize(bool trans, bool bf16, const Int8CastArgs &p, hipStream_t s);
+
+// A held matrix.
+struct Int8Matrix {
+  const char *codes;
+  const float *scales;
+  long ld;
+};
+
+// C = alpha A B^T + beta C over held operands; or A of values that the kernel
+// casts (a.codes points to them and a.ld is their leading dimension).  offsets:
+// null, or the groups of sgemm_run_int8_grouped.
+struct Int8Args {
+  int M, N, K, groups;
+  float alpha, beta;
+  Int8Matrix a, b;
+  void *C;
+  long ldc;
+  const int64_t *offsets;
+};
+
+// Whether the product's kernel is to cast A itself: only then may a_type below
+// be other than SGEMM_TYPE_INT8.
+bool int8_casts(const Int8Args &p, int cus);
+// Picks the kernel for the product.
+hipError_t launch_int8_product(const Int8Args &p, int a_type, bool c_bf16, int cus, hipStream_t s);
+// int8_tile.hip: tiles through LDS; A held.
+hipError_t launch_int8_tile(const Int8Args &p, bool c_bf16, int cus, hipStream_t s);
+
+typedef int i32x16 __attribute__((ext_vector_type(16)));
+
+// The scale of a row whose largest magnitude has the bits `top`: NaN where that
+// is an infinity or a NaN.  The division is the correctly rounded one.
+__device__ __forceinline__ float int8_scale(unsigned top) {
+  return top >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : __uint_as_float(top) / 127.0f;
+}
+
+// What a row's casts share: the scale, and an estimate of its reciprocal.  Codes
+// are 0 where the scale is 0 or NaN.
+struct Int8Scale {
+  float scale, inverse;
+  bool zero;
+  __device__ __forceinline__ explicit Int8Scale(float s) : scale(s), inverse(1.0f / s) {
+    zero = !(s > 0.f);
+  }
+  // The whole number nearest to x / scale, halves to the even one.  x times the
+  // reciprocal is off by at most 127 2 2^-24, so q is the nearest or, next
+  // to a half, the other one; x - q scale is exact (a multiple of the smaller of
+  // the two's units, below scale in magnitude), and says which.  Scales so small
+  // that the reciprocal overflows are divided by.
+  __device__ __forceinline__ int code(float x) const {
+    if (zero) return 0;
+    float q = rintf(inverse <= 3.4028235e38f ? x * inverse : x / scale);
+    const float r = fmaf(-q, scale, x), twice = 2.f * fabsf(r);
+    const bool odd = ((int)q & 1) != 0;
+    if (twice > scale || (twice == scale && odd)) q += r > 0.f ? 1.f : -1.f;
+    return (int)fminf(fmaxf(q, -127.f), 127.f);
+  }
+};
+
+// Four codes as bytes, the first lowest.
+__device__ __forceinline__ unsigned int8_pack(int a, int b, int c, int d) {
+  return (unsigned)(a & 255) | (unsigned)(b & 255) << 8 | (unsigned)(c & 255) << 16 |
+         (unsigned)d << 24;
+}
+
+__device__ __forceinline__ float int8_value(int sum, float sa, float sb) {
+  return (float)sum * sa * sb;
+}
+
+}  // namespace sgemm

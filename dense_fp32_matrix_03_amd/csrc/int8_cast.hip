@@ -1,0 +1,141 @@
+// int8_cast.hip -- the cast of matrices to 8-bit integers with a scale for each
+// row (include/sgemm_int8.h).
+//
+// Bound by memory: a cast reads 4 (or 2) bytes a value and writes 1.
+#include "int8.hpp"
+#include "mfma_dma.hpp"
+
+namespace sgemm {
+
+namespace {
+
+// T threads (a wave, or the work-group of four) have a row, 8 consecutive values
+// of every 8 T each.  The first kHeld runs of 8 stay in registers between the
+// search for the largest magnitude and the cast; longer rows are read again,
+// from the caches.
+constexpr int kHeld = 4;
+
+template <bool BF16, int T>
+__global__ void __launch_bounds__(256) int8_quantize_kernel(Int8CastArgs p) {
+  static_assert(T == 64 || T == 256, "a wave or a work-group has a row");
+  const int t = threadIdx.x % T;
+  const long row = (long)blockIdx.x * (256 / T) + threadIdx.x / T;
+  if (T < 256 && row >= p.rows) return;  // whole waves: no barrier follows
+  const char *x = static_cast<const char *>(p.X) + row * p.ldx * (BF16 ? 2 : 4);
+  auto load = [&](int k, float v[8]) { load8<BF16, true>(x + (long)k * (BF16 ? 2 : 4), p.K - k, v); };
+  float v[kHeld][8];
+  unsigned top = 0;
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) load(8 * (t + i * T), v[i]);
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) top = max(top, magnitude_bits(v[i]));
+  for (int k = 8 * (t + kHeld * T); k < p.K; k += 8 * T) {
+    float w[8];
+    load8<BF16>(x + (long)k * (BF16 ? 2 : 4), p.K - k, w);
+    top = max(top, magnitude_bits(w));
+  }
+#pragma unroll
+  for (int d = 32; d > 0; d /= 2) top = max(top, (unsigned)__shfl_xor((int)top, d));
+  if constexpr (T == 256) {
+    __shared__ unsigned tops[4];
+    if (threadIdx.x % kWave == 0) tops[threadIdx.x / kWave] = top;
+    __syncthreads();
+    top = max(max(tops[0], tops[1]), max(tops[2], tops[3]));
+  }
+  const Int8Scale s(int8_scale(top));
+  if (t == 0) p.scales[row] = s.scale;
+  const int kp = (p.K + 127) / 128 * 128;
+  char *codes = p.codes + row * p.ldq;
+  auto store = [&](int k, const float w[8]) {
+    if (k >= kp) return;
+    uint2 c;
+    c.x = int8_pack(s.code(w[0]), s.code(w[1]), s.code(w[2]), s.code(w[3]));
+    c.y = int8_pack(s.code(w[4]), s.code(w[5]), s.code(w[6]), s.code(w[7]));
+    *reinterpret_cast<uint2 *>(codes + k) = c;
+  };
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) store(8 * (t + i * T), v[i]);
+  for (int k = 8 * (t + kHeld * T); k < kp; k += 8 * T) {
+    float w[8];
+    load8<BF16>(x + (long)k * (BF16 ? 2 : 4), p.K - k, w);
+    store(k, w);
+  }
+}
+
+// Values stored transposed: a work-group has 32 rows (neighbouring columns of X),
+// 8 threads each; a thread takes 16 consecutive k of every 128.  Loads of 32
+// lanes adjoin.  Two passes: X is read twice.
+template <bool BF16>
+__global__ void __launch_bounds__(256) int8_quantize_transposed_kernel(Int8CastArgs p) {
+  const int c = threadIdx.x % 32, part = threadIdx.x / 32;
+  const long row = (long)blockIdx.x * 32 + c;
+  // Every thread loads, from the nearest element there is, so that the loads go
+  // out together; what lies past K or the last row is then dropped.
+  const long col = min(row, (long)p.rows - 1);
+  auto load = [&](int k0, float v[16]) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const long at = (long)min(k0 + e, p.K - 1) * p.ldx + col;
+      if constexpr (BF16)
+        v[e] = __uint_as_float((unsigned)static_cast<const unsigned short *>(p.X)[at] << 16);
+      else
+        v[e] = static_cast<const float *>(p.X)[at];
+    }
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] = k0 + e < p.K ? v[e] : 0.f;
+  };
+  unsigned top = 0;
+  for (int k = part * 16; k < p.K; k += 128) {
+    float v[16];
+    load(k, v);
+    top = max(top, max(magnitude_bits(v), magnitude_bits(v + 8)));
+  }
+  __shared__ unsigned tops[8][32];
+  tops[part][c] = top;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = max(top, tops[i][c]);
+  if (row >= p.rows) return;
+  const Int8Scale s(int8_scale(top));
+  if (part == 0) p.scales[row] = s.scale;
+  const int kp = (p.K + 127) / 128 * 128;
+  for (int k = part * 16; k < kp; k += 128) {
+    float v[16];
+    load(k, v);
+    uint4 q;
+    unsigned *w = &q.x;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      w[e] = int8_pack(s.code(v[4 * e]), s.code(v[4 * e + 1]), s.code(v[4 * e + 2]),
+                       s.code(v[4 * e + 3]));
+    *reinterpret_cast<uint4 *>(p.codes + row * p.ldq + k) = q;
+  }
+}
+
+}  // namespace
+
+hipError_t launch_int8_quantize(bool trans, bool bf16, const Int8CastArgs &p, hipStream_t s) {
+  const dim3 block(256);
+  if (trans) {
+    const dim3 grid((unsigned)((p.rows + 31L) / 32));
+    if (bf16)
+      hipLaunchKernelGGL(int8_quantize_transposed_kernel<true>, grid, block, 0, s, p);
+    else
+      hipLaunchKernelGGL(int8_quantize_transposed_kernel<false>, grid, block, 0, s, p);
+  } else if (p.K > 1024) {
+    const dim3 grid((unsigned)p.rows);
+    if (bf16)
+      hipLaunchKernelGGL((int8_quantize_kernel<true, 256>), grid, block, 0, s, p);
+    else
+      hipLaunchKernelGGL((int8_quantize_kernel<false, 256>), grid, block, 0, s, p);
+  } else {
+    const dim3 grid((unsigned)((p.rows + 3L) / 4));
+    if (bf16)
+      hipLaunchKernelGGL((int8_quantize_kernel<true, 64>), grid, block, 0, s, p);
+    else
+      hipLaunchKernelGGL((int8_quantize_kernel<false, 64>), grid, block, 0, s, p);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace sgemm

@@ -1,0 +1,125 @@
+// int8_tile.hip -- products of matrices held in 8-bit integers on tiles through
+// LDS (slice_tile.hpp).
+//
+// C(m, n) = alpha sa(m) sb(n) sum_k a(m, k) b(n, k) + beta C(m, n), on
+// v_mfma_i32_32x32x32_i8: 32 rows of A by 32 rows of B over 32 k, lane half h
+// supplying 16 codes of row l % 32 of each operand.  A slice is 128 k: half h has
+// its chunks 4 h .. 4 h + 3 and instruction s the s-th of them (which k an
+// instruction adds does not matter, as long as A and B agree).
+#include <math.h>
+
+#include "grouped_map.hpp"
+#include "int8.hpp"
+#include "slice_tile.hpp"
+
+namespace sgemm {
+
+namespace {
+
+struct Int8Format {
+  typedef i32x16 Acc;
+  typedef slice_i32x4 Frag;
+  static constexpr int kSteps = 4, kReads = 1, kMfma = 1;
+  template <int S, class At>
+  __device__ __forceinline__ static Frag load(int half, At at) {
+    return *at(4 * half + S);
+  }
+  __device__ __forceinline__ static void mma(const Frag &a, const Frag &b, Acc &c) {
+    c = __builtin_amdgcn_mfma_i32_32x32x32_i8(a, b, c, 0, 0, 0);
+  }
+};
+
+template <int BM, int BN, int WM, int WN, int KS, bool CBF16>
+__global__ void __launch_bounds__(WM *WN *KS *kWave, 2)
+int8_tile_kernel(Int8Args p, TileMap tmap, GroupMap map) {
+  using Tile = SliceTile<Int8Format, BM, BN, WM, WN, KS>;
+  constexpr int FM = Tile::FM, FN = Tile::FN;
+  const int lane = threadIdx.x % kWave, r32 = lane % 32, half = lane / 32;
+
+  long a_row = 0, b_row = 0;  // first row of the group in A (and C), and of its B
+  int m0, n0, m_end = p.M;
+  if (p.offsets) {
+    const GroupTile t = group_tile(p.offsets, p.groups, p.M, BM, map);
+    if (!t.valid) return;
+    a_row = t.row0;
+    b_row = (long)t.g * p.N;
+    m0 = t.tm * BM;
+    n0 = t.tn * BN;
+    m_end = t.rows;
+  } else {
+    int bidx, tm, tn;
+    tmap.tile(xcd_contiguous_id(blockIdx.x, gridDim.x), bidx, tm, tn);
+    m0 = tm * BM;
+    n0 = tn * BN;
+  }
+  const int rows_a = min(BM, m_end - m0), rows_b = min(BN, p.N - n0);
+  i32x16 acc[FM][FN];
+  if (!Tile::run(p.a.codes + (a_row + m0) * p.a.ld, (int)p.a.ld, rows_a,
+                 p.b.codes + (b_row + n0) * p.b.ld, (int)p.b.ld, rows_b, (p.K + 127) / 128, acc))
+    return;
+
+  // Register e of lane l holds row acc32_row(l, e), column l % 32 of a block:
+  // row 4 (l / 32) of a uniform base and a constant number of rows past it.
+  using T = std::conditional_t<CBF16, __bf16, float>;
+  const int mt = Tile::row0() + 4 * half, nt = Tile::col0() + r32;  // inside the tile
+  T *const C = static_cast<T *>(p.C) + (a_row + m0 + mt) * p.ldc + n0 + nt;
+  const int rows = rows_a - mt, cols = rows_b - nt;
+  const bool sums = p.K > 0;  // without k there are no scales either
+  const float *sa = p.a.scales + a_row + m0 + mt, *sb = p.b.scales + b_row + n0 + nt;
+  float scale_b[FN];
+#pragma unroll
+  for (int j = 0; j < FN; ++j) scale_b[j] = sums && j * 32 < cols ? sb[j * 32] : 0.f;
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int quad = 0; quad < 4; ++quad) {
+      const int r0 = i * 32 + 8 * quad;
+      float scale_a[4], c[4][FN];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) scale_a[e] = sums && r0 + e < rows ? sa[r0 + e] : 0.f;
+      if (p.beta != 0.f) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int j = 0; j < FN; ++j)
+            c[e][j] = r0 + e < rows && j * 32 < cols ? (float)C[(r0 + e) * p.ldc + j * 32] : 0.f;
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (r0 + e >= rows) continue;
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+          if (j * 32 >= cols) continue;
+          const float v = int8_value(acc[i][j][4 * quad + e], scale_a[e], scale_b[j]);
+          C[(r0 + e) * p.ldc + j * 32] =
+              (T)(p.beta != 0.f ? fmaf(p.alpha, v, p.beta * c[e][j]) : p.alpha * v);
+        }
+      }
+    }
+}
+
+template <int BM, int BN, int WM, int WN, int KS>
+hipError_t launch(const Int8Args &p, bool c_bf16, hipStream_t s) {
+  const int tiles_m = (p.M + BM - 1) / BM, tiles_n = (p.N + BN - 1) / BN;
+  const long rows = p.offsets ? group_tile_rows(p.M, p.groups, BM) : tiles_m;
+  const dim3 grid((unsigned)(rows * tiles_n)), block(WM * WN * KS * kWave);
+  const TileMap tmap = make_tile_map(tiles_m, tiles_n, kGroupRaster);
+  const GroupMap map = make_group_map(tiles_n);
+  if (c_bf16)
+    hipLaunchKernelGGL((int8_tile_kernel<BM, BN, WM, WN, KS, true>), grid, block, 0, s, p, tmap,
+                       map);
+  else
+    hipLaunchKernelGGL((int8_tile_kernel<BM, BN, WM, WN, KS, false>), grid, block, 0, s, p, tmap,
+                       map);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+bool int8_casts(const Int8Args &, int) { return false; }
+
+hipError_t launch_int8_product(const Int8Args &p, int, bool c_bf16, int, hipStream_t s) {
+  return launch<64, 64, 2, 2, 1>(p, c_bf16, s);
+}
+
+}  // namespace sgemm
