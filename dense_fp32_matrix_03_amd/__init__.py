@@ -20,6 +20,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libsgemm.so")
 HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "sgemm.h")
 MXFP4_HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "sgemm_mxfp4.h")
+ROUTE_HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "sgemm_route.h")
 INT8_HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "sgemm_int8.h")
 
 
@@ -39,6 +40,9 @@ NUM_VARIANTS = _C["SGEMM_NUM_VARIANTS"]
 # Element types of operands: "f32", "bf16", "mxfp4", "int8".
 TYPES = {k[len("SGEMM_TYPE_"):].lower(): v for path in (MXFP4_HEADER_PATH, INT8_HEADER_PATH)
          for k, v in _header_constants(path).items() if k.startswith("SGEMM_TYPE_")}
+# How sgemm_route makes scores of logits: "softmax", "sigmoid".
+SCORES = {k[len("SGEMM_SCORE_"):].lower(): v
+          for k, v in _header_constants(ROUTE_HEADER_PATH).items() if k.startswith("SGEMM_SCORE_")}
 
 
 class SgemmError(RuntimeError):
@@ -117,6 +121,22 @@ def load_library(path: str = LIB_PATH):
     lib.sgemm_run_int8.restype = ci
     lib.sgemm_run_int8_grouped.argtypes = [i64] + int8_args + [vp, vp, i64, vp]
     lib.sgemm_run_int8_grouped.restype = ci
+    route_args = [i64, i64, i64, ci, ci, vp, i64]
+    lib.sgemm_route.argtypes = route_args + [vp, i64, i64, i64, ci, f32, vp, vp, vp]
+    lib.sgemm_route.restype = ci
+    lib.sgemm_route_backward.argtypes = route_args + [ci, f32, vp, vp, vp, i64, vp]
+    lib.sgemm_route_backward.restype = ci
+    lib.sgemm_route_plan_workspace_size.argtypes = [i64, i64]
+    lib.sgemm_route_plan_workspace_size.restype = i64
+    lib.sgemm_route_plan.argtypes = [i64, i64, i64, vp, vp, vp, vp, vp, i64, vp]
+    lib.sgemm_route_plan.restype = ci
+    rows_args = [i64, i64, i64, i64, ci, vp, i64]
+    lib.sgemm_rows_gather.argtypes = rows_args + [vp, vp, vp, i64, vp]
+    lib.sgemm_rows_gather.restype = ci
+    lib.sgemm_rows_combine.argtypes = rows_args + [vp, vp, vp, i64, vp]
+    lib.sgemm_rows_combine.restype = ci
+    lib.sgemm_rows_combine_backward.argtypes = rows_args + [vp, i64, vp, vp, vp, i64, vp, vp]
+    lib.sgemm_rows_combine_backward.restype = ci
     lib.vector_add.argtypes = [i64, vp, vp, vp, vp]
     lib.vector_add.restype = ci
     lib.sgemm_mfma_ceiling.argtypes = [ci, ci, vp, i64, ctypes.POINTER(ctypes.c_double), vp]
@@ -184,6 +204,10 @@ def _type(t) -> int:
     return TYPES[t] if isinstance(t, str) else int(t)
 
 
+def _score(s) -> int:
+    return SCORES[s] if isinstance(s, str) else int(s)
+
+
 def _offsets(x, groups=0):
     """_ptr of group offsets, which the kernels read as groups + 1 64-bit integers."""
     if hasattr(x, "dtype"):
@@ -193,6 +217,18 @@ def _offsets(x, groups=0):
             raise ValueError("offsets must be contiguous")
         if groups > 0 and x.numel() <= groups:
             raise ValueError(f"offsets must hold groups + 1 = {groups + 1} values, not {x.numel()}")
+    return _ptr(x)
+
+
+def _typed(x, name, dtype, size=0):
+    """_ptr of `size` contiguous 32-bit values, of which the kernels know only the address."""
+    if hasattr(x, "dtype"):
+        if str(x.dtype) != "torch." + dtype:
+            raise TypeError(f"{name} must be {dtype}")
+        if not x.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if x.numel() < size:
+            raise ValueError(f"{name} must hold {size} values, not {x.numel()}")
     return _ptr(x)
 
 
@@ -368,8 +404,13 @@ def sgemm_int8_quantize(trans, rows, K, type, X, ldx, codes, ldq, scales, stream
     """Cast X (rows x K, or with trans stored K x rows; type "f32" or "bf16") to 8-bit integers
     with a scale for each row."""
     _check("sgemm_int8_quantize", load_library().sgemm_int8_quantize(
-        int(trans), rows, K, _type(type), _ptr(X), ldx, _ptr(codes), ldq, _ptr(scales),
-        _stream(stream)))
+        int(trans), rows, K, _type(type), _ptr(X), ldx, _ptr(codes), ldq,
+        _typed(scales, "scales", "float32", rows), _stream(stream)))
+
+
+def _scales_a(typeA, scales, M):
+    """A's scales, which are read only where A is held."""
+    return _typed(scales, "scalesA", "float32", M if _type(typeA) == TYPES["int8"] else 0)
 
 
 def sgemm_run_int8(M, N, K, alpha, typeA, A, lda, scalesA, B, ldb, scalesB, beta, typeC, C, ldc,
@@ -377,9 +418,9 @@ def sgemm_run_int8(M, N, K, alpha, typeA, A, lda, scalesA, B, ldb, scalesB, beta
     """C = alpha A B^T + beta C with B (and, for typeA "int8", A) held in 8-bit integers; an "f32"
     or "bf16" A is cast on the way."""
     _check("sgemm_run_int8", load_library().sgemm_run_int8(
-        M, N, K, float(alpha), _type(typeA), _ptr(A), lda, _ptr(scalesA), _ptr(B), ldb,
-        _ptr(scalesB), float(beta), _type(typeC), _ptr(C), ldc, _ptr(workspace), workspace_bytes,
-        _stream(stream)))
+        M, N, K, float(alpha), _type(typeA), _ptr(A), lda, _scales_a(typeA, scalesA, M), _ptr(B),
+        ldb, _typed(scalesB, "scalesB", "float32", N), float(beta), _type(typeC), _ptr(C), ldc,
+        _ptr(workspace), workspace_bytes, _stream(stream)))
 
 
 def sgemm_run_int8_grouped(groups, M, N, K, alpha, typeA, A, lda, scalesA, B, ldb, scalesB, beta,
@@ -387,9 +428,73 @@ def sgemm_run_int8_grouped(groups, M, N, K, alpha, typeA, A, lda, scalesA, B, ld
                            stream=None) -> None:
     """sgemm_run_int8 for rows in groups, group g with rows g N .. of B."""
     _check("sgemm_run_int8_grouped", load_library().sgemm_run_int8_grouped(
-        groups, M, N, K, float(alpha), _type(typeA), _ptr(A), lda, _ptr(scalesA), _ptr(B), ldb,
-        _ptr(scalesB), float(beta), _type(typeC), _ptr(C), ldc, _offsets(offsets, groups),
+        groups, M, N, K, float(alpha), _type(typeA), _ptr(A), lda, _scales_a(typeA, scalesA, M),
+        _ptr(B), ldb, _typed(scalesB, "scalesB", "float32", groups * N), float(beta), _type(typeC),
+        _ptr(C), ldc, _offsets(offsets, groups), _ptr(workspace), workspace_bytes,
+        _stream(stream)))
+
+
+def sgemm_route(tokens, experts, topk, score, type, logits, ldl, bias, groups, topk_groups,
+                group_top, renormalize, scale, picks, weights, stream=None) -> None:
+    """The topk experts of each token and their weights, from logits (include/sgemm_route.h);
+    score: "softmax" or "sigmoid", picks int32, weights float32, tokens x topk."""
+    _check("sgemm_route", load_library().sgemm_route(
+        tokens, experts, topk, _score(score), _type(type), _ptr(logits), ldl,
+        _typed(bias, "bias", "float32", experts), groups, topk_groups, group_top,
+        int(renormalize), float(scale), _typed(picks, "picks", "int32", tokens * topk),
+        _typed(weights, "weights", "float32", tokens * topk), _stream(stream)))
+
+
+def sgemm_route_backward(tokens, experts, topk, score, type, logits, ldl, renormalize, scale, picks,
+                         dweights, dlogits, ldd, stream=None) -> None:
+    """The gradient of sgemm_route's weights with respect to its logits."""
+    _check("sgemm_route_backward", load_library().sgemm_route_backward(
+        tokens, experts, topk, _score(score), _type(type), _ptr(logits), ldl, int(renormalize),
+        float(scale), _typed(picks, "picks", "int32", tokens * topk),
+        _typed(dweights, "dweights", "float32", tokens * topk), _ptr(dlogits), ldd,
+        _stream(stream)))
+
+
+def sgemm_route_plan_workspace_size(pairs, groups) -> int:
+    """Workspace bytes of sgemm_route_plan."""
+    return _size("sgemm_route_plan_workspace_size", pairs, groups)
+
+
+def sgemm_route_plan(pairs, first, groups, picks, offsets, sources, places, workspace=None,
+                     workspace_bytes=0, stream=None) -> None:
+    """Sort pairs (token, pick) by expert: the groups' offsets (int64), the pair of each row and
+    the row of each pair (int32)."""
+    _check("sgemm_route_plan", load_library().sgemm_route_plan(
+        pairs, first, groups, _typed(picks, "picks", "int32", pairs), _offsets(offsets, groups),
+        _typed(sources, "sources", "int32", pairs), _typed(places, "places", "int32", pairs),
         _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def sgemm_rows_gather(rows, pairs, topk, N, type, X, ldx, sources, weights, Y, ldy,
+                      stream=None) -> None:
+    """Y(r, :) = weights[sources[r]] X(sources[r] / topk, :), weights None for ones."""
+    _check("sgemm_rows_gather", load_library().sgemm_rows_gather(
+        rows, pairs, topk, N, _type(type), _ptr(X), ldx, _typed(sources, "sources", "int32", rows),
+        _typed(weights, "weights", "float32", pairs), _ptr(Y), ldy, _stream(stream)))
+
+
+def sgemm_rows_combine(tokens, topk, rows, N, type, X, ldx, places, weights, Y, ldy,
+                       stream=None) -> None:
+    """Y(t, :) = sum_j weights[t, j] X(places[t, j], :), weights None for ones."""
+    _check("sgemm_rows_combine", load_library().sgemm_rows_combine(
+        tokens, topk, rows, N, _type(type), _ptr(X), ldx,
+        _typed(places, "places", "int32", tokens * topk),
+        _typed(weights, "weights", "float32", tokens * topk), _ptr(Y), ldy, _stream(stream)))
+
+
+def sgemm_rows_combine_backward(tokens, topk, rows, N, type, X, ldx, dY, lddy, places, weights, dX,
+                                lddx, dweights, stream=None) -> None:
+    """The gradients dX and dweights (either may be None) of sgemm_rows_combine."""
+    pairs = tokens * topk
+    _check("sgemm_rows_combine_backward", load_library().sgemm_rows_combine_backward(
+        tokens, topk, rows, N, _type(type), _ptr(X), ldx, _ptr(dY), lddy,
+        _typed(places, "places", "int32", pairs), _typed(weights, "weights", "float32", pairs),
+        _ptr(dX), lddx, _typed(dweights, "dweights", "float32", pairs), _stream(stream)))
 
 
 def vector_add(n, A, B, C, stream=None) -> None:

@@ -1,0 +1,228 @@
+// rows.hip -- rows gathered by expert, brought back to their tokens, and the
+// gradients of that (include/sgemm_route.h).
+//
+// Bound by memory.  A wave has a piece of up to 4096 bytes of a row, 16 bytes a
+// lane in each of four loads that go out together.
+#include "mxfp4.hpp"
+#include "route.hpp"
+
+namespace sgemm {
+
+namespace {
+
+constexpr int kUnits = 4;  // waves of a work-group
+
+// 16 bytes of a row, at any element: V values, zeros and no access past the n-th.
+template <bool BF16>
+struct Piece {
+  static constexpr int V = BF16 ? 8 : 4;
+  using T = std::conditional_t<BF16, unsigned short, float>;
+  using Raw = std::conditional_t<BF16, u32x4_any, f32x4_any>;
+  Raw raw;
+  __device__ __forceinline__ void load(const void *row, long at, int n) {
+    const T *x = static_cast<const T *>(row) + at;
+    if (n >= V) {
+      raw = *reinterpret_cast<const Raw *>(x);
+    } else {
+      T v[V];
+#pragma unroll
+      for (int e = 0; e < V; ++e) v[e] = e < n ? x[e] : T(0);
+      __builtin_memcpy(&raw, v, 16);
+    }
+  }
+  __device__ __forceinline__ void store(void *row, long at, int n) const {
+    T *x = static_cast<T *>(row) + at;
+    if (n >= V) {
+      *reinterpret_cast<Raw *>(x) = raw;
+    } else {
+      T v[V];
+      __builtin_memcpy(v, &raw, 16);
+#pragma unroll
+      for (int e = 0; e < V; ++e)
+        if (e < n) x[e] = v[e];
+    }
+  }
+  __device__ __forceinline__ void get(float v[V]) const {
+    if constexpr (BF16) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[2 * e] = __uint_as_float(raw[e] << 16);
+        v[2 * e + 1] = __uint_as_float(raw[e] & 0xffff0000u);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = raw[e];
+    }
+  }
+  __device__ __forceinline__ void set(const float v[V]) {
+    if constexpr (BF16) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        raw[e] = __builtin_bit_cast(unsigned short, (__bf16)v[2 * e]) |
+                 (unsigned)__builtin_bit_cast(unsigned short, (__bf16)v[2 * e + 1]) << 16;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) raw[e] = v[e];
+    }
+  }
+};
+
+// The unit (row and piece of it) of a wave; false past the last.
+__device__ __forceinline__ bool unit_of(const RowsArgs &p, long &row, int &piece) {
+  const int u = blockIdx.x * kUnits + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int r = p.by_pieces(u);
+  row = r;
+  piece = u - r * p.pieces;
+  return r < p.rows;
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(kUnits *kWave) rows_gather_kernel(RowsArgs p) {
+  using P = Piece<BF16>;
+  long r;
+  int piece;
+  if (!unit_of(p, r, piece)) return;
+  const int source = p.index[r];
+  if (source < 0 || source >= p.limit) return;
+  const int lane = threadIdx.x % kWave;
+  const int n0 = piece * (kRowPiece / 16 * P::V) + lane * P::V;
+  const long x = (long)(source / p.topk) * p.ldx, y = r * p.ldy;
+  P v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int n = n0 + i * kWave * P::V;
+    v[i].load(p.X, x + n, p.N - n);
+  }
+  if (p.weights) {
+    const float w = p.weights[source];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float f[P::V];
+      v[i].get(f);
+#pragma unroll
+      for (int e = 0; e < P::V; ++e) f[e] *= w;
+      v[i].set(f);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int n = n0 + i * kWave * P::V;
+    v[i].store(p.Y, y + n, p.N - n);
+  }
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(kUnits *kWave) rows_combine_kernel(RowsArgs p) {
+  using P = Piece<BF16>;
+  long t;
+  int piece;
+  if (!unit_of(p, t, piece)) return;
+  const int lane = threadIdx.x % kWave;
+  const int n0 = piece * (kRowPiece / 16 * P::V) + lane * P::V;
+  float sum[4][P::V];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int e = 0; e < P::V; ++e) sum[i][e] = 0.f;
+  for (int j = 0; j < p.topk; ++j) {
+    const long pair = t * p.topk + j;
+    const int place = p.index[pair];
+    if (place < 0 || place >= p.limit) continue;
+    const float w = p.weights ? p.weights[pair] : 1.f;
+    P v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int n = n0 + i * kWave * P::V;
+      v[i].load(p.X, place * p.ldx + n, p.N - n);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float f[P::V];
+      v[i].get(f);
+#pragma unroll
+      for (int e = 0; e < P::V; ++e) sum[i][e] = fmaf(w, f[e], sum[i][e]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int n = n0 + i * kWave * P::V;
+    P v;
+    v.set(sum[i]);
+    v.store(p.Y, t * p.ldy + n, p.N - n);
+  }
+}
+
+// A wave has a pair.
+template <bool BF16>
+__global__ void __launch_bounds__(kUnits *kWave) rows_combine_backward_kernel(RowsBackArgs p) {
+  using P = Piece<BF16>;
+  const long pair = (long)blockIdx.x * kUnits + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  if (pair >= p.pairs) return;
+  const int lane = threadIdx.x % kWave;
+  const int place = p.places[pair];
+  if (place < 0 || place >= p.rows) {
+    if (p.dweights && lane == 0) p.dweights[pair] = 0.f;
+    return;
+  }
+  const long dy = pair / p.topk * p.lddy;
+  const float w = p.weights ? p.weights[pair] : 1.f;
+  float dot = 0.f;
+  for (int n = lane * P::V; n < p.N; n += kWave * P::V) {
+    P v;
+    float g[P::V];
+    v.load(p.dY, dy + n, p.N - n);
+    v.get(g);
+    if (p.dweights) {
+      P x;
+      float f[P::V];
+      x.load(p.X, place * p.ldx + n, p.N - n);
+      x.get(f);
+#pragma unroll
+      for (int e = 0; e < P::V; ++e) dot = fmaf(f[e], g[e], dot);
+    }
+    if (p.dX) {
+#pragma unroll
+      for (int e = 0; e < P::V; ++e) g[e] *= w;
+      v.set(g);
+      v.store(p.dX, place * p.lddx + n, p.N - n);
+    }
+  }
+  if (p.dweights) {
+#pragma unroll
+    for (int d = 32; d > 0; d /= 2) dot += __shfl_xor(dot, d);
+    if (lane == 0) p.dweights[pair] = dot;
+  }
+}
+
+dim3 units(long n) { return dim3((unsigned)((n + kUnits - 1) / kUnits)); }
+
+}  // namespace
+
+hipError_t launch_rows_gather(const RowsArgs &p, bool bf16, hipStream_t s) {
+  const dim3 grid = units((long)p.rows * p.pieces), block(kUnits * kWave);
+  if (bf16)
+    hipLaunchKernelGGL(rows_gather_kernel<true>, grid, block, 0, s, p);
+  else
+    hipLaunchKernelGGL(rows_gather_kernel<false>, grid, block, 0, s, p);
+  return hipGetLastError();
+}
+
+hipError_t launch_rows_combine(const RowsArgs &p, bool bf16, hipStream_t s) {
+  const dim3 grid = units((long)p.rows * p.pieces), block(kUnits * kWave);
+  if (bf16)
+    hipLaunchKernelGGL(rows_combine_kernel<true>, grid, block, 0, s, p);
+  else
+    hipLaunchKernelGGL(rows_combine_kernel<false>, grid, block, 0, s, p);
+  return hipGetLastError();
+}
+
+hipError_t launch_rows_combine_backward(const RowsBackArgs &p, bool bf16, hipStream_t s) {
+  const dim3 grid = units(p.pairs), block(kUnits * kWave);
+  if (bf16)
+    hipLaunchKernelGGL(rows_combine_backward_kernel<true>, grid, block, 0, s, p);
+  else
+    hipLaunchKernelGGL(rows_combine_backward_kernel<false>, grid, block, 0, s, p);
+  return hipGetLastError();
+}
+
+}  // namespace sgemm
