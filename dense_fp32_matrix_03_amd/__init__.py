@@ -137,6 +137,11 @@ def load_library(path: str = LIB_PATH):
     lib.sgemm_rows_combine.restype = ci
     lib.sgemm_rows_combine_backward.argtypes = rows_args + [vp, i64, vp, vp, vp, i64, vp, vp]
     lib.sgemm_rows_combine_backward.restype = ci
+    lib.sgemm_orthogonalize_workspace_size.argtypes = [i64, i64, i64]
+    lib.sgemm_orthogonalize_workspace_size.restype = i64
+    lib.sgemm_orthogonalize.argtypes = [i64, i64, i64, i64, i64, ctypes.POINTER(f32), f32, f32, ci,
+                                        vp, i64, i64, ci, vp, i64, i64, vp, i64, vp]
+    lib.sgemm_orthogonalize.restype = ci
     lib.vector_add.argtypes = [i64, vp, vp, vp, vp]
     lib.vector_add.restype = ci
     lib.sgemm_mfma_ceiling.argtypes = [ci, ci, vp, i64, ctypes.POINTER(ctypes.c_double), vp]
@@ -495,6 +500,24 @@ def sgemm_rows_combine_backward(tokens, topk, rows, N, type, X, ldx, dY, lddy, p
         tokens, topk, rows, N, _type(type), _ptr(X), ldx, _ptr(dY), lddy,
         _typed(places, "places", "int32", pairs), _typed(weights, "weights", "float32", pairs),
         _ptr(dX), lddx, _typed(dweights, "dweights", "float32", pairs), _stream(stream)))
+
+
+def sgemm_orthogonalize_workspace_size(batch, M, N) -> int:
+    """Workspace bytes of sgemm_orthogonalize."""
+    return _size("sgemm_orthogonalize_workspace_size", batch, M, N)
+
+
+def sgemm_orthogonalize(batch, M, N, steps, coefficients, eps, alpha, typeX, X, ldx, strideX, typeY,
+                        Y, ldy, strideY, workspace=None, workspace_bytes=0, stream=None) -> None:
+    """Y = alpha times the Newton-Schulz iterate of each X / (|X| + eps)
+    (include/sgemm_orthogonalize.h); coefficients: a, b, c for all steps alike, or 3 * steps."""
+    n = len(coefficients)
+    if n not in (3, 3 * steps):
+        raise ValueError(f"coefficients must hold 3 or 3 * steps = {3 * steps} values, not {n}")
+    _check("sgemm_orthogonalize", load_library().sgemm_orthogonalize(
+        batch, M, N, steps, n // 3, (ctypes.c_float * n)(*coefficients), float(eps), float(alpha),
+        _type(typeX), _ptr(X), ldx, strideX, _type(typeY), _ptr(Y), ldy, strideY, _ptr(workspace),
+        workspace_bytes, _stream(stream)))
 
 
 def vector_add(n, A, B, C, stream=None) -> None:

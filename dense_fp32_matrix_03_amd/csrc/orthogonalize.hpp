@@ -1,0 +1,60 @@
+// orthogonalize.hpp -- matrices held as two half-precision pieces, and the
+// launchers of the Newton-Schulz steps on them (include/sgemm_orthogonalize.h).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "common.hpp"
+
+namespace sgemm {
+
+// A batch of matrices in pieces: rows of `pitch` bytes, 128 for each 32 columns
+// (the last 32 padded with zeros): 32 high pieces, then 32 low ones.  A value is
+// (high + low) 2^-s with an s that the host keeps.
+struct SplitMatrix {
+  char *at;
+  int rows, cols;
+  int pitch;
+  long stride;  // bytes from one matrix to the next
+};
+inline int split_pitch(long cols) { return (int)((cols + 31) / 32 * 128); }
+
+// The sum of squares, in parts, of every matrix of the batch.
+struct OrthoNormArgs {
+  int M, N;
+  const void *X;
+  long ldx, strideX;
+  double *parts;  // [batch][n_parts]
+  int n_parts;
+};
+constexpr int kNormParts = 256;
+hipError_t launch_ortho_norm(const OrthoNormArgs &p, bool bf16, int batch, hipStream_t s);
+
+// X 2^shift / (|X| + eps), in pieces, as it is and transposed.
+struct OrthoSplitArgs {
+  OrthoNormArgs x;
+  float eps;
+  int shift;
+  SplitMatrix rows, cols;  // M x N and N x M
+};
+hipError_t launch_ortho_split(const OrthoSplitArgs &p, bool bf16, int batch, hipStream_t s);
+
+// D = f1 A B^T + f2 E, of A's rows by B's rows.
+struct OrthoProductArgs {
+  SplitMatrix a, b;
+  SplitMatrix e_t;  // E transposed; at == null: none
+  float f1, f2;
+  SplitMatrix d, d_t;  // D as it is and transposed; at == null: not written
+  // The last product's D instead, in a user's type: element (m, n) at m ld + n, or
+  // at n ld + m.
+  void *Y;
+  long ldy, strideY;
+  bool y_transposed;
+};
+// symmetric: D is symmetric, A and B the same, and one half of its tiles is
+// computed.
+hipError_t launch_ortho_product(const OrthoProductArgs &p, bool symmetric, bool y_bf16, int batch,
+                                int cus, hipStream_t s);
+
+}  // namespace sgemm
