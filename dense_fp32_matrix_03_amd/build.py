@@ -40,7 +40,7 @@ SOURCES = ["api.hip", "mfma_kernels.hip", "mfma_layout_nn.hip", "mfma_layout_nn_
            "valu_kernels.hip", "vector_add.hip", "bf16x3.hip", "ceiling.hip", "noalloc.hip",
            "api_grouped.hip", "grouped.hip",
            "api_mxfp4.hip", "mxfp4_cast.hip", "mxfp4_gemm.hip", "mxfp4_tile.hip",
-           "api_int8.hip", "int8_cast.hip", "int8_tile.hip",
+           "api_int8.hip", "int8_cast.hip", "int8_rows.hip", "int8_tile.hip",
            "api_route.hip", "route.hip", "route_plan.hip", "rows.hip",
            "api_orthogonalize.hip", "orthogonalize.hip"]
 ARCH = "gfx950"

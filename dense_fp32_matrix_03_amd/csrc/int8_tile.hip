@@ -116,10 +116,23 @@ hipError_t launch(const Int8Args &p, bool c_bf16, hipStream_t s) {
 
 }  // namespace
 
-bool int8_casts(const Int8Args &, int) { return false; }
-
-hipError_t launch_int8_product(const Int8Args &p, int, bool c_bf16, int, hipStream_t s) {
-  return launch<64, 64, 2, 2, 1>(p, c_bf16, s);
+hipError_t launch_int8_tile(const Int8Args &p, bool c_bf16, int cus, hipStream_t s) {
+  const long groups = !p.offsets ? 1 : p.groups < p.M ? p.groups : p.M;
+  const double mean = (double)p.M / groups;
+  auto per_cu = [&](long t) {
+    const double rows = p.offsets ? fmax(1.0, mean / t + 0.5) : ceil(mean / t);
+    return ceil(groups * rows * ((p.N + t - 1) / t) / cus);
+  };
+  const double n64 = per_cu(64), n128 = per_cu(128);
+  const double c64 = n64 == 1 ? 0.35 : n64 == 2 ? 0.42 : 0.16 * n64;
+  const double c128 = n128 == 1 ? 0.65 : n128 == 2 ? 0.77 : 0.29 * n128;
+  if ((p.offsets && mean <= 64) || (c64 <= c128 && c64 <= per_cu(256))) {
+    if (n64 == 1 && p.K >= 6144) return launch<64, 64, 2, 2, 4>(p, c_bf16, s);
+    if (n64 == 2 && p.K >= 6144) return launch<64, 64, 2, 2, 2>(p, c_bf16, s);
+    return launch<64, 64, 2, 2, 1>(p, c_bf16, s);
+  }
+  return c128 <= per_cu(256) ? launch<128, 128, 2, 2, 1>(p, c_bf16, s)
+                             : launch<256, 256, 2, 4, 1>(p, c_bf16, s);
 }
 
 }  // namespace sgemm
