@@ -53,49 +53,76 @@ int8_tile_kernel(Int8Args p, TileMap tmap, GroupMap map) {
     n0 = tn * BN;
   }
   const int rows_a = min(BM, m_end - m0), rows_b = min(BN, p.N - n0);
+  // The tile's scales go to LDS while the first slices are on their way: read from
+  // memory in the epilogue, each block of four rows waited for its own (17 us a
+  // round of 256 x 256 tiles without stores, and without any k to speak of).
+  const bool sums = p.K > 0;  // without k there are no scales either
+  __shared__ __attribute__((aligned(16))) float scales_a[BM], scales_b[BN];
+  for (int i = threadIdx.x; i < BM + BN; i += Tile::kThreads) {
+    if (i < BM)
+      scales_a[i] = sums && i < rows_a ? p.a.scales[a_row + m0 + i] : 0.f;
+    else
+      scales_b[i - BM] = sums && i - BM < rows_b ? p.b.scales[b_row + n0 + i - BM] : 0.f;
+  }
   i32x16 acc[FM][FN];
   if (!Tile::run(p.a.codes + (a_row + m0) * p.a.ld, (int)p.a.ld, rows_a,
                  p.b.codes + (b_row + n0) * p.b.ld, (int)p.b.ld, rows_b, (p.K + 127) / 128, acc))
     return;
+  // run's barriers lie between the writes above and the reads below, but for K == 0,
+  // where scales are not read.
 
   // Register e of lane l holds row acc32_row(l, e), column l % 32 of a block:
   // row 4 (l / 32) of a uniform base and a constant number of rows past it.
   using T = std::conditional_t<CBF16, __bf16, float>;
   const int mt = Tile::row0() + 4 * half, nt = Tile::col0() + r32;  // inside the tile
-  T *const C = static_cast<T *>(p.C) + (a_row + m0 + mt) * p.ldc + n0 + nt;
+  T *const C = static_cast<T *>(p.C) + (a_row + m0 + Tile::row0()) * p.ldc + n0 + Tile::col0();
+  const unsigned lane_at = (unsigned)((4 * half * p.ldc + r32) * sizeof(T));
   const int rows = rows_a - mt, cols = rows_b - nt;
-  const bool sums = p.K > 0;  // without k there are no scales either
-  const float *sa = p.a.scales + a_row + m0 + mt, *sb = p.b.scales + b_row + n0 + nt;
   float scale_b[FN];
 #pragma unroll
-  for (int j = 0; j < FN; ++j) scale_b[j] = sums && j * 32 < cols ? sb[j * 32] : 0.f;
+  for (int j = 0; j < FN; ++j) scale_b[j] = sums ? scales_b[nt + j * 32] : 0.f;
+  auto store = [&](auto whole, auto with_c) {
 #pragma unroll
-  for (int i = 0; i < FM; ++i)
+    for (int i = 0; i < FM; ++i)
 #pragma unroll
-    for (int quad = 0; quad < 4; ++quad) {
-      const int r0 = i * 32 + 8 * quad;
-      float scale_a[4], c[4][FN];
+      for (int quad = 0; quad < 4; ++quad) {
+        const int r0 = i * 32 + 8 * quad;
+        f32x4 scale_a = {0.f, 0.f, 0.f, 0.f};
+        if (sums) scale_a = *reinterpret_cast<const f32x4 *>(scales_a + mt + r0);
+        auto at = [&](int e, int j) {
+          return reinterpret_cast<T *>(reinterpret_cast<char *>(C + (r0 + e) * p.ldc + j * 32) +
+                                       lane_at);
+        };
+        auto in = [&](int e, int j) {
+          return decltype(whole)::value || (r0 + e < rows && j * 32 < cols);
+        };
+        float c[4][FN];
+        if constexpr (decltype(with_c)::value) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) scale_a[e] = sums && r0 + e < rows ? sa[r0 + e] : 0.f;
-      if (p.beta != 0.f) {
+          for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int j = 0; j < FN; ++j) c[e][j] = in(e, j) ? (float)*at(e, j) : 0.f;
+        }
 #pragma unroll
         for (int e = 0; e < 4; ++e)
 #pragma unroll
-          for (int j = 0; j < FN; ++j)
-            c[e][j] = r0 + e < rows && j * 32 < cols ? (float)C[(r0 + e) * p.ldc + j * 32] : 0.f;
+          for (int j = 0; j < FN; ++j) {
+            const float v = int8_value(acc[i][j][4 * quad + e], scale_a[e], scale_b[j]);
+            if (!in(e, j)) continue;
+            if constexpr (decltype(with_c)::value)
+              *at(e, j) = (T)fmaf(p.alpha, v, p.beta * c[e][j]);
+            else
+              *at(e, j) = (T)(p.alpha * v);
+          }
       }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (r0 + e >= rows) continue;
-#pragma unroll
-        for (int j = 0; j < FN; ++j) {
-          if (j * 32 >= cols) continue;
-          const float v = int8_value(acc[i][j][4 * quad + e], scale_a[e], scale_b[j]);
-          C[(r0 + e) * p.ldc + j * 32] =
-              (T)(p.beta != 0.f ? fmaf(p.alpha, v, p.beta * c[e][j]) : p.alpha * v);
-        }
-      }
-    }
+  };
+  const bool full = rows_a == BM && rows_b == BN;
+  if (p.beta != 0.f)
+    store(std::false_type(), std::true_type());
+  else if (full)
+    store(std::true_type(), std::false_type());
+  else
+    store(std::false_type(), std::false_type());
 }
 
 template <int BM, int BN, int WM, int WN, int KS>
