@@ -14,6 +14,7 @@ namespace {
 using sgemm_api::kMaxDim;
 using sgemm_api::kMaxWorkItems;
 
+constexpr int64_t kSlice = sgemm::kSliceRow;
 constexpr int64_t kMaxK = (int64_t(1) << 17) - 1;
 constexpr int64_t kMaxPitch = int64_t(1) << 22;  // offsets in a tile of 256 rows: below 2^30
 constexpr int64_t kMaxLdc = int64_t(1) << 27;    // offsets in 8 rows of C: below 4 GiB
@@ -32,7 +33,7 @@ bool cast_fits(int64_t rows) { return rows <= kMaxWorkItems / 256; }
 
 bool bad_pitch(int64_t ld, int64_t K) { return ld < kp(K) || ld % 16 != 0; }
 
-// The codes come first in a workspace, the scales after them.
+// The codes come first in a workspace, slice by slice, the scales after them.
 int64_t codes_bytes(int64_t rows, int64_t K) { return rows * kp(K); }
 
 // Both product entry points; groups < 0: not grouped.
@@ -87,8 +88,8 @@ int run(int64_t groups, int64_t M, int64_t N, int64_t K, float alpha, int typeA,
   p.groups = (int)b_groups;
   p.alpha = reads_ab ? alpha : 0.f;  // an empty sum is 0, whatever alpha is
   p.beta = beta;
-  p.a = {static_cast<const char *>(A), scalesA, lda};
-  p.b = {static_cast<const char *>(B), scalesB, ldb};
+  p.a = {static_cast<const char *>(A), scalesA, lda, kSlice};
+  p.b = {static_cast<const char *>(B), scalesB, ldb, kSlice};
   p.C = C;
   p.ldc = ldc;
   p.offsets = grouped ? offsets : nullptr;
@@ -101,8 +102,9 @@ int run(int64_t groups, int64_t M, int64_t N, int64_t K, float alpha, int typeA,
       char *codes = static_cast<char *>(workspace);
       float *scales = reinterpret_cast<float *>(codes + codes_bytes(M, K));
       err = sgemm::launch_int8_quantize(false, typeA == SGEMM_TYPE_BF16,
-                                        {(int)M, (int)K, lda, A, codes, kp(K), scales}, s);
-      p.a = {codes, scales, kp(K)};
+                                        {(int)M, (int)K, lda, A, codes, kSlice, M * kSlice, scales},
+                                        s);
+      p.a = {codes, scales, kSlice, M * kSlice};
     }
   }
   if (err == hipSuccess)
@@ -148,7 +150,7 @@ int sgemm_int8_quantize(int trans, int64_t rows, int64_t K, int type, const void
   if (rc != SGEMM_OK) return rc;
   const hipError_t err = sgemm::launch_int8_quantize(
       trans != 0, type == SGEMM_TYPE_BF16,
-      {(int)rows, (int)K, ldx, X, static_cast<char *>(codes), ldq, scales},
+      {(int)rows, (int)K, ldx, X, static_cast<char *>(codes), ldq, kSlice, scales},
       reinterpret_cast<hipStream_t>(stream));
   return err == hipSuccess ? SGEMM_OK : SGEMM_ERR_LAUNCH;
 }

@@ -14,7 +14,7 @@ namespace {
 using sgemm_api::kMaxDim;
 using sgemm_api::kMaxWorkItems;
 
-constexpr int64_t kMaxSize = int64_t(1) << 20;  // of a matrix: a tile of 256 rows is below 2^31 bytes
+constexpr int64_t kMaxSize = int64_t(1) << 20;  // of a matrix: a slice of it is below 2^31 bytes
 constexpr int64_t kMaxBatch = 65535;            // the second dimension of a launch
 constexpr int64_t kMaxSteps = 64;
 
@@ -33,11 +33,11 @@ struct Layout {
   Layout(int64_t batch, int64_t M, int64_t N) {
     m = (int)(M < N ? M : N);
     n = (int)(M < N ? N : M);
-    z = (int64_t)m * sgemm::split_pitch(n);
-    zt = (int64_t)n * sgemm::split_pitch(m);
-    s = (int64_t)m * sgemm::split_pitch(m);
-    const int64_t runs = M * tiles(N, 2048);
-    parts = runs < sgemm::kNormParts ? runs : sgemm::kNormParts;
+    z = sgemm::split_bytes(m, n);
+    zt = sgemm::split_bytes(n, m);
+    s = sgemm::split_bytes(m, m);
+    parts = tiles(M * tiles(N, sgemm::kNormRun), 16);
+    if (parts > sgemm::kNormParts) parts = sgemm::kNormParts;
     total = batch * (z + 2 * zt + 2 * s + 8 * parts);
   }
 };
@@ -130,14 +130,13 @@ int sgemm_orthogonalize(int64_t batch, int64_t M, int64_t N, int64_t steps, int6
   const Layout l(batch, M, N);
   char *at = static_cast<char *>(workspace);
   auto matrix = [&](int rows, int cols) {
-    const sgemm::SplitMatrix x{at, rows, cols, sgemm::split_pitch(cols),
-                               (long)rows * sgemm::split_pitch(cols)};
+    const sgemm::SplitMatrix x{at, rows, cols, sgemm::split_bytes(rows, cols)};
     at += batch * x.stride;
     return x;
   };
   const sgemm::SplitMatrix z = matrix(l.m, l.n), S = matrix(l.m, l.m), P = matrix(l.m, l.m);
   sgemm::SplitMatrix zt[2] = {matrix(l.n, l.m), matrix(l.n, l.m)};
-  const sgemm::SplitMatrix none{nullptr, 0, 0, 0, 0};
+  const sgemm::SplitMatrix none{nullptr, 0, 0, 0};
   const bool tall = M > N;
 
   sgemm::OrthoSplitArgs in;

@@ -7,6 +7,7 @@
 
 #include "common.hpp"
 #include "mxfp4.hpp"  // load8: eight values of either type
+#include "slice_tile.hpp"
 
 namespace sgemm {
 
@@ -17,17 +18,23 @@ struct Int8CastArgs {
   long ldx;
   const void *X;
   char *codes;
-  long ldq;
+  long ldq, slice;  // as in Int8Matrix
   float *scales;
 };
 
 hipError_t launch_int8_quantize(bool trans, bool bf16, const Int8CastArgs &p, hipStream_t s);
 
-// A held matrix.
+// A held matrix: slices of 128 k of a row lie `slice` bytes apart, rows of a slice
+// `ld`: 128 and the user's ldq, or in the workspace 128 * rows and 128 (the
+// reason stands at SliceRows in slice_tile.hpp).
 struct Int8Matrix {
   const char *codes;
   const float *scales;
   long ld;
+  long slice;
+  __device__ __forceinline__ SliceRows tile_rows(long first, int rows) const {
+    return {codes + first * ld, (int)ld, slice, rows};
+  }
 };
 
 // C = alpha A B^T + beta C over held operands; or A of values that the kernel

@@ -51,7 +51,7 @@ __global__ void __launch_bounds__(256) int8_quantize_kernel(Int8CastArgs p) {
     uint2 c;
     c.x = int8_pack(s.code(w[0]), s.code(w[1]), s.code(w[2]), s.code(w[3]));
     c.y = int8_pack(s.code(w[4]), s.code(w[5]), s.code(w[6]), s.code(w[7]));
-    *reinterpret_cast<uint2 *>(codes + k) = c;
+    *reinterpret_cast<uint2 *>(codes + (k / 128) * p.slice + k % 128) = c;
   };
 #pragma unroll
   for (int i = 0; i < kHeld; ++i) store(8 * (t + i * T), v[i]);
@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(256) int8_quantize_transposed_kernel(Int8CastA
     for (int e = 0; e < 4; ++e)
       w[e] = int8_pack(s.code(v[4 * e]), s.code(v[4 * e + 1]), s.code(v[4 * e + 2]),
                        s.code(v[4 * e + 3]));
-    *reinterpret_cast<uint4 *>(p.codes + row * p.ldq + k) = q;
+    *reinterpret_cast<uint4 *>(p.codes + row * p.ldq + (k / 128) * p.slice + k % 128) = q;
   }
 }
 

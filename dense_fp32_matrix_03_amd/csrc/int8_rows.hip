@@ -55,12 +55,12 @@ __global__ void __launch_bounds__(KS *kWave) int8_rows_kernel(Int8Args p, GroupM
   const char *a_at[MT], *b_at[NT];
 #pragma unroll
   for (int i = 0; i < MT; ++i)
-    a_at[i] = p.a.codes + (a_row + min(16 * i + r16, M - 1)) * p.a.ld + 64 * q;
+    a_at[i] = p.a.codes + (a_row + min(16 * i + r16, M - 1)) * p.a.ld;
   float scale_b[NT];
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
     const long r = b_row + min(n0 + 16 * j + r16, p.N - 1);
-    b_at[j] = p.b.codes + r * p.b.ld + 64 * q;
+    b_at[j] = p.b.codes + r * p.b.ld;
     scale_b[j] = p.K > 0 ? p.b.scales[r] : 0.f;
   }
   i32x4 acc[MT][NT];
@@ -80,13 +80,14 @@ __global__ void __launch_bounds__(KS *kWave) int8_rows_kernel(Int8Args p, GroupM
     for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int s = 0; s < 4; ++s)
-        o.b[j][s] = in ? *reinterpret_cast<const i32x4 *>(b_at[j] + k + 16 * s) : zero;
+        o.b[j][s] = in ? *reinterpret_cast<const i32x4 *>(b_at[j] + k + 64 * q + 16 * s) : zero;
     if constexpr (!CAST) {
+      const long a_k = (k / 128 + q / 2) * p.a.slice + 64 * (q % 2);
 #pragma unroll
       for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int s = 0; s < 4; ++s)
-          o.a[i][s] = in ? *reinterpret_cast<const i32x4 *>(a_at[i] + k + 16 * s) : zero;
+          o.a[i][s] = in ? *reinterpret_cast<const i32x4 *>(a_at[i] + a_k + 16 * s) : zero;
     }
   };
   auto load_any = [&](int k, Operand &o) {

@@ -19,11 +19,12 @@ namespace {
 struct Int8Format {
   typedef i32x16 Acc;
   typedef slice_i32x4 Frag;
-  static constexpr int kSteps = 4, kReads = 1, kMfma = 1;
+  static constexpr int kSteps = 4, kReads = 1, kMfma = 1, kChains = 2;
   template <int S, class At>
   __device__ __forceinline__ static Frag load(int half, At at) {
     return *at(4 * half + S);
   }
+  template <int I>
   __device__ __forceinline__ static void mma(const Frag &a, const Frag &b, Acc &c) {
     c = __builtin_amdgcn_mfma_i32_32x32x32_i8(a, b, c, 0, 0, 0);
   }
@@ -32,7 +33,7 @@ struct Int8Format {
 template <int BM, int BN, int WM, int WN, int KS, bool CBF16>
 __global__ void __launch_bounds__(WM *WN *KS *kWave, 2)
 int8_tile_kernel(Int8Args p, TileMap tmap, GroupMap map) {
-  using Tile = SliceTile<Int8Format, BM, BN, WM, WN, KS>;
+  using Tile = SliceTile<Int8Format, BM, BN, WM, WN, KS, 2>;
   constexpr int FM = Tile::FM, FN = Tile::FN;
   const int lane = threadIdx.x % kWave, r32 = lane % 32, half = lane / 32;
 
@@ -65,8 +66,10 @@ int8_tile_kernel(Int8Args p, TileMap tmap, GroupMap map) {
       scales_b[i - BM] = sums && i - BM < rows_b ? p.b.scales[b_row + n0 + i - BM] : 0.f;
   }
   i32x16 acc[FM][FN];
-  if (!Tile::run(p.a.codes + (a_row + m0) * p.a.ld, (int)p.a.ld, rows_a,
-                 p.b.codes + (b_row + n0) * p.b.ld, (int)p.b.ld, rows_b, (p.K + 127) / 128, acc))
+  char *lds[2];
+  const int nk = (p.K + 127) / 128;
+  if (!Tile::run(p.a.tile_rows(a_row + m0, rows_a), p.b.tile_rows(b_row + n0, rows_b), nk, 0, acc,
+                 lds))
     return;
   // run's barriers lie between the writes above and the reads below, but for K == 0,
   // where scales are not read.

@@ -9,16 +9,20 @@
 
 namespace sgemm {
 
-// A batch of matrices in pieces: rows of `pitch` bytes, 128 for each 32 columns
-// (the last 32 padded with zeros): 32 high pieces, then 32 low ones.  A value is
-// (high + low) 2^-s with an s that the host keeps.
+// A batch of matrices in pieces: [cols / 32][rows] blocks of 128 bytes, 32 high
+// pieces of a row and then 32 low ones, the last columns padded with zeros.  A
+// value is (high + low) 2^-s with an s that the host keeps.
 struct SplitMatrix {
   char *at;
   int rows, cols;
-  int pitch;
   long stride;  // bytes from one matrix to the next
+  // Where the high piece of (r, c) lies; the low one is 64 bytes after it.
+  __device__ __forceinline__ char *place(int batch, int r, int c) const {
+    return at + batch * stride + ((long)(c / 32) * rows + r) * 128 + c % 32 * 2;
+  }
+  __host__ __device__ __forceinline__ int padded() const { return (cols + 31) / 32 * 32; }
 };
-inline int split_pitch(long cols) { return (int)((cols + 31) / 32 * 128); }
+inline long split_bytes(long rows, long cols) { return (cols + 31) / 32 * rows * 128; }
 
 // The sum of squares, in parts, of every matrix of the batch.
 struct OrthoNormArgs {
@@ -28,7 +32,8 @@ struct OrthoNormArgs {
   double *parts;  // [batch][n_parts]
   int n_parts;
 };
-constexpr int kNormParts = 256;
+constexpr int kNormRun = 512;    // elements of a row that a wave adds up at a time
+constexpr int kNormParts = 256;  // parts, at most: a work-group each, of 16 such runs or more
 hipError_t launch_ortho_norm(const OrthoNormArgs &p, bool bf16, int batch, hipStream_t s);
 
 // X 2^shift / (|X| + eps), in pieces, as it is and transposed.

@@ -5,7 +5,7 @@
 //
 // A slice is [row][8 chunks of 16 bytes] in LDS, chunk c at c ^ kc_swizzle
 // (mfma_dma.hpp), which is conflict-free for 16 lanes that read one chunk of 16
-// consecutive rows.  There are two stages: while one is multiplied the other is
+// consecutive rows.  There are NST stages: while one is multiplied the others are
 // loaded.  The descriptors end at the last row's last byte, so rows past it read
 // as zeros.
 //
@@ -15,7 +15,10 @@
 //   Frag             a lane's operands of 32 rows in a step
 //   load(row, at)    reads a Frag from LDS: `at` gives the address of a chunk
 //   kReads           its LDS reads
-//   mma(a, b, acc)   a step's products; kMfma matrix instructions.
+//   mma<I>(a, b, acc)  the I-th of the kMfma matrix instructions of a step.
+// An instruction that adds to the sums of the one before waits for it: the
+// instructions of a step go through all blocks one by one, and a wave with a single
+// block adds to kChains sums in turn.
 #pragma once
 
 #include "mfma_dma.hpp"
@@ -26,11 +29,51 @@ typedef int slice_i32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kSliceRow = 128;  // bytes of a row's slice
 
+// Barrier of the work-group that retires all except this wave's N most recent
+// buffer-to-LDS loads, and its LDS reads and writes.  __syncthreads is a fence too, at
+// which the compiler waits for every such load, so that no more than one slice was
+// ever on its way, however many stages there were.  Here the waits are the ones
+// written (s_waitcnt: vmcnt(N), lgkmcnt(0)), and the fences of a single wave only
+// keep the compiler from moving LDS accesses across.
+template <int N>
+__device__ __forceinline__ void slice_barrier() {
+  static_assert(N >= 0 && N < 64, "vmcnt is 6 bits");
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_s_waitcnt((N & 15) | (0x7 << 4) | ((N >> 4) << 14));
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+}
+
+// Rows of an operand: the first one's first slice, and the bytes from a row and from
+// a slice to the next (row_step x the tile's rows stays below 2^31).  Rows one after
+// the other have row_step = their length and slice_step = 128.  Where that length is
+// a multiple of some KiB, the slices that the whole chip reads at a time lie in few
+// of the memory's channels: 8192^3 in 8-bit integers 540 us with both operands' rows
+// 8192 bytes apart, 459 with rows 8320 apart.  Slices one after the other, row_step =
+// 128, are free of that.
+struct SliceRows {
+  const char *at;
+  int row_step;
+  long slice_step;
+  int rows;
+  // The same in scalar registers.  All waves of a work-group have the same operands,
+  // but where the compiler does not see it, as with tiles of groups, it wraps each
+  // load in a loop over the lanes' descriptors.
+  __device__ __forceinline__ SliceRows uniform() const {
+    auto u32 = [](unsigned v) { return (unsigned)__builtin_amdgcn_readfirstlane((int)v); };
+    auto u64 = [&](uint64_t v) {
+      return (uint64_t)u32((unsigned)(v >> 32)) << 32 | u32((unsigned)v);
+    };
+    return {reinterpret_cast<const char *>(u64(reinterpret_cast<uint64_t>(at))),
+            (int)u32((unsigned)row_step), (long)u64((uint64_t)slice_step), (int)u32((unsigned)rows)};
+  }
+};
+
 // KS sets of WM x WN waves share a tile; set q takes slices q, q + KS, ..
 // through LDS stages of its own, and the sets' sums are added in order at the
 // end.  With few tiles the time is a chain of slices, each as long as its
 // loads take to arrive: the sets walk KS chains at once.
-template <class F, int BM, int BN, int WM, int WN, int KS>
+template <class F, int BM, int BN, int WM, int WN, int KS, int NST>
 struct SliceTile {
   static constexpr int NW = WM * WN;  // waves of a set
   static constexpr int WTM = BM / WM, WTN = BN / WN, FM = WTM / 32, FN = WTN / 32;
@@ -49,38 +92,49 @@ struct SliceTile {
   __device__ __forceinline__ static int row0() { return wave_id() / WN * WTM; }
   __device__ __forceinline__ static int col0() { return wave_id() % WN * WTN; }
 
-  // acc = the tile's sums over nk slices.  a, b: the first rows' first bytes, rows
-  // a_pitch (b_pitch) bytes apart, at least 128 nk; rows_a (rows_b) of them are
-  // there.  BM a_pitch and BN b_pitch stay below 2^31.  False for waves
-  // whose sums went to another set.
-  __device__ __forceinline__ static bool run(const char *a, int a_pitch, int rows_a, const char *b,
-                                             int b_pitch, int rows_b, int nk,
-                                             Acc (&acc)[FM][FN]) {
-    // One LDS array per stage and operand, so that the compiler sees that loads
-    // into one stage do not touch the one that is read (mfma_dma.hpp).
+  // acc = the tile's sums over nk slices, from the `start`-th on and round to it.
+  // False for waves whose sums went to another set.  lds: the stages' memory, which is
+  // free once every wave has passed a barrier after this (STAGE_BYTES each).
+  static constexpr int STAGE_BYTES = KS * (BM + BN) * kSliceRow;
+  __device__ __forceinline__ static bool run(const SliceRows &rows_a, const SliceRows &rows_b,
+                                             int nk, int start, Acc (&acc)[FM][FN],
+                                             char *(&lds)[NST]) {
+    const SliceRows a = rows_a.uniform(), b = rows_b.uniform();
+    // One LDS array per stage, so that the compiler sees that loads into one stage do
+    // not touch the one that is read (mfma_dma.hpp).  It tells four arrays apart; with
+    // one for each operand of four stages it waited for all loads before most reads.
     constexpr int SA = BM * kSliceRow / 4, SB = BN * kSliceRow / 4;
-    __shared__ __attribute__((aligned(1024))) float As0[KS * SA], As1[KS * SA];
-    __shared__ __attribute__((aligned(1024))) float Bs0[KS * SB], Bs1[KS * SB];
+    static_assert(NST >= 2 && NST <= 4, "two to four stages");
+    constexpr auto room = [](int stage) { return stage < NST ? KS * (SA + SB) : 4; };
+    __shared__ __attribute__((aligned(1024))) float stage0[room(0)], stage1[room(1)];
+    __shared__ __attribute__((aligned(16))) float stage2[room(2)], stage3[room(3)];
 
+    {
+      float *const all[] = {stage0, stage1, stage2, stage3};
+      for (int i = 0; i < NST; ++i) lds[i] = reinterpret_cast<char *>(all[i]);
+    }
     const int lane = threadIdx.x % kWave;
     const int all_waves = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int kq = KS > 1 ? all_waves / NW : 0;
     const int wave = KS > 1 ? all_waves % NW : all_waves;
     const int wm = wave / WN, wn = wave % WN;
     const int r32 = lane % 32, half = lane / 32;
-    auto stage_a = [&](auto S) -> float * { return (decltype(S)::value ? As1 : As0) + kq * SA; };
-    auto stage_b = [&](auto S) -> float * { return (decltype(S)::value ? Bs1 : Bs0) + kq * SB; };
+    auto stage_a = [&](auto S) -> float * {
+      constexpr int s = decltype(S)::value;
+      return (s == 0 ? stage0 : s == 1 ? stage1 : s == 2 ? stage2 : stage3) + kq * SA;
+    };
+    auto stage_b = [&](auto S) -> float * { return stage_a(S) + KS * SA + kq * (SB - SA); };
 
     // Load q of a wave fetches rows 8 (wave + q NW) .. + 7 of the slice.
     unsigned off_a[QA], off_b[QB];
-    auto offset = [&](int q, int pitch) {
+    auto offset = [&](int q, int step) {
       const int row = 8 * (wave + q * NW) + lane / 8;
-      return (unsigned)(row * pitch + 16 * ((lane % 8) ^ kc_swizzle<32, true>(row)));
+      return (unsigned)(row * step + 16 * ((lane % 8) ^ kc_swizzle<32, true>(row)));
     };
 #pragma unroll
-    for (int q = 0; q < QA; ++q) off_a[q] = offset(q, a_pitch);
+    for (int q = 0; q < QA; ++q) off_a[q] = offset(q, a.row_step);
 #pragma unroll
-    for (int q = 0; q < QB; ++q) off_b[q] = offset(q, b_pitch);
+    for (int q = 0; q < QB; ++q) off_b[q] = offset(q, b.row_step);
 
     auto rsrc = [](const void *base, int records) {
       return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, records,
@@ -90,11 +144,13 @@ struct SliceTile {
     // descriptors without records: nothing is fetched.  No branch depends on
     // that, so that the loads can be scheduled between matrix-core instructions.
     int k = kq;  // the slice
+    const int end_a = (a.rows - 1) * a.row_step + kSliceRow;
+    const int end_b = (b.rows - 1) * b.row_step + kSliceRow;
     auto dma = [&](auto S) {
       const bool live = k < nk;
-      const int k0 = k * kSliceRow;
-      const __amdgpu_buffer_rsrc_t ra = rsrc(a + k0, live ? rows_a * a_pitch - k0 : 0);
-      const __amdgpu_buffer_rsrc_t rb = rsrc(b + k0, live ? rows_b * b_pitch - k0 : 0);
+      const int at = k + start < nk ? k + start : k + start - nk;
+      const __amdgpu_buffer_rsrc_t ra = rsrc(a.at + at * a.slice_step, live ? end_a : 0);
+      const __amdgpu_buffer_rsrc_t rb = rsrc(b.at + at * b.slice_step, live ? end_b : 0);
 #pragma unroll
       for (int q = 0; q < QA; ++q) lds_dma<true>(ra, stage_a(S) + (wave + q * NW) * 256, off_a[q]);
 #pragma unroll
@@ -106,19 +162,16 @@ struct SliceTile {
     struct Ops {
       typename F::Frag a[FM], b[FN];
     };
+    // B first: its operands are needed first.
     auto read_ops = [&](auto S, auto STEP, Ops &o) {
-#pragma unroll
-      for (int i = 0; i < FM; ++i) {
-        const float *row = stage_a(S) + (wm * WTM + i * 32 + r32) * 32;
-        o.a[i] = F::template load<decltype(STEP)::value>(
+      auto read = [&](const float *row) {
+        return F::template load<decltype(STEP)::value>(
             half, [&](int c) { return reinterpret_cast<const slice_i32x4 *>(row + (c ^ sw) * 4); });
-      }
+      };
 #pragma unroll
-      for (int j = 0; j < FN; ++j) {
-        const float *row = stage_b(S) + (wn * WTN + j * 32 + r32) * 32;
-        o.b[j] = F::template load<decltype(STEP)::value>(
-            half, [&](int c) { return reinterpret_cast<const slice_i32x4 *>(row + (c ^ sw) * 4); });
-      }
+      for (int j = 0; j < FN; ++j) o.b[j] = read(stage_b(S) + (wn * WTN + j * 32 + r32) * 32);
+#pragma unroll
+      for (int i = 0; i < FM; ++i) o.a[i] = read(stage_a(S) + (wm * WTM + i * 32 + r32) * 32);
     };
 
 #pragma unroll
@@ -128,39 +181,52 @@ struct SliceTile {
 #pragma unroll
         for (int e = 0; e < 16; ++e) acc[i][j][e] = 0;
 
-    auto mma = [&](const Ops &o) {
+    // The sums that a wave with one block adds to in turn, but for the last.
+    constexpr int kChains = FM * FN == 1 ? F::kChains : 1;
+    Acc chain[kChains];
 #pragma unroll
-      for (int i = 0; i < FM; ++i)
+    for (int c = 0; c + 1 < kChains; ++c)
 #pragma unroll
-        for (int j = 0; j < FN; ++j) F::mma(o.a[i], o.b[j], acc[i][j]);
+      for (int e = 0; e < 16; ++e) chain[c][e] = 0;
+    auto mma = [&](auto STEP, const Ops &o) {
+      static_for<F::kMfma>([&](auto I) {
+        constexpr int c = (decltype(STEP)::value * F::kMfma + decltype(I)::value) % kChains;
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+          for (int j = 0; j < FN; ++j)
+            F::template mma<decltype(I)::value>(o.a[i], o.b[j],
+                                                c + 1 < kChains ? chain[c] : acc[i][j]);
+      });
     };
 
     // A step's operand reads (and a slice's loads) are spread between its
-    // matrix-core instructions.
+    // matrix-core instructions, the reads over the first three quarters of them: they
+    // have arrived when the next step begins.
     constexpr int kMfma = FM * FN * F::kMfma, kReads = (FM + FN) * F::kReads;
     auto interleave = [&](auto last) {
       constexpr int loads = decltype(last)::value ? kLoads : 0;
       static_for<kMfma>([&](auto I) {
         constexpr int i = decltype(I)::value;
         constexpr int v = loads * (i + 1) / kMfma - loads * i / kMfma;
-        constexpr int d = kReads * (i + 1) / kMfma - kReads * i / kMfma;
+        constexpr int span = (kMfma * 3 + 3) / 4;
+        constexpr int d = kReads * (i + 1 < span ? i + 1 : span) / span -
+                          kReads * (i < span ? i : span) / span;
         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                       // matrix core
         if constexpr (d > 0) __builtin_amdgcn_sched_group_barrier(0x100, d, 0);  // DS read
         if constexpr (v > 0) __builtin_amdgcn_sched_group_barrier(0x020, v, 0);  // VMEM read
       });
     };
     using S0 = std::integral_constant<int, 0>;
-    using S1 = std::integral_constant<int, 1>;
-    // The set's t-th slice is in stage S, the next one on its way to the
-    // other.
+    // The set's t-th slice is in stage S, the next ones on their way to the others.
     // WHOLE: a wave with one block of 32 x 32 has too few matrix-core
     // instructions in a step to cover the next one's reads, and registers to
     // spare: it reads a whole slice's operands while it multiplies the one
     // before.  The barrier waits for slice t + 1, and for every wave to have read
-    // slice t; then slice t + 2 goes to stage S.
+    // slice t; then slice t + NST goes to stage S.
     // Otherwise the operands are read a step ahead, and the last step of a slice
     // waits for slice t + 1, and for every wave to be done with stage S, sends
-    // slice t + 2 there and reads slice t + 1's first operands.
+    // slice t + NST there and reads slice t + 1's first operands.
     constexpr bool WHOLE = FM * FN == 1;
     constexpr int kSteps = F::kSteps, kAhead = WHOLE ? kSteps : 1;
     Ops cur[kAhead], nxt[kAhead];
@@ -168,12 +234,12 @@ struct SliceTile {
       static_for<kAhead>([&](auto STEP) { read_ops(S, STEP, o[decltype(STEP)::value]); });
     };
     auto slice = [&](auto S) {
-      using SN = std::integral_constant<int, 1 - decltype(S)::value>;
+      using SN = std::integral_constant<int, (decltype(S)::value + 1) % NST>;
       if constexpr (WHOLE) {
-        dma_barrier_keep<0>();
+        slice_barrier<(NST - 2) * kLoads>();
         dma(S);
         read_ahead(SN(), nxt);
-        static_for<kSteps>([&](auto STEP) { mma(cur[decltype(STEP)::value]); });
+        static_for<kSteps>([&](auto STEP) { mma(STEP, cur[decltype(STEP)::value]); });
 #pragma unroll
         for (int s = 0; s < kAhead; ++s) cur[s] = nxt[s];
       } else {
@@ -181,13 +247,13 @@ struct SliceTile {
           constexpr int s = decltype(STEP)::value;
           if constexpr (s < kSteps - 1) {
             read_ops(S, std::integral_constant<int, s + 1>(), nxt[0]);
-            mma(cur[0]);
+            mma(STEP, cur[0]);
             interleave(std::false_type());
           } else {
-            dma_barrier_keep<0>();
+            slice_barrier<(NST - 2) * kLoads>();
             dma(S);
             read_ops(SN(), S0(), nxt[0]);
-            mma(cur[0]);
+            mma(STEP, cur[0]);
             interleave(std::true_type());
           }
           cur[0] = nxt[0];
@@ -197,29 +263,34 @@ struct SliceTile {
 
     if (nk > 0) {
       const int turns = (nk + KS - 1) / KS;  // the same for all sets: they share the barriers
-      dma(S0());
-      dma(S1());
-      dma_barrier_keep<kLoads>();
+      static_for<NST>([&](auto S) { dma(S); });
+      slice_barrier<(NST - 1) * kLoads>();
       read_ahead(S0(), cur);
-      for (int t = 0; t < turns; t += 2) {
-        slice(S0());
-        if (t + 1 < turns) slice(S1());
-      }
+      // Whole rounds of the stages without a test between them, then the rest: at a
+      // branch the compiler would lose count of the loads on their way.
+      int t = 0;
+      for (; t + NST <= turns; t += NST) static_for<NST>([&](auto S) { slice(S); });
+      static_for<NST - 1>([&](auto S) {
+        if (t + decltype(S)::value < turns) slice(S);
+      });
       // The last slices sent loads past the end (no memory traffic): let them
       // retire before the work-group gives up its LDS.
       __builtin_amdgcn_s_waitcnt(0x0f70);
     }
 
+#pragma unroll
+    for (int c = 0; c + 1 < kChains; ++c)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[0][0][e] += chain[c][e];
+
     if constexpr (KS > 1) {
       // The stages are free: every load has landed, every operand has been read.
-      // Set s > 0 leaves its sums at 4 Ki (s - 1) of As0, the last of four sets in
-      // Bs0.
-      static_assert(FM * FN * NW == 4 && (KS == 2 || KS == 4) && KS * SA == 2048 * KS &&
-                        SB == SA, "a set's sums are 16 KiB");
+      // Set s > 0 leaves its sums at 4 Ki (s - 1) of the first stage.
+      static_assert(FM * FN * NW == 4 && (KS - 1) * 4096 <= KS * (SA + SB),
+                    "a set's sums are 16 KiB");
       __syncthreads();
       auto sums = [&](int set) {
-        return reinterpret_cast<Word *>(set == 3 ? Bs0 : As0 + (set - 1) * 4096) + wave * 1024 +
-               lane;
+        return reinterpret_cast<Word *>(stage0 + (set - 1) * 4096) + wave * 1024 + lane;
       };
       if (kq > 0) {
         Word *at = sums(kq);
