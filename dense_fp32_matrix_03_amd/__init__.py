@@ -225,11 +225,20 @@ def _offsets(x, groups=0):
     return _ptr(x)
 
 
+_dtypes = {}
+
+
 def _typed(x, name, dtype, size=0):
     """_ptr of `size` contiguous 32-bit values, of which the kernels know only the address."""
-    if hasattr(x, "dtype"):
-        if str(x.dtype) != "torch." + dtype:
-            raise TypeError(f"{name} must be {dtype}")
+    if x is None or isinstance(x, int):
+        return x
+    want = _dtypes.get(dtype)
+    if want is None:
+        import torch
+        want = _dtypes[dtype] = getattr(torch, dtype)
+    if getattr(x, "dtype", want) is not want:
+        raise TypeError(f"{name} must be {dtype}")
+    if hasattr(x, "numel"):
         if not x.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
         if x.numel() < size:

@@ -74,9 +74,12 @@ int sgemm_route(int64_t tokens, int64_t experts, int64_t topk, int score, int ty
   if (!sgemm_api::ready()) return SGEMM_ERR_NOT_INITIALIZED;
   if (tokens == 0) return SGEMM_OK;
   if ((rc = launchable()) != SGEMM_OK) return rc;
+  int share = 64;
+  while (share * groups > 64) share /= 2;
   const sgemm::RouteArgs p{(int)tokens, (int)experts, (int)topk, score == SGEMM_SCORE_SIGMOID,
                            renormalize != 0, logits, ldl, bias, (int)groups, (int)topk_groups,
-                           (int)group_top, scale, picks, weights};
+                           (int)group_top, scale, picks, weights,
+                           sgemm::make_fast_div((int)(experts / groups)), share};
   return status(sgemm::launch_route(p, type == SGEMM_TYPE_BF16, stream_of(stream)));
 }
 

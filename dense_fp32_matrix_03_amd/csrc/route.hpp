@@ -19,6 +19,8 @@ struct RouteArgs {
   float scale;
   int32_t *picks;
   float *weights;
+  FastDiv by_size;  // experts of a group
+  int group_share;  // lanes of a group: a power of two, groups * group_share <= 64
 };
 hipError_t launch_route(const RouteArgs &p, bool bf16, hipStream_t s);
 
