@@ -70,9 +70,8 @@ __device__ __forceinline__ float int8_scale(unsigned top) {
 struct Int8Scale {
   float scale, inverse;
   bool zero;
-  __device__ __forceinline__ explicit Int8Scale(float s) : scale(s), inverse(1.0f / s) {
-    zero = !(s > 0.f);
-  }
+  __device__ __forceinline__ explicit Int8Scale(float s) : Int8Scale(s, 1.0f / s) {}
+  __device__ __forceinline__ Int8Scale(float s, float i) : scale(s), inverse(i), zero(!(s > 0.f)) {}
   // The whole number nearest to x / scale, halves to the even one.  x times the
   // reciprocal is off by at most 127 2 2^-24, so q is the nearest or, next
   // to a half, the other one; x - q scale is exact (a multiple of the smaller of
@@ -92,6 +91,42 @@ struct Int8Scale {
 __device__ __forceinline__ unsigned int8_pack(int a, int b, int c, int d) {
   return (unsigned)(a & 255) | (unsigned)(b & 255) << 8 | (unsigned)(c & 255) << 16 |
          (unsigned)d << 24;
+}
+
+// N values' codes, packed.  A fused multiply-add with 1.5
+// 2^23 rounds x times the reciprocal to a whole number, halves to even, and has its
+// code in its last bits.  The reciprocal is off by 2^-24 of itself, the product by less
+// than 2^-17, so that the code is the right one unless the product is that near to a
+// half: then, and for scales that have few bits, each is found as in Int8Scale.
+template <int N>
+__device__ __forceinline__ void int8_codes(const Int8Scale &s, const float v[N],
+                                           unsigned packed[N / 4]) {
+  if (s.zero) {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) packed[i] = 0;
+    return;
+  }
+  constexpr float kWhole = 12582912.f;
+  float worst = 0.f;
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i) {
+    unsigned y[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float x = v[4 * i + e], whole = fmaf(x, s.inverse, kWhole);
+      worst = fmaxf(worst, fabsf(fmaf(x, s.inverse, kWhole - whole)));
+      y[e] = __float_as_uint(whole);
+    }
+    // v_perm_b32: bytes 0 .. 3 are the second operand's, 4 .. 7 the first one's.
+    packed[i] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(y[3], y[2], 0x0c0c0400u),
+                                      __builtin_amdgcn_perm(y[1], y[0], 0x0c0c0400u), 0x05040100u);
+  }
+  if (__ballot(!(worst < 0.5f - 0x1p-16f)) != 0 || !(s.scale >= 0x1p-100f)) {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i)
+      packed[i] = int8_pack(s.code(v[4 * i]), s.code(v[4 * i + 1]), s.code(v[4 * i + 2]),
+                            s.code(v[4 * i + 3]));
+  }
 }
 
 __device__ __forceinline__ float int8_value(int sum, float sa, float sb) {

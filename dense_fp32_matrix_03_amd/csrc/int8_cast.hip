@@ -3,36 +3,36 @@
 //
 // Bound by memory: a cast reads 4 (or 2) bytes a value and writes 1.
 #include "int8.hpp"
-#include "mfma_dma.hpp"
+#include "piece.hpp"
 
 namespace sgemm {
 
 namespace {
 
-// T threads (a wave, or the work-group of four) have a row, 8 consecutive values
-// of every 8 T each.  The first kHeld runs of 8 stay in registers between the
-// search for the largest magnitude and the cast; longer rows are read again,
-// from the caches.
-constexpr int kHeld = 4;
-
+// T threads (a wave, or the work-group of four) have a row, 16 bytes each of every 16 T.
+// The first 8192 values stay in registers between the search for the largest magnitude
+// and the cast (2048 where a wave has the row); longer rows are read again, from the
+// caches.  8192 x 8192 from bfloat16 TODO us.
 template <bool BF16, int T>
 __global__ void __launch_bounds__(256) int8_quantize_kernel(Int8CastArgs p) {
   static_assert(T == 64 || T == 256, "a wave or a work-group has a row");
+  using P = Piece<BF16>;
+  constexpr int V = P::V, kStep = V * T, kHeld = BF16 ? 4 : 8;
   const int t = threadIdx.x % T;
   const long row = (long)blockIdx.x * (256 / T) + threadIdx.x / T;
   if (T < 256 && row >= p.rows) return;  // whole waves: no barrier follows
   const char *x = static_cast<const char *>(p.X) + row * p.ldx * (BF16 ? 2 : 4);
-  auto load = [&](int k, float v[8]) { load8<BF16, true>(x + (long)k * (BF16 ? 2 : 4), p.K - k, v); };
-  float v[kHeld][8];
+  P held[kHeld];
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i)
+    held[i].load(x, i * kStep + t * V, p.K - (i * kStep + t * V), (i + 1) * kStep <= p.K);
   unsigned top = 0;
 #pragma unroll
-  for (int i = 0; i < kHeld; ++i) load(8 * (t + i * T), v[i]);
-#pragma unroll
-  for (int i = 0; i < kHeld; ++i) top = max(top, magnitude_bits(v[i]));
-  for (int k = 8 * (t + kHeld * T); k < p.K; k += 8 * T) {
-    float w[8];
-    load8<BF16>(x + (long)k * (BF16 ? 2 : 4), p.K - k, w);
-    top = max(top, magnitude_bits(w));
+  for (int i = 0; i < kHeld; ++i) top = max(top, held[i].top());
+  for (int k = kHeld * kStep + t * V; k < p.K; k += kStep) {
+    P v;
+    v.load(x, k, p.K - k, false);
+    top = max(top, v.top());
   }
 #pragma unroll
   for (int d = 32; d > 0; d /= 2) top = max(top, (unsigned)__shfl_xor((int)top, d));
@@ -46,27 +46,30 @@ __global__ void __launch_bounds__(256) int8_quantize_kernel(Int8CastArgs p) {
   if (t == 0) p.scales[row] = s.scale;
   const int kp = (p.K + 127) / 128 * 128;
   char *codes = p.codes + row * p.ldq;
-  auto store = [&](int k, const float w[8]) {
+  auto store = [&](int k, const P &v) {
     if (k >= kp) return;
-    uint2 c;
-    c.x = int8_pack(s.code(w[0]), s.code(w[1]), s.code(w[2]), s.code(w[3]));
-    c.y = int8_pack(s.code(w[4]), s.code(w[5]), s.code(w[6]), s.code(w[7]));
-    *reinterpret_cast<uint2 *>(codes + (k / 128) * p.slice + k % 128) = c;
+    float f[V];
+    unsigned c[V / 4];
+    v.get(f);
+    int8_codes<V>(s, f, c);
+    __builtin_memcpy(__builtin_assume_aligned(codes + (k / 128) * p.slice + k % 128, V), c, V);
   };
 #pragma unroll
-  for (int i = 0; i < kHeld; ++i) store(8 * (t + i * T), v[i]);
-  for (int k = 8 * (t + kHeld * T); k < kp; k += 8 * T) {
-    float w[8];
-    load8<BF16>(x + (long)k * (BF16 ? 2 : 4), p.K - k, w);
-    store(k, w);
+  for (int i = 0; i < kHeld; ++i) store(i * kStep + t * V, held[i]);
+  for (int k = kHeld * kStep + t * V; k < kp; k += kStep) {
+    P v;
+    v.load(x, k, p.K - k, false);
+    store(k, v);
   }
 }
 
 // Values stored transposed: a work-group has 32 rows (neighbouring columns of X),
-// 8 threads each; a thread takes 16 consecutive k of every 128.  Loads of 32
+// kParts threads each; a thread takes 16 consecutive k of every 16 kParts.  Loads of 32
 // lanes adjoin.  Two passes: X is read twice.
+constexpr int kParts = 32;
+
 template <bool BF16>
-__global__ void __launch_bounds__(256) int8_quantize_transposed_kernel(Int8CastArgs p) {
+__global__ void __launch_bounds__(32 * kParts) int8_quantize_transposed_kernel(Int8CastArgs p) {
   const int c = threadIdx.x % 32, part = threadIdx.x / 32;
   const long row = (long)blockIdx.x * 32 + c;
   // Every thread loads, from the nearest element there is, so that the loads go
@@ -85,30 +88,27 @@ __global__ void __launch_bounds__(256) int8_quantize_transposed_kernel(Int8CastA
     for (int e = 0; e < 16; ++e) v[e] = k0 + e < p.K ? v[e] : 0.f;
   };
   unsigned top = 0;
-  for (int k = part * 16; k < p.K; k += 128) {
+  for (int k = part * 16; k < p.K; k += 16 * kParts) {
     float v[16];
     load(k, v);
     top = max(top, max(magnitude_bits(v), magnitude_bits(v + 8)));
   }
-  __shared__ unsigned tops[8][32];
+  __shared__ unsigned tops[kParts][32];
   tops[part][c] = top;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 8; ++i) top = max(top, tops[i][c]);
+  for (int i = 0; i < kParts; ++i) top = max(top, tops[i][c]);
   if (row >= p.rows) return;
   const Int8Scale s(int8_scale(top));
   if (part == 0) p.scales[row] = s.scale;
   const int kp = (p.K + 127) / 128 * 128;
-  for (int k = part * 16; k < kp; k += 128) {
+  for (int k = part * 16; k < kp; k += 16 * kParts) {
     float v[16];
     load(k, v);
-    uint4 q;
-    unsigned *w = &q.x;
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      w[e] = int8_pack(s.code(v[4 * e]), s.code(v[4 * e + 1]), s.code(v[4 * e + 2]),
-                       s.code(v[4 * e + 3]));
-    *reinterpret_cast<uint4 *>(p.codes + row * p.ldq + (k / 128) * p.slice + k % 128) = q;
+    unsigned c[4];
+    int8_codes<16>(s, v, c);
+    *reinterpret_cast<uint4 *>(p.codes + row * p.ldq + (k / 128) * p.slice + k % 128) =
+        uint4{c[0], c[1], c[2], c[3]};
   }
 }
 
@@ -117,12 +117,12 @@ __global__ void __launch_bounds__(256) int8_quantize_transposed_kernel(Int8CastA
 hipError_t launch_int8_quantize(bool trans, bool bf16, const Int8CastArgs &p, hipStream_t s) {
   const dim3 block(256);
   if (trans) {
-    const dim3 grid((unsigned)((p.rows + 31L) / 32));
+    const dim3 grid((unsigned)((p.rows + 31L) / 32)), wide(32 * kParts);
     if (bf16)
-      hipLaunchKernelGGL(int8_quantize_transposed_kernel<true>, grid, block, 0, s, p);
+      hipLaunchKernelGGL(int8_quantize_transposed_kernel<true>, grid, wide, 0, s, p);
     else
-      hipLaunchKernelGGL(int8_quantize_transposed_kernel<false>, grid, block, 0, s, p);
-  } else if (p.K > 1024) {
+      hipLaunchKernelGGL(int8_quantize_transposed_kernel<false>, grid, wide, 0, s, p);
+  } else if (p.K > 2048) {
     const dim3 grid((unsigned)p.rows);
     if (bf16)
       hipLaunchKernelGGL((int8_quantize_kernel<true, 256>), grid, block, 0, s, p);

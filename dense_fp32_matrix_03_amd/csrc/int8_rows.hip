@@ -28,66 +28,49 @@ namespace {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
-// All of A's rows (GROUPED: up to 16 MT of a group's), MT blocks of 16, and NT
-// blocks of 16 rows of B per work-group; KS waves split k in units of 256.
-// TA: A's type (SGEMM_TYPE_*).
-template <int MT, int NT, int KS, int TA, bool CBF16, bool GROUPED>
+// All of A's rows, 16 at most (GROUPED: 16 of a group's), and 16 rows of B per
+// work-group; KS waves split k in units of 256.  TA: A's type (SGEMM_TYPE_*).
+template <int KS, int TA, bool CBF16, bool GROUPED>
 __global__ void __launch_bounds__(KS *kWave) int8_rows_kernel(Int8Args p, GroupMap map) {
   constexpr bool CAST = TA != SGEMM_TYPE_INT8;
-  static_assert(!CAST || MT == 1, "only 16 rows are cast on the way");
   constexpr int kUnit = 256;
   const int lane = threadIdx.x % kWave;
   const int kq = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int r16 = lane % 16, q = lane / 16;
   const int kp = (p.K + 127) / 128 * 128;
   long a_row = 0, b_row = 0;  // first rows of A (and C) and of B
-  int n0 = blockIdx.x * NT * 16, M = p.M;
+  int n0 = blockIdx.x * 16, M = p.M;
   if constexpr (GROUPED) {
-    const GroupTile t = group_tile(p.offsets, p.groups, p.M, 16 * MT, map);
+    const GroupTile t = group_tile(p.offsets, p.groups, p.M, 16, map);
     if (!t.valid) return;
-    a_row = t.row0 + t.tm * (16 * MT);
+    a_row = t.row0 + t.tm * 16;
     b_row = (long)t.g * p.N;
-    n0 = t.tn * NT * 16;
-    M = min(t.rows - t.tm * (16 * MT), 16 * MT);
+    n0 = t.tn * 16;
+    M = min(t.rows - t.tm * 16, 16);
   }
 
   // Rows past the end repeat the last one: what they give is not stored.
-  const char *a_at[MT], *b_at[NT];
-#pragma unroll
-  for (int i = 0; i < MT; ++i)
-    a_at[i] = p.a.codes + (a_row + min(16 * i + r16, M - 1)) * p.a.ld;
-  float scale_b[NT];
-#pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    const long r = b_row + min(n0 + 16 * j + r16, p.N - 1);
-    b_at[j] = p.b.codes + r * p.b.ld;
-    scale_b[j] = p.K > 0 ? p.b.scales[r] : 0.f;
-  }
-  i32x4 acc[MT][NT];
-#pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int j = 0; j < NT; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+  const char *const a_at = p.a.codes + (a_row + min(r16, M - 1)) * p.a.ld;
+  const long b_at_row = b_row + min(n0 + r16, p.N - 1);
+  const char *const b_at = p.b.codes + b_at_row * p.b.ld + 64 * q;
+  const float scale_b = p.K > 0 ? p.b.scales[b_at_row] : 0.f;
+  i32x4 acc = {0, 0, 0, 0};
 
   struct Operand {
-    i32x4 a[MT][4], b[NT][4];
+    i32x4 a[4], b[4];
   };
   // Quarters past the padded k give zeros.
   auto load = [&](int k, Operand &o, auto whole) {
     const bool in = decltype(whole)::value || k + 64 * q < kp;
     const i32x4 zero = {0, 0, 0, 0};
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
+    for (int s = 0; s < 4; ++s)
+      o.b[s] = in ? *reinterpret_cast<const i32x4 *>(b_at + k + 16 * s) : zero;
+    if constexpr (!CAST) {
+      const char *const at = a_at + (k / 128 + q / 2) * p.a.slice + 64 * (q % 2);
 #pragma unroll
       for (int s = 0; s < 4; ++s)
-        o.b[j][s] = in ? *reinterpret_cast<const i32x4 *>(b_at[j] + k + 64 * q + 16 * s) : zero;
-    if constexpr (!CAST) {
-      const long a_k = (k / 128 + q / 2) * p.a.slice + 64 * (q % 2);
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int s = 0; s < 4; ++s)
-          o.a[i][s] = in ? *reinterpret_cast<const i32x4 *>(a_at[i] + a_k + 16 * s) : zero;
+        o.a[s] = in ? *reinterpret_cast<const i32x4 *>(at + 16 * s) : zero;
     }
   };
   auto load_any = [&](int k, Operand &o) {
@@ -104,7 +87,7 @@ __global__ void __launch_bounds__(KS *kWave) int8_rows_kernel(Int8Args p, GroupM
   constexpr int kPitch = 272 / 4;
   __shared__ __attribute__((aligned(16))) unsigned cast_codes[CAST ? KS * 16 * kPitch : 4];
   __shared__ unsigned tops[CAST ? KS : 1][16];
-  __shared__ float scales[16];
+  __shared__ float scales[16], inverses[16];
   constexpr bool BF16 = TA == SGEMM_TYPE_BF16;
   const long row_bytes = p.a.ld * (BF16 ? 2 : 4);
   const char *const x = p.a.codes + a_row * row_bytes;
@@ -156,17 +139,19 @@ __global__ void __launch_bounds__(KS *kWave) int8_rows_kernel(Int8Args p, GroupM
       unsigned top = 0;
 #pragma unroll
       for (int w = 0; w < KS; ++w) top = max(top, tops[w][threadIdx.x]);
-      scales[threadIdx.x] = int8_scale(top);
+      const Int8Scale s(int8_scale(top));
+      scales[threadIdx.x] = s.scale;
+      inverses[threadIdx.x] = s.inverse;
     }
     __syncthreads();
   }
   auto cast = [&](int k, Operand &o) {
     unsigned *codes = cast_codes + kq * 16 * kPitch;
     for (int r = 0; r < M; ++r) {
-      const Int8Scale s(scales[r]);
+      const Int8Scale s(scales[r], inverses[r]);
       float v[4];
       values(r, k, v);
-      codes[r * kPitch + lane] = int8_pack(s.code(v[0]), s.code(v[1]), s.code(v[2]), s.code(v[3]));
+      int8_codes<4>(s, v, codes + r * kPitch + lane);
     }
     // The wave's own LDS accesses keep their order; the fence keeps the
     // compiler's.
@@ -174,7 +159,7 @@ __global__ void __launch_bounds__(KS *kWave) int8_rows_kernel(Int8Args p, GroupM
     const int r = min(r16, M - 1);
 #pragma unroll
     for (int s = 0; s < 4; ++s)
-      o.a[0][s] = *reinterpret_cast<const i32x4 *>(codes + r * kPitch + q * 16 + s * 4);
+      o.a[s] = *reinterpret_cast<const i32x4 *>(codes + r * kPitch + q * 16 + s * 4);
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   };
 
@@ -184,79 +169,58 @@ __global__ void __launch_bounds__(KS *kWave) int8_rows_kernel(Int8Args p, GroupM
     if constexpr (CAST) cast(k, cur);
 #pragma unroll
     for (int s = 0; s < 4; ++s)
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(cur.a[i][s], cur.b[j][s], acc[i][j], 0,
-                                                            0, 0);
+      acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(cur.a[s], cur.b[s], acc, 0, 0, 0);
     cur = nxt;
   }
 
-  __shared__ i32x4 red[(KS - 1) * MT * NT * kWave];
-  if (kq > 0) {
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-        red[((kq - 1) * MT * NT + i * NT + j) * kWave + lane] = acc[i][j];
-  }
+  __shared__ i32x4 red[(KS - 1) * kWave];
+  if (kq > 0) red[(kq - 1) * kWave + lane] = acc;
   __syncthreads();
   if (kq > 0) return;
 #pragma unroll
-  for (int s = 0; s < KS - 1; ++s)
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int j = 0; j < NT; ++j) acc[i][j] += red[(s * MT * NT + i * NT + j) * kWave + lane];
+  for (int s = 0; s < KS - 1; ++s) acc += red[s * kWave + lane];
 
-  // Register e of lane l holds row 4 (l / 16) + e, column l % 16 of a block.
+  // Register e of lane l holds row 4 (l / 16) + e, column l % 16 of the block.
   using T = std::conditional_t<CBF16, __bf16, float>;
+  const int n = n0 + r16;
+  if (n >= p.N) return;
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int m = 16 * i + 4 * q + e;
-      if (m >= M) continue;
-      float sa = 0.f;
-      if (p.K > 0) sa = CAST ? scales[m] : p.a.scales[a_row + m];
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const int n = n0 + 16 * j + r16;
-        if (n >= p.N) continue;
-        T *const C = static_cast<T *>(p.C) + (a_row + m) * p.ldc + n;
-        const float v = int8_value(acc[i][j][e], sa, scale_b[j]);
-        *C = (T)(p.beta == 0.f ? p.alpha * v : fmaf(p.alpha, v, p.beta * (float)*C));
-      }
-    }
+  for (int e = 0; e < 4; ++e) {
+    const int m = 4 * q + e;
+    if (m >= M) continue;
+    float sa = 0.f;
+    if (p.K > 0) sa = CAST ? scales[m] : p.a.scales[a_row + m];
+    T *const C = static_cast<T *>(p.C) + (a_row + m) * p.ldc + n;
+    const float v = int8_value(acc[e], sa, scale_b);
+    *C = (T)(p.beta == 0.f ? p.alpha * v : fmaf(p.alpha, v, p.beta * (float)*C));
+  }
 }
 
-template <int MT, int NT, int KS, int TA, bool GROUPED>
-hipError_t launch_sets(const Int8Args &p, bool c_bf16, hipStream_t s) {
-  const int tiles_n = (int)((p.N + NT * 16L - 1) / (NT * 16));
-  const long rows = GROUPED ? group_tile_rows(p.M, p.groups, 16 * MT) : 1;
+template <int KS, int TA, bool GROUPED>
+hipError_t launch(const Int8Args &p, bool c_bf16, hipStream_t s) {
+  const int tiles_n = (int)((p.N + 15L) / 16);
+  const long rows = GROUPED ? group_tile_rows(p.M, p.groups, 16) : 1;
   const dim3 grid((unsigned)(rows * tiles_n)), block(KS * kWave);
   const GroupMap map = make_group_map(tiles_n);
   if (c_bf16)
-    hipLaunchKernelGGL((int8_rows_kernel<MT, NT, KS, TA, true, GROUPED>), grid, block, 0, s, p, map);
+    hipLaunchKernelGGL((int8_rows_kernel<KS, TA, true, GROUPED>), grid, block, 0, s, p, map);
   else
-    hipLaunchKernelGGL((int8_rows_kernel<MT, NT, KS, TA, false, GROUPED>), grid, block, 0, s, p, map);
+    hipLaunchKernelGGL((int8_rows_kernel<KS, TA, false, GROUPED>), grid, block, 0, s, p, map);
   return hipGetLastError();
 }
 
-template <int MT, int NT, int TA>
-hipError_t launch(const Int8Args &p, bool c_bf16, hipStream_t s) {
-  return p.K > 1024 ? launch_sets<MT, NT, 8, TA, false>(p, c_bf16, s)
-                    : launch_sets<MT, NT, 4, TA, false>(p, c_bf16, s);
-}
-
+// Eight waves where there are more than four units of k.
 template <int TA>
 hipError_t launch_rows(const Int8Args &p, bool c_bf16, hipStream_t s) {
-  return p.offsets ? launch_sets<1, 1, 4, TA, true>(p, c_bf16, s) : launch<1, 1, TA>(p, c_bf16, s);
+  if (p.offsets) return launch<4, TA, true>(p, c_bf16, s);
+  return p.K > 1024 ? launch<8, TA, false>(p, c_bf16, s) : launch<4, TA, false>(p, c_bf16, s);
 }
 
 // Rows spread thin over groups, in few work-groups (16 columns each; the host
-// counts a row of tiles for each group that can have rows).
+// counts a row of tiles for each group that can have rows).  With the cast first: 8
+// groups, 16 rows by 4096 x 4096 26 us (tiles of 64 x 64 35), 16 groups, 24 rows by 2048 x
+// 2048 14.7 (15.7); 8 groups, 64 rows by 4096 x 4096 41 (40), 64 groups, 512 rows by 1024
+// x 1024 27 (19).
 bool spread_thin(const Int8Args &p, int cus) {
   const long groups = p.groups < p.M ? p.groups : p.M;
   return p.M <= 2L * p.groups && groups * ((p.N + 15L) / 16) <= 8L * cus;
@@ -264,17 +228,29 @@ bool spread_thin(const Int8Args &p, int cus) {
 
 }  // namespace
 
+// Casting a row in every work-group beats a launch of the cast while the values are few
+// and a wave has a single unit of k: 1 x 8192 x 2048 7.2 us against 10.5, 4 x 8192 x 2048
+// 9.1 against 10.8, 8 x 4096 x 1024 8.3 against 9.2; 8 x 8192 x 2048 12.5 against 10.4, 2
+// x 14336 x 4096 22.4 against 17.8.  In groups, a row each: 64 groups, 8 rows by 2048 x
+// 2048 10.9 against 13.8; 16 groups, 24 rows by 2048 x 2048 21.2 against 14.7.
 bool int8_casts(const Int8Args &p, int cus) {
-  if (p.offsets) return spread_thin(p, cus);
-  return p.M <= 16 && (long)p.M * p.K <= 16384;
+  if (p.K > 2048) return false;
+  if (p.offsets)
+    return spread_thin(p, cus) && p.M <= p.groups && (long)p.M * p.K <= 16384;
+  return p.M <= 16 && (long)p.M * p.K <= 8192;
 }
 
+// Up to 16 rows, and rows spread thin over groups, this kernel, but from 5 rows on tiles
+// of 64 x 64 where they reach most of the compute units: 16 x 8192 x 8192 22.9 us here
+// (tiles 24), 16 x 8192 x 2048 11.2 (12.3), 16 x 14336 x 4096 23.0 (16.3); 4 x 14336 x
+// 4096 19.2 (16.3, but 4 x 8192 x 8192 18.7, 24); 32 x 8192 x 8192 in two blocks of 16
+// rows 29.7 (24).
 hipError_t launch_int8_product(const Int8Args &p, int a_type, bool c_bf16, int cus, hipStream_t s) {
   if (a_type == SGEMM_TYPE_F32) return launch_rows<SGEMM_TYPE_F32>(p, c_bf16, s);
   if (a_type == SGEMM_TYPE_BF16) return launch_rows<SGEMM_TYPE_BF16>(p, c_bf16, s);
-  if (p.offsets ? !spread_thin(p, cus) : p.M > 32) return launch_int8_tile(p, c_bf16, cus, s);
-  return p.offsets || p.M <= 16 ? launch_rows<SGEMM_TYPE_INT8>(p, c_bf16, s)
-                                : launch<2, 2, SGEMM_TYPE_INT8>(p, c_bf16, s);
+  const bool few = p.M <= 4 || (p.M <= 16 && 4L * ((p.N + 63L) / 64) < 3L * cus);
+  return (p.offsets ? spread_thin(p, cus) : few) ? launch_rows<SGEMM_TYPE_INT8>(p, c_bf16, s)
+                                                 : launch_int8_tile(p, c_bf16, cus, s);
 }
 
 }  // namespace sgemm

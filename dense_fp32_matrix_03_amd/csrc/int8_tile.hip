@@ -30,10 +30,10 @@ struct Int8Format {
   }
 };
 
-template <int BM, int BN, int WM, int WN, int KS, bool CBF16>
-__global__ void __launch_bounds__(WM *WN *KS *kWave, 2)
+template <int BM, int BN, int WM, int WN, int NST, bool CBF16>
+__global__ void __launch_bounds__(WM *WN *kWave, 2)
 int8_tile_kernel(Int8Args p, TileMap tmap, GroupMap map) {
-  using Tile = SliceTile<Int8Format, BM, BN, WM, WN, KS, 2>;
+  using Tile = SliceTile<Int8Format, BM, BN, WM, WN, NST>;
   constexpr int FM = Tile::FM, FN = Tile::FN;
   const int lane = threadIdx.x % kWave, r32 = lane % 32, half = lane / 32;
 
@@ -66,11 +66,9 @@ int8_tile_kernel(Int8Args p, TileMap tmap, GroupMap map) {
       scales_b[i - BM] = sums && i - BM < rows_b ? p.b.scales[b_row + n0 + i - BM] : 0.f;
   }
   i32x16 acc[FM][FN];
-  char *lds[2];
-  const int nk = (p.K + 127) / 128;
-  if (!Tile::run(p.a.tile_rows(a_row + m0, rows_a), p.b.tile_rows(b_row + n0, rows_b), nk, 0, acc,
-                 lds))
-    return;
+  char *lds[NST];
+  Tile::run(p.a.tile_rows(a_row + m0, rows_a), p.b.tile_rows(b_row + n0, rows_b),
+            (p.K + 127) / 128, acc, lds);
   // run's barriers lie between the writes above and the reads below, but for K == 0,
   // where scales are not read.
 
@@ -128,41 +126,58 @@ int8_tile_kernel(Int8Args p, TileMap tmap, GroupMap map) {
     store(std::false_type(), std::false_type());
 }
 
-template <int BM, int BN, int WM, int WN, int KS>
+template <int BM, int BN, int WM, int WN, int NST>
 hipError_t launch(const Int8Args &p, bool c_bf16, hipStream_t s) {
   const int tiles_m = (p.M + BM - 1) / BM, tiles_n = (p.N + BN - 1) / BN;
   const long rows = p.offsets ? group_tile_rows(p.M, p.groups, BM) : tiles_m;
-  const dim3 grid((unsigned)(rows * tiles_n)), block(WM * WN * KS * kWave);
+  const dim3 grid((unsigned)(rows * tiles_n)), block(WM * WN * kWave);
   const TileMap tmap = make_tile_map(tiles_m, tiles_n, kGroupRaster);
   const GroupMap map = make_group_map(tiles_n);
   if (c_bf16)
-    hipLaunchKernelGGL((int8_tile_kernel<BM, BN, WM, WN, KS, true>), grid, block, 0, s, p, tmap,
+    hipLaunchKernelGGL((int8_tile_kernel<BM, BN, WM, WN, NST, true>), grid, block, 0, s, p, tmap,
                        map);
   else
-    hipLaunchKernelGGL((int8_tile_kernel<BM, BN, WM, WN, KS, false>), grid, block, 0, s, p, tmap,
+    hipLaunchKernelGGL((int8_tile_kernel<BM, BN, WM, WN, NST, false>), grid, block, 0, s, p, tmap,
                        map);
   return hipGetLastError();
 }
 
 }  // namespace
 
+// The tile by times in microseconds: rounds of tiles on the compute units, each with nk
+// slices of 128 k.  Groups count with their mean length: the host does not know more.
+// Measured on 256 compute units, A cast first (5 to 8 us of it) and C of bfloat16, tiles
+// of 64 x 64 / 128 x 128 / 128 x 256 / 256 x 256:
+//   N = K = 8192   M = 64   26 / 36 / 55 / 88     M = 256  43 / 45 / 61 / 98
+//                  M = 512  76 / 49 / 63 / 101    M = 1024 136 / 91 / 75 / 106
+//                  M = 2048 258 / 174 / 143 / 128
+//   8192 x 2048    M = 128  13 / 16 / 20 / 30     M = 1024 39 / 32 / 29 / 34
+// Stages of a 64 x 64 tile, 2 / 3 / 4: 64 x 8192 x 8192 49 / - / 26 us (two sets of waves
+// over k 37, four 32); in groups, where many tiles share a compute unit, 32 groups,
+// 48 rows by 4096 x 2048 48 / 43 / 44, 32 groups, 600 rows by 2048 x 2048 45 / 38 / 40, 64
+// groups, 512 rows by 1024 x 1024 19.0 / 21.6 / 20.9.  In groups, 64 x 64 and 128 x 128:
+// 64 groups, 4099 rows by 1000 x 777 29 and 36, 8 groups, 2000 rows by 4096 x 1024 30 and
+// 35, 16 groups, 8192 rows by 2048 x 2048 93 and 80.
 hipError_t launch_int8_tile(const Int8Args &p, bool c_bf16, int cus, hipStream_t s) {
   const long groups = !p.offsets ? 1 : p.groups < p.M ? p.groups : p.M;
-  const double mean = (double)p.M / groups;
-  auto per_cu = [&](long t) {
-    const double rows = p.offsets ? fmax(1.0, mean / t + 0.5) : ceil(mean / t);
-    return ceil(groups * rows * ((p.N + t - 1) / t) / cus);
+  const double mean = (double)p.M / groups, nk = (p.K + 127) / 128;
+  auto rounds = [&](long bm, long bn) {
+    const double rows = p.offsets ? fmax(1.0, mean / bm + 0.5) : ceil(mean / bm);
+    return ceil(groups * rows * ((p.N + bn - 1) / bn) / cus);
   };
-  const double n64 = per_cu(64), n128 = per_cu(128);
-  const double c64 = n64 == 1 ? 0.35 : n64 == 2 ? 0.42 : 0.16 * n64;
-  const double c128 = n128 == 1 ? 0.65 : n128 == 2 ? 0.77 : 0.29 * n128;
-  if ((p.offsets && mean <= 64) || (c64 <= c128 && c64 <= per_cu(256))) {
-    if (n64 == 1 && p.K >= 6144) return launch<64, 64, 2, 2, 4>(p, c_bf16, s);
-    if (n64 == 2 && p.K >= 6144) return launch<64, 64, 2, 2, 2>(p, c_bf16, s);
-    return launch<64, 64, 2, 2, 1>(p, c_bf16, s);
-  }
-  return c128 <= per_cu(256) ? launch<128, 128, 2, 2, 1>(p, c_bf16, s)
-                             : launch<256, 256, 2, 4, 1>(p, c_bf16, s);
+  const double c64 = rounds(64, 64) * (0.22 * nk + 1.5) + 6;
+  const double c128 = rounds(128, 128) * (0.6 * nk + 2.5) + 6;
+  const double c128x256 = rounds(128, 256) * (nk + 3.5) + 6;
+  const double c256 = rounds(256, 256) * (1.55 * nk + 5) + 12;
+  const double large = fmin(c128x256, c256);
+  // Groups of unequal length leave larger tiles emptier.
+  if (p.offsets ? mean <= 96 || c64 <= 1.3 * fmin(c128, large) : c64 <= fmin(c128, large))
+    return !p.offsets ? launch<64, 64, 2, 2, 4>(p, c_bf16, s)
+           : nk <= 8  ? launch<64, 64, 2, 2, 2>(p, c_bf16, s)
+                      : launch<64, 64, 2, 2, 3>(p, c_bf16, s);
+  if (c128 <= large) return launch<128, 128, 2, 4, 4>(p, c_bf16, s);
+  return c128x256 <= c256 ? launch<128, 256, 2, 4, 3>(p, c_bf16, s)
+                          : launch<256, 256, 2, 4, 2>(p, c_bf16, s);
 }
 
 }  // namespace sgemm

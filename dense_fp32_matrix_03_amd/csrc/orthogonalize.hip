@@ -188,11 +188,11 @@ __device__ __forceinline__ void triangle_tile(int id, int &tm, int &tn) {
 // and 1 KiB of consecutive bytes an instruction.  Straight from the registers' layout,
 // with 2 and 8 bytes a lane over rows 128 bytes apart, E and the two results took
 // 45 of 105 us of a 2048 x 4096 x 2048 product.
-template <int BM, int BN, int WM, int WN, int KS, int NST, bool SYMMETRIC>
-__global__ void __launch_bounds__(WM *WN *KS *kWave, 2)
+template <int BM, int BN, int WM, int WN, int NST, bool SYMMETRIC>
+__global__ void __launch_bounds__(WM *WN *kWave, 2)
 ortho_product_kernel(OrthoProductArgs p, TileMap map, FastDiv by_triangle, int triangle,
                      bool y_bf16) {
-  using Tile = SliceTile<SplitFormat, BM, BN, WM, WN, KS, NST>;
+  using Tile = SliceTile<SplitFormat, BM, BN, WM, WN, NST>;
   constexpr int FM = Tile::FM, FN = Tile::FN;
   static_assert(Tile::STAGE_BYTES >= WM * WN * 4096 && NST >= 3, "a block per wave and image");
   const int lane = threadIdx.x % kWave, r32 = lane % 32, half = lane / 32;
@@ -230,8 +230,7 @@ ortho_product_kernel(OrthoProductArgs p, TileMap map, FastDiv by_triangle, int t
   };
   f32x16 acc[FM][FN];
   char *lds[NST];
-  if (!Tile::run(rows(p.a, m0, rows_a), rows(p.b, n0, rows_b), (p.a.cols + 31) / 32, 0, acc, lds))
-    return;
+  Tile::run(rows(p.a, m0, rows_a), rows(p.b, n0, rows_b), (p.a.cols + 31) / 32, acc, lds);
   __syncthreads();  // no loads into the stages are left, of any wave
   const int wave = Tile::wave_id();
   const BlockImage e_image{lds[0] + wave * 4096}, t_image{lds[1] + wave * 4096},
@@ -317,22 +316,22 @@ ortho_product_kernel(OrthoProductArgs p, TileMap map, FastDiv by_triangle, int t
     }
 }
 
-template <int BM, int BN, int WM, int WN, int KS, int NST>
+template <int BM, int BN, int WM, int WN, int NST>
 hipError_t launch(const OrthoProductArgs &p, bool symmetric, bool y_bf16, int batch,
                   hipStream_t s) {
   const int tiles_m = (p.a.rows + BM - 1) / BM, tiles_n = (p.b.rows + BN - 1) / BN;
   const TileMap map = make_tile_map(tiles_m, tiles_n, 8);
-  const dim3 block(WM * WN * KS * kWave);
+  const dim3 block(WM * WN * kWave);
   if constexpr (BM == BN) {
     if (symmetric) {
       const int triangle = tiles_m * (tiles_m + 1) / 2;
-      hipLaunchKernelGGL((ortho_product_kernel<BM, BN, WM, WN, KS, NST, true>),
+      hipLaunchKernelGGL((ortho_product_kernel<BM, BN, WM, WN, NST, true>),
                          dim3((unsigned)(triangle * batch)), block, 0, s, p, map,
                          make_fast_div(triangle), triangle, y_bf16);
       return hipGetLastError();
     }
   }
-  hipLaunchKernelGGL((ortho_product_kernel<BM, BN, WM, WN, KS, NST, false>),
+  hipLaunchKernelGGL((ortho_product_kernel<BM, BN, WM, WN, NST, false>),
                      dim3((unsigned)((long)tiles_m * tiles_n * batch)), block, 0, s, p, map,
                      make_fast_div(1), 1, y_bf16);
   return hipGetLastError();
@@ -384,16 +383,16 @@ hipError_t launch_ortho_product(const OrthoProductArgs &p, bool symmetric, bool 
   const double c64 = ceil(n64) * (0.2 * nk + 2);
   if (symmetric) {
     const double c128 = ceil(n128) * (0.38 * nk + 6 + 12 * fmin(n128, 1));
-    return c64 <= c128 ? launch<64, 64, 2, 2, 1, 4>(p, true, y_bf16, batch, s)
-                       : launch<128, 128, 2, 4, 1, 3>(p, true, y_bf16, batch, s);
+    return c64 <= c128 ? launch<64, 64, 2, 2, 4>(p, true, y_bf16, batch, s)
+                       : launch<128, 128, 2, 4, 3>(p, true, y_bf16, batch, s);
   }
   const double c128 =
       fmax(1, (ceil(n128) + n128) / 2) * ((0.38 + 0.22 * fmin(n128, 1)) * nk + 11);
   const double n256 = tiles(128, 256);
   const double c256 = ceil(n256) * (0.85 * nk + 12 + 50 * fmin(fmax(n256 - 0.6, 0), 0.4));
-  if (c64 <= c128 && c64 <= c256) return launch<64, 64, 2, 2, 1, 4>(p, false, y_bf16, batch, s);
-  return c128 <= c256 ? launch<128, 128, 2, 4, 1, 3>(p, false, y_bf16, batch, s)
-                      : launch<128, 256, 2, 4, 1, 3>(p, false, y_bf16, batch, s);
+  if (c64 <= c128 && c64 <= c256) return launch<64, 64, 2, 2, 4>(p, false, y_bf16, batch, s);
+  return c128 <= c256 ? launch<128, 128, 2, 4, 3>(p, false, y_bf16, batch, s)
+                      : launch<128, 256, 2, 4, 3>(p, false, y_bf16, batch, s);
 }
 
 }  // namespace sgemm

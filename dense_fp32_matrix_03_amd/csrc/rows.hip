@@ -3,7 +3,7 @@
 //
 // Bound by memory.  A wave has a piece of up to 4096 bytes of a row, 16 bytes a
 // lane in each of four loads that go out together.
-#include "mxfp4.hpp"
+#include "piece.hpp"
 #include "route.hpp"
 
 namespace sgemm {
@@ -11,61 +11,6 @@ namespace sgemm {
 namespace {
 
 constexpr int kUnits = 4;  // waves of a work-group
-
-// 16 bytes of a row, at any element: V values, zeros and no access past the n-th.
-template <bool BF16>
-struct Piece {
-  static constexpr int V = BF16 ? 8 : 4;
-  using T = std::conditional_t<BF16, unsigned short, float>;
-  using Raw = std::conditional_t<BF16, u32x4_any, f32x4_any>;
-  Raw raw;
-  __device__ __forceinline__ void load(const void *row, long at, int n) {
-    const T *x = static_cast<const T *>(row) + at;
-    if (n >= V) {
-      raw = *reinterpret_cast<const Raw *>(x);
-    } else {
-      T v[V];
-#pragma unroll
-      for (int e = 0; e < V; ++e) v[e] = e < n ? x[e] : T(0);
-      __builtin_memcpy(&raw, v, 16);
-    }
-  }
-  __device__ __forceinline__ void store(void *row, long at, int n) const {
-    T *x = static_cast<T *>(row) + at;
-    if (n >= V) {
-      *reinterpret_cast<Raw *>(x) = raw;
-    } else {
-      T v[V];
-      __builtin_memcpy(v, &raw, 16);
-#pragma unroll
-      for (int e = 0; e < V; ++e)
-        if (e < n) x[e] = v[e];
-    }
-  }
-  __device__ __forceinline__ void get(float v[V]) const {
-    if constexpr (BF16) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v[2 * e] = __uint_as_float(raw[e] << 16);
-        v[2 * e + 1] = __uint_as_float(raw[e] & 0xffff0000u);
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = raw[e];
-    }
-  }
-  __device__ __forceinline__ void set(const float v[V]) {
-    if constexpr (BF16) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        raw[e] = __builtin_bit_cast(unsigned short, (__bf16)v[2 * e]) |
-                 (unsigned)__builtin_bit_cast(unsigned short, (__bf16)v[2 * e + 1]) << 16;
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) raw[e] = v[e];
-    }
-  }
-};
 
 // The unit (row and piece of it) of a wave; false past the last.
 __device__ __forceinline__ bool unit_of(const RowsArgs &p, long &row, int &piece) {
@@ -86,12 +31,13 @@ __global__ void __launch_bounds__(kUnits *kWave) rows_gather_kernel(RowsArgs p) 
   if (source < 0 || source >= p.limit) return;
   const int lane = threadIdx.x % kWave;
   const int n0 = piece * (kRowPiece / 16 * P::V) + lane * P::V;
+  const bool whole = (piece + 1) * (kRowPiece / 16 * P::V) <= p.N;
   const long x = (long)(source / p.topk) * p.ldx, y = r * p.ldy;
   P v[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int n = n0 + i * kWave * P::V;
-    v[i].load(p.X, x + n, p.N - n);
+    v[i].load(p.X, x + n, p.N - n, whole);
   }
   if (p.weights) {
     const float w = p.weights[source];
@@ -119,6 +65,7 @@ __global__ void __launch_bounds__(kUnits *kWave) rows_combine_kernel(RowsArgs p)
   if (!unit_of(p, t, piece)) return;
   const int lane = threadIdx.x % kWave;
   const int n0 = piece * (kRowPiece / 16 * P::V) + lane * P::V;
+  const bool whole = (piece + 1) * (kRowPiece / 16 * P::V) <= p.N;
   float sum[4][P::V];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -133,7 +80,7 @@ __global__ void __launch_bounds__(kUnits *kWave) rows_combine_kernel(RowsArgs p)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int n = n0 + i * kWave * P::V;
-      v[i].load(p.X, place * p.ldx + n, p.N - n);
+      v[i].load(p.X, place * p.ldx + n, p.N - n, whole);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -167,24 +114,33 @@ __global__ void __launch_bounds__(kUnits *kWave) rows_combine_backward_kernel(Ro
   const long dy = pair / p.topk * p.lddy;
   const float w = p.weights ? p.weights[pair] : 1.f;
   float dot = 0.f;
-  for (int n = lane * P::V; n < p.N; n += kWave * P::V) {
-    P v;
-    float g[P::V];
-    v.load(p.dY, dy + n, p.N - n);
-    v.get(g);
-    if (p.dweights) {
-      P x;
-      float f[P::V];
-      x.load(p.X, place * p.ldx + n, p.N - n);
-      x.get(f);
+  // Two steps' loads go out together.
+  constexpr int kStep = kWave * P::V, kTogether = 2;
+  for (int n0 = 0; n0 < p.N; n0 += kTogether * kStep) {
+    P g[kTogether], x[kTogether];
+    const bool whole = n0 + kTogether * kStep <= p.N;
 #pragma unroll
-      for (int e = 0; e < P::V; ++e) dot = fmaf(f[e], g[e], dot);
+    for (int i = 0; i < kTogether; ++i) {
+      const int n = n0 + i * kStep + lane * P::V;
+      g[i].load(p.dY, dy + n, p.N - n, whole);
+      if (p.dweights) x[i].load(p.X, place * p.ldx + n, p.N - n, whole);
     }
-    if (p.dX) {
 #pragma unroll
-      for (int e = 0; e < P::V; ++e) g[e] *= w;
-      v.set(g);
-      v.store(p.dX, place * p.lddx + n, p.N - n);
+    for (int i = 0; i < kTogether; ++i) {
+      const int n = n0 + i * kStep + lane * P::V;
+      float f[P::V], v[P::V];
+      g[i].get(v);
+      if (p.dweights) {
+        x[i].get(f);
+#pragma unroll
+        for (int e = 0; e < P::V; ++e) dot = fmaf(f[e], v[e], dot);
+      }
+      if (p.dX) {
+#pragma unroll
+        for (int e = 0; e < P::V; ++e) v[e] *= w;
+        g[i].set(v);
+        g[i].store(p.dX, place * p.lddx + n, p.N - n);
+      }
     }
   }
   if (p.dweights) {

@@ -69,43 +69,37 @@ struct SliceRows {
   }
 };
 
-// KS sets of WM x WN waves share a tile; set q takes slices q, q + KS, ..
-// through LDS stages of its own, and the sets' sums are added in order at the
-// end.  With few tiles the time is a chain of slices, each as long as its
-// loads take to arrive: the sets walk KS chains at once.
-template <class F, int BM, int BN, int WM, int WN, int KS, int NST>
+// WM x WN waves have a tile of BM x BN.
+template <class F, int BM, int BN, int WM, int WN, int NST>
 struct SliceTile {
-  static constexpr int NW = WM * WN;  // waves of a set
+  static constexpr int NW = WM * WN;  // waves
   static constexpr int WTM = BM / WM, WTN = BN / WN, FM = WTM / 32, FN = WTN / 32;
-  static constexpr int kThreads = NW * KS * kWave;
+  static constexpr int kThreads = NW * kWave;
   static constexpr int QA = BM * kSliceRow / 1024 / NW, QB = BN * kSliceRow / 1024 / NW;
   static_assert(QA * NW * 1024 == BM * kSliceRow && QB * NW * 1024 == BN * kSliceRow,
                 "loads must split evenly over the waves");
   static constexpr int kLoads = QA + QB;
   using Acc = typename F::Acc;
-  using Word = decltype(Acc()[0] + Acc()[0]);
 
   // Where this wave's sums lie in the tile.
   __device__ __forceinline__ static int wave_id() {
-    return __builtin_amdgcn_readfirstlane(threadIdx.x / kWave) % NW;
+    return __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   }
   __device__ __forceinline__ static int row0() { return wave_id() / WN * WTM; }
   __device__ __forceinline__ static int col0() { return wave_id() % WN * WTN; }
 
-  // acc = the tile's sums over nk slices, from the `start`-th on and round to it.
-  // False for waves whose sums went to another set.  lds: the stages' memory, which is
-  // free once every wave has passed a barrier after this (STAGE_BYTES each).
-  static constexpr int STAGE_BYTES = KS * (BM + BN) * kSliceRow;
-  __device__ __forceinline__ static bool run(const SliceRows &rows_a, const SliceRows &rows_b,
-                                             int nk, int start, Acc (&acc)[FM][FN],
-                                             char *(&lds)[NST]) {
+  // acc = the tile's sums over nk slices.  lds: the stages' memory, which is free once
+  // every wave has passed a barrier after this (STAGE_BYTES each).
+  static constexpr int STAGE_BYTES = (BM + BN) * kSliceRow;
+  __device__ __forceinline__ static void run(const SliceRows &rows_a, const SliceRows &rows_b,
+                                             int nk, Acc (&acc)[FM][FN], char *(&lds)[NST]) {
     const SliceRows a = rows_a.uniform(), b = rows_b.uniform();
     // One LDS array per stage, so that the compiler sees that loads into one stage do
     // not touch the one that is read (mfma_dma.hpp).  It tells four arrays apart; with
     // one for each operand of four stages it waited for all loads before most reads.
     constexpr int SA = BM * kSliceRow / 4, SB = BN * kSliceRow / 4;
     static_assert(NST >= 2 && NST <= 4, "two to four stages");
-    constexpr auto room = [](int stage) { return stage < NST ? KS * (SA + SB) : 4; };
+    constexpr auto room = [](int stage) { return stage < NST ? SA + SB : 4; };
     __shared__ __attribute__((aligned(1024))) float stage0[room(0)], stage1[room(1)];
     __shared__ __attribute__((aligned(16))) float stage2[room(2)], stage3[room(3)];
 
@@ -114,16 +108,14 @@ struct SliceTile {
       for (int i = 0; i < NST; ++i) lds[i] = reinterpret_cast<char *>(all[i]);
     }
     const int lane = threadIdx.x % kWave;
-    const int all_waves = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int kq = KS > 1 ? all_waves / NW : 0;
-    const int wave = KS > 1 ? all_waves % NW : all_waves;
+    const int wave = wave_id();
     const int wm = wave / WN, wn = wave % WN;
     const int r32 = lane % 32, half = lane / 32;
     auto stage_a = [&](auto S) -> float * {
       constexpr int s = decltype(S)::value;
-      return (s == 0 ? stage0 : s == 1 ? stage1 : s == 2 ? stage2 : stage3) + kq * SA;
+      return s == 0 ? stage0 : s == 1 ? stage1 : s == 2 ? stage2 : stage3;
     };
-    auto stage_b = [&](auto S) -> float * { return stage_a(S) + KS * SA + kq * (SB - SA); };
+    auto stage_b = [&](auto S) -> float * { return stage_a(S) + SA; };
 
     // Load q of a wave fetches rows 8 (wave + q NW) .. + 7 of the slice.
     unsigned off_a[QA], off_b[QB];
@@ -140,22 +132,21 @@ struct SliceTile {
       return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, records,
                                                kRawBufferWord3);
     };
-    // Loads of the set's next slice into stage S.  Slices at or past nk get
+    // Loads of the next slice into stage S.  Slices at or past nk get
     // descriptors without records: nothing is fetched.  No branch depends on
     // that, so that the loads can be scheduled between matrix-core instructions.
-    int k = kq;  // the slice
+    int k = 0;  // the slice
     const int end_a = (a.rows - 1) * a.row_step + kSliceRow;
     const int end_b = (b.rows - 1) * b.row_step + kSliceRow;
     auto dma = [&](auto S) {
       const bool live = k < nk;
-      const int at = k + start < nk ? k + start : k + start - nk;
-      const __amdgpu_buffer_rsrc_t ra = rsrc(a.at + at * a.slice_step, live ? end_a : 0);
-      const __amdgpu_buffer_rsrc_t rb = rsrc(b.at + at * b.slice_step, live ? end_b : 0);
+      const __amdgpu_buffer_rsrc_t ra = rsrc(a.at + k * a.slice_step, live ? end_a : 0);
+      const __amdgpu_buffer_rsrc_t rb = rsrc(b.at + k * b.slice_step, live ? end_b : 0);
 #pragma unroll
       for (int q = 0; q < QA; ++q) lds_dma<true>(ra, stage_a(S) + (wave + q * NW) * 256, off_a[q]);
 #pragma unroll
       for (int q = 0; q < QB; ++q) lds_dma<true>(rb, stage_b(S) + (wave + q * NW) * 256, off_b[q]);
-      k += KS;
+      ++k;
     };
 
     const int sw = kc_swizzle<32, true>(r32);
@@ -262,16 +253,15 @@ struct SliceTile {
     };
 
     if (nk > 0) {
-      const int turns = (nk + KS - 1) / KS;  // the same for all sets: they share the barriers
       static_for<NST>([&](auto S) { dma(S); });
       slice_barrier<(NST - 1) * kLoads>();
       read_ahead(S0(), cur);
       // Whole rounds of the stages without a test between them, then the rest: at a
       // branch the compiler would lose count of the loads on their way.
       int t = 0;
-      for (; t + NST <= turns; t += NST) static_for<NST>([&](auto S) { slice(S); });
+      for (; t + NST <= nk; t += NST) static_for<NST>([&](auto S) { slice(S); });
       static_for<NST - 1>([&](auto S) {
-        if (t + decltype(S)::value < turns) slice(S);
+        if (t + decltype(S)::value < nk) slice(S);
       });
       // The last slices sent loads past the end (no memory traffic): let them
       // retire before the work-group gives up its LDS.
@@ -282,29 +272,6 @@ struct SliceTile {
     for (int c = 0; c + 1 < kChains; ++c)
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[0][0][e] += chain[c][e];
-
-    if constexpr (KS > 1) {
-      // The stages are free: every load has landed, every operand has been read.
-      // Set s > 0 leaves its sums at 4 Ki (s - 1) of the first stage.
-      static_assert(FM * FN * NW == 4 && (KS - 1) * 4096 <= KS * (SA + SB),
-                    "a set's sums are 16 KiB");
-      __syncthreads();
-      auto sums = [&](int set) {
-        return reinterpret_cast<Word *>(stage0 + (set - 1) * 4096) + wave * 1024 + lane;
-      };
-      if (kq > 0) {
-        Word *at = sums(kq);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) at[e * kWave] = acc[0][0][e];
-      }
-      __syncthreads();
-      if (kq > 0) return false;
-#pragma unroll
-      for (int set = 1; set < KS; ++set)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) acc[0][0][e] += sums(set)[e * kWave];
-    }
-    return true;
   }
 };
 
