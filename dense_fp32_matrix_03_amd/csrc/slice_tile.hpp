@@ -88,8 +88,8 @@ struct SliceTile {
   __device__ __forceinline__ static int row0() { return wave_id() / WN * WTM; }
   __device__ __forceinline__ static int col0() { return wave_id() % WN * WTN; }
 
-  // acc = the tile's sums over nk slices.  lds: the stages' memory, which is free once
-  // every wave has passed a barrier after this (STAGE_BYTES each).
+  // acc = the tile's sums over nk slices.  lds: the stages' memory (STAGE_BYTES each),
+  // free once all waves have passed another barrier.
   static constexpr int STAGE_BYTES = (BM + BN) * kSliceRow;
   __device__ __forceinline__ static void run(const SliceRows &rows_a, const SliceRows &rows_b,
                                              int nk, Acc (&acc)[FM][FN], char *(&lds)[NST]) {
@@ -111,11 +111,12 @@ struct SliceTile {
     const int wave = wave_id();
     const int wm = wave / WN, wn = wave % WN;
     const int r32 = lane % 32, half = lane / 32;
-    auto stage_a = [&](auto S) -> float * {
+    // An address is the array and a single offset: through more steps than that the
+    // compiler loses sight of the array.
+    auto stage = [&](auto S) -> float * {
       constexpr int s = decltype(S)::value;
       return s == 0 ? stage0 : s == 1 ? stage1 : s == 2 ? stage2 : stage3;
     };
-    auto stage_b = [&](auto S) -> float * { return stage_a(S) + SA; };
 
     // Load q of a wave fetches rows 8 (wave + q NW) .. + 7 of the slice.
     unsigned off_a[QA], off_b[QB];
@@ -143,9 +144,9 @@ struct SliceTile {
       const __amdgpu_buffer_rsrc_t ra = rsrc(a.at + k * a.slice_step, live ? end_a : 0);
       const __amdgpu_buffer_rsrc_t rb = rsrc(b.at + k * b.slice_step, live ? end_b : 0);
 #pragma unroll
-      for (int q = 0; q < QA; ++q) lds_dma<true>(ra, stage_a(S) + (wave + q * NW) * 256, off_a[q]);
+      for (int q = 0; q < QA; ++q) lds_dma<true>(ra, stage(S) + (wave + q * NW) * 256, off_a[q]);
 #pragma unroll
-      for (int q = 0; q < QB; ++q) lds_dma<true>(rb, stage_b(S) + (wave + q * NW) * 256, off_b[q]);
+      for (int q = 0; q < QB; ++q) lds_dma<true>(rb, stage(S) + (SA + (wave + q * NW) * 256), off_b[q]);
       ++k;
     };
 
@@ -155,14 +156,15 @@ struct SliceTile {
     };
     // B first: its operands are needed first.
     auto read_ops = [&](auto S, auto STEP, Ops &o) {
-      auto read = [&](const float *row) {
-        return F::template load<decltype(STEP)::value>(
-            half, [&](int c) { return reinterpret_cast<const slice_i32x4 *>(row + (c ^ sw) * 4); });
+      auto read = [&](int row) {
+        return F::template load<decltype(STEP)::value>(half, [&](int c) {
+          return reinterpret_cast<const slice_i32x4 *>(stage(S) + (row + (c ^ sw) * 4));
+        });
       };
 #pragma unroll
-      for (int j = 0; j < FN; ++j) o.b[j] = read(stage_b(S) + (wn * WTN + j * 32 + r32) * 32);
+      for (int j = 0; j < FN; ++j) o.b[j] = read(SA + (wn * WTN + j * 32 + r32) * 32);
 #pragma unroll
-      for (int i = 0; i < FM; ++i) o.a[i] = read(stage_a(S) + (wm * WTM + i * 32 + r32) * 32);
+      for (int i = 0; i < FM; ++i) o.a[i] = read((wm * WTM + i * 32 + r32) * 32);
     };
 
 #pragma unroll
@@ -195,21 +197,23 @@ struct SliceTile {
     // matrix-core instructions, the reads over the first three quarters of them: they
     // have arrived when the next step begins.
     constexpr int kMfma = FM * FN * F::kMfma, kReads = (FM + FN) * F::kReads;
-    auto interleave = [&](auto last) {
+    auto interleave = [&](auto steps, auto last) {  // of that many steps together
+      constexpr int mfma = kMfma * decltype(steps)::value, reads = kReads * decltype(steps)::value;
       constexpr int loads = decltype(last)::value ? kLoads : 0;
-      static_for<kMfma>([&](auto I) {
+      static_for<mfma>([&](auto I) {
         constexpr int i = decltype(I)::value;
-        constexpr int v = loads * (i + 1) / kMfma - loads * i / kMfma;
-        constexpr int span = (kMfma * 3 + 3) / 4;
-        constexpr int d = kReads * (i + 1 < span ? i + 1 : span) / span -
-                          kReads * (i < span ? i : span) / span;
+        constexpr int v = loads * (i + 1) / mfma - loads * i / mfma;
+        constexpr int span = (mfma * 3 + 3) / 4;
+        constexpr int d = reads * (i + 1 < span ? i + 1 : span) / span -
+                          reads * (i < span ? i : span) / span;
         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                       // matrix core
         if constexpr (d > 0) __builtin_amdgcn_sched_group_barrier(0x100, d, 0);  // DS read
         if constexpr (v > 0) __builtin_amdgcn_sched_group_barrier(0x020, v, 0);  // VMEM read
       });
     };
     using S0 = std::integral_constant<int, 0>;
-    // The set's t-th slice is in stage S, the next ones on their way to the others.
+    using S1 = std::integral_constant<int, 1>;
+    // Slice t is in stage S, the next ones on their way to the others.
     // WHOLE: a wave with one block of 32 x 32 has too few matrix-core
     // instructions in a step to cover the next one's reads, and registers to
     // spare: it reads a whole slice's operands while it multiplies the one
@@ -231,6 +235,8 @@ struct SliceTile {
         dma(S);
         read_ahead(SN(), nxt);
         static_for<kSteps>([&](auto STEP) { mma(STEP, cur[decltype(STEP)::value]); });
+        interleave(std::integral_constant<int, kSteps>(), std::true_type());
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int s = 0; s < kAhead; ++s) cur[s] = nxt[s];
       } else {
@@ -239,13 +245,13 @@ struct SliceTile {
           if constexpr (s < kSteps - 1) {
             read_ops(S, std::integral_constant<int, s + 1>(), nxt[0]);
             mma(STEP, cur[0]);
-            interleave(std::false_type());
+            interleave(S1(), std::false_type());
           } else {
             slice_barrier<(NST - 2) * kLoads>();
             dma(S);
             read_ops(SN(), S0(), nxt[0]);
             mma(STEP, cur[0]);
-            interleave(std::true_type());
+            interleave(S1(), std::true_type());
           }
           cur[0] = nxt[0];
         });
