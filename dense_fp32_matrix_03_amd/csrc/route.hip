@@ -11,9 +11,8 @@
 // values are further apart than twice that, from each other and from the next, are the
 // right ones.  Where some are not (one token in some hundreds), picking goes on until
 // the next value is apart, and what was picked is put in order in double precision;
-// where it is groups that are close, these are chosen again in double precision.  8192 tokens, 256 experts in 8 groups: 28.4 us all in double precision
-// with exchanges through LDS.  Without bias and groups the logits are compared, which
-// is exact.
+// where it is groups that are close, these are chosen again in double precision.
+// Without bias and groups the logits are compared, which is exact.
 #include "mxfp4.hpp"
 #include "route.hpp"
 
@@ -413,10 +412,11 @@ __global__ void __launch_bounds__(kTokens *kWave) route_kernel(RouteArgs p) {
     const float sum = wave_sum(w);
     w = sum == 0.f ? 0.f : w / sum;
   }
+  w = pick < 0 ? 0.f : w * p.scale;
   if (odd) w = __uint_as_float(0x7fc00000u);
   if (lane < p.topk) {
     p.picks[t * p.topk + lane] = pick;
-    p.weights[t * p.topk + lane] = w * p.scale;
+    p.weights[t * p.topk + lane] = w;
   }
 }
 

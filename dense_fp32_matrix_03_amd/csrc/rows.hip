@@ -31,7 +31,7 @@ __global__ void __launch_bounds__(kUnits *kWave) rows_gather_kernel(RowsArgs p) 
   if (source < 0 || source >= p.limit) return;
   const int lane = threadIdx.x % kWave;
   const int n0 = piece * (kRowPiece / 16 * P::V) + lane * P::V;
-  const bool whole = (piece + 1) * (kRowPiece / 16 * P::V) <= p.N;
+  const bool whole = p.N - piece * (kRowPiece / 16 * P::V) >= kRowPiece / 16 * P::V;
   const long x = (long)(source / p.topk) * p.ldx, y = r * p.ldy;
   P v[4];
 #pragma unroll
@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(kUnits *kWave) rows_combine_kernel(RowsArgs p)
   if (!unit_of(p, t, piece)) return;
   const int lane = threadIdx.x % kWave;
   const int n0 = piece * (kRowPiece / 16 * P::V) + lane * P::V;
-  const bool whole = (piece + 1) * (kRowPiece / 16 * P::V) <= p.N;
+  const bool whole = p.N - piece * (kRowPiece / 16 * P::V) >= kRowPiece / 16 * P::V;
   float sum[4][P::V];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -116,18 +116,19 @@ __global__ void __launch_bounds__(kUnits *kWave) rows_combine_backward_kernel(Ro
   float dot = 0.f;
   // Two steps' loads go out together.
   constexpr int kStep = kWave * P::V, kTogether = 2;
-  for (int n0 = 0; n0 < p.N; n0 += kTogether * kStep) {
+  for (int left = p.N; left > 0; left -= kTogether * kStep) {
+    const int n0 = p.N - left + lane * P::V;
     P g[kTogether], x[kTogether];
-    const bool whole = n0 + kTogether * kStep <= p.N;
+    const bool whole = left >= kTogether * kStep;
 #pragma unroll
     for (int i = 0; i < kTogether; ++i) {
-      const int n = n0 + i * kStep + lane * P::V;
+      const int n = n0 + i * kStep;
       g[i].load(p.dY, dy + n, p.N - n, whole);
       if (p.dweights) x[i].load(p.X, place * p.ldx + n, p.N - n, whole);
     }
 #pragma unroll
     for (int i = 0; i < kTogether; ++i) {
-      const int n = n0 + i * kStep + lane * P::V;
+      const int n = n0 + i * kStep;
       float f[P::V], v[P::V];
       g[i].get(v);
       if (p.dweights) {

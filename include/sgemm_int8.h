@@ -50,7 +50,7 @@ int64_t sgemm_int8_codes_size(int64_t rows, int64_t K);
  * rows x K with leading dimension ldx >= max(1, K), or with trans == 1 the
  * transpose, K x rows with ldx >= max(1, rows) -- how sgemm_run takes a B
  * whose columns are output channels.  Writes the Kp bytes of each row of the
- * codes, padding included, and the scales.
+ * codes, padding included, and the scales.  rows == 0 or K == 0 is a no-op.
  */
 int sgemm_int8_quantize(int trans, int64_t rows, int64_t K, int type, const void *X, int64_t ldx,
                         void *codes, int64_t ldq, float *scales, void *stream);

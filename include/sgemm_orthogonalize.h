@@ -21,7 +21,7 @@
  * half-precision numbers under a power of two that keeps it in range, 22 bits,
  * and three of the four products of the pieces are added up in single
  * precision.  An operand is off by at most 2^-22 of its value + 2^-39 of the
- * largest that the singular values allow, a product of pieces that is left out
+ * largest that the singular values allow (of 2^-60 where that is less), a product of pieces that is left out
  * is below 2^-22 of the whole: results are those of single-precision products
  * within a small factor.  S and S S are symmetric; each is computed once.  Sums
  * are taken in an order that is fixed for a call's sizes, so repeated calls give

@@ -22,9 +22,10 @@
  * runtime are as in sgemm.h; pointers must be aligned to their elements
  * (SGEMM_ERR_INVALID_VALUE), offsets to 8 bytes.  Outputs must not overlap inputs.
  * Limits (SGEMM_ERR_TOO_LARGE): sizes and leading dimensions below 2^31, pairs =
- * tokens * topk too, each launch below 2^32 work-items (one wave of 64 for each
- * token in sgemm_route and sgemm_route_backward; 256 for each row and 2048
- * elements of it in the others).
+ * tokens * topk too, each launch below 2^32 work-items (a wave of 64 for each
+ * token in sgemm_route and sgemm_route_backward; for each row that is written and
+ * 4096 bytes of it in sgemm_rows_gather and sgemm_rows_combine, for each pair and
+ * 4096 bytes in sgemm_rows_combine_backward).
  */
 #ifndef SGEMM_ROUTE_H_
 #define SGEMM_ROUTE_H_
@@ -63,12 +64,13 @@ extern "C" {
  * and groups they are those of the logits.  Weights are single precision, off by
  * a few roundings.
  *
- * A logit of -infinity disables an expert: it is never picked, and counts
- * for nothing in its group's score (a group with no other expert comes
+ * A logit or a bias of -infinity disables an expert: it is never picked, and
+ * counts for nothing in its group's score (a group with no other expert comes
  * last).  Where fewer than topk experts can be picked, the last picks are -1
  * with weight 0; without any all are.  Picked scores that sum to 0 (by
  * underflow) renormalise to 0.  A row with a NaN, and under softmax one with a
- * +infinity, gets NaN weights; its picks are some distinct experts or -1.
+ * +infinity, gets NaN weights; its picks are some distinct experts or -1, as are
+ * those of all rows where a bias is NaN.
  *
  * 1 <= topk <= min(experts, SGEMM_ROUTE_MAX_TOPK), 1 <= experts, groups a divisor
  * of experts, 1 <= topk_groups <= groups, group_top 1 or 2

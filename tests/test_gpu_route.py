@@ -356,3 +356,50 @@ def test_rows_past_4_gib():
     assert torch.equal(Y[:3], X[at.long()])
     sg.sgemm_rows_combine_backward(3, 1, rows, N, "bf16", None, 0, X, ld, at, None, Y, ld, None)
     assert torch.equal(Y[at.long()], X[:3]) and (Y[6] == 3).all()
+
+
+def test_a_row_of_the_largest_length():
+    """2^31 - 1 columns: the last piece ends one element before the index would overflow.  Sums
+    of small whole numbers are exact."""
+    import torch
+    N = (1 << 31) - 1
+    X = torch.zeros(N, dtype=torch.bfloat16, device="cuda")
+    X[0], X[N - 1025], X[N - 1] = 3, 5, 7
+    Y = torch.full((N + 8,), 2.0, dtype=torch.bfloat16, device="cuda")
+    at = torch.zeros(1, dtype=torch.int32, device="cuda")
+    sg.sgemm_rows_gather(1, 1, 1, N, "bf16", X, N, at, None, Y, N)
+    assert torch.equal(Y[:N], X) and (Y[N:] == 2).all()
+    Y.fill_(2)
+    sg.sgemm_rows_combine(1, 1, 1, N, "bf16", X, N, at, None, Y, N)
+    assert torch.equal(Y[:N], X) and (Y[N:] == 2).all()
+    Y.fill_(2)
+    dw = torch.full((1,), 9.0, device="cuda")
+    sg.sgemm_rows_combine_backward(1, 1, 1, N, "bf16", X, N, X, N, at, None, Y, N, dw)
+    assert torch.equal(Y[:N], X) and (Y[N:] == 2).all() and dw.item() == 9 + 25 + 49
+
+
+@pytest.mark.parametrize("scale", [np.inf, -np.inf, np.nan])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_scales_that_are_not_finite_leave_missing_picks_at_0(score, scale):
+    import torch
+    l = np.full((2, 8), -np.inf, np.float32)
+    l[0, :2] = 1, 2
+    picks, weights = torch.empty(2, 4, dtype=torch.int32, device="cuda"), torch.empty(
+        2, 4, device="cuda")
+    sg.sgemm_route(2, 8, 4, score, "f32", _cuda(l), 8, None, 1, 1, 1, True, scale, picks, weights)
+    weights = weights.cpu().numpy()
+    assert picks.cpu().numpy().tolist() == [[1, 0, -1, -1], [-1] * 4]
+    assert not weights[0, 2:].any() and not weights[1].any()
+    assert np.array_equal(weights[0, :2], np.full(2, scale, np.float32), equal_nan=True)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups,keep", [(1, 1), (4, 2)])
+def test_bias_of_infinity(score, groups, keep):
+    """-infinity: never picked, like a disabled logit; +infinity: picked first."""
+    l = _logits(8, 40, 32)
+    b = (np.random.default_rng(9).standard_normal(32) * 0.1).astype(np.float32)
+    b[[3, 17]], b[[9, 30]] = -np.inf, np.inf
+    picks, _ = _route(l, 6, "f32", score, b, groups, keep, 1)
+    assert not np.isin(picks, [3, 17]).any()
+    assert (picks[:, :2] == [9, 30]).all()
