@@ -4,7 +4,7 @@
                     [--variant V] [--no-cpu-baseline] [--no-secondary]
     python bench.py --table | --general | --small | --shards | --ladder
                     | --vector-add | --bf16x3 | --bf16x3-general | --experts
-                    | --copy-calibration
+                    | --more-operators | --copy-calibration
 
 One step is one call of sgemm_run on the 8192^3 workload (uniform[-1, 1)
 inputs from seed 4, already resident in HBM).  W untimed calls, then exactly
@@ -19,8 +19,9 @@ products with sgemm_run's tile and every forced tile (--small), one
 GPU's share of 8192^3 split by rows over 1-8 GPUs (--shards), the pages'
 progression (--ladder), the vector add (--vector-add), the bfloat16 split
 path (--bf16x3, --bf16x3-general), products of grouped rows and of 4-bit
-operands (--experts), and the copy that calibrates the HBM counters
-(--copy-calibration).
+operands (--experts), routing, rows to experts and back, 8-bit products and
+orthogonalised updates (--more-operators), and the copy that calibrates the
+HBM counters (--copy-calibration).
 
 The CPU baseline is the oracle (double-precision triple loop) timed on the
 host cores on a bounded sample of the same workload: the first R rows of C,
@@ -463,12 +464,11 @@ def general_table(settle: float) -> list[dict]:
     return rows
 
 
-def operators():
-    """perf/operators.py as a module."""
+def operators(name: str = "operators"):
+    """perf/operators.py, or another file there, as a module."""
     import importlib.util
 
-    spec = importlib.util.spec_from_file_location("operators",
-                                                  os.path.join(ROOT, "perf", "operators.py"))
+    spec = importlib.util.spec_from_file_location(name, os.path.join(ROOT, "perf", name + ".py"))
     ops = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(ops)
     return ops
@@ -480,19 +480,27 @@ def operand_sets(nbytes: int) -> int:
     return max(2, int(8e8 / nbytes) + 1)
 
 
-def experts_table(settle: float) -> list[dict]:
+# Sets of operands, at most: the calls whose operands are so small that more
+# would be needed are held by their launches, not by memory.
+MOST_SETS = 256
+
+
+def experts_table(settle: float, name: str = "operators") -> list[dict]:
     """Time the calls of perf/operators.py's cases (products of grouped rows,
-    casts to 4-bit floats and products of them), one JSON line each.  Several
-    sets of operands are used in turn, more of them than the caches hold."""
+    casts to 4-bit floats and products of them), or of more_operators.py's
+    (routing, rows moved, 8-bit products, orthogonalised updates), one JSON
+    line each.  Several sets of operands are used in turn, more of them than
+    the caches hold."""
     import torch
 
-    ops = operators()
+    ops = operators(name)
     ops.own = True
     rows = []
     stream = torch.cuda.current_stream()
     for case in ops.listed():
         need = ops.work(case)
-        sets = [ops.prepare(case, i) for i in range(operand_sets(need["bytes"]))]
+        sets = [ops.prepare(case, i)
+                for i in range(min(MOST_SETS, operand_sets(need["bytes"])))]
         for st in sets:
             ops.run(st)
         torch.cuda.synchronize()
@@ -984,6 +992,10 @@ def main(argv=None) -> int:
     ap.add_argument("--experts", action="store_true",
                     help="time products of grouped rows, casts to 4-bit floats and products of "
                          "them on the cases of perf/operators.py, one JSON line each")
+    ap.add_argument("--more-operators", action="store_true",
+                    help="time routing, rows to experts and back, 8-bit products and "
+                         "orthogonalised updates on the cases of perf/more_operators.py, one "
+                         "JSON line each")
     ap.add_argument("--kscan", action="store_true",
                     help="time sgemm_run at M = N = 256 and 1024 over K = 32 .. 4096, two "
                          "floor cases and the five workloads, one JSON line each (with the "
@@ -1050,8 +1062,8 @@ def main(argv=None) -> int:
         bf16x3_table(a.steps, a.warmup, a.settle, general=a.bf16x3_general)
         sg.sgemm_destroy()
         return 0
-    if a.experts:
-        experts_table(a.settle)
+    if a.experts or a.more_operators:
+        experts_table(a.settle, "more_operators" if a.more_operators else "operators")
         sg.sgemm_destroy()
         return 0
     if a.vector_add:

@@ -236,6 +236,11 @@ def _typed(x, name, dtype, size=0):
     if want is None:
         import torch
         want = _dtypes[dtype] = getattr(torch, dtype)
+    try:  # all at once: 0.2 us where the checks below take 0.4
+        if x.dtype is want and x.is_cuda and x.numel() >= size and x.is_contiguous():
+            return x.data_ptr()
+    except AttributeError:
+        pass
     if getattr(x, "dtype", want) is not want:
         raise TypeError(f"{name} must be {dtype}")
     if hasattr(x, "numel"):
