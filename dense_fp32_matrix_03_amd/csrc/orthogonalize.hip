@@ -13,8 +13,8 @@
 // diagonal are computed, and written to both sides.
 #include <math.h>
 
-#include "mxfp4.hpp"
 #include "orthogonalize.hpp"
+#include "piece.hpp"
 #include "slice_tile.hpp"
 
 namespace sgemm {
@@ -72,22 +72,39 @@ __device__ __forceinline__ double group_sum(double v) {  // of 256 threads
 }
 
 // Part blockIdx.x of matrix blockIdx.y: a wave has every 4 n_parts-th run of 512
-// elements of a row.
+// elements of a row, and loads four of them together.
 template <bool BF16>
 __global__ void __launch_bounds__(256) ortho_norm_kernel(OrthoNormArgs p) {
+  using P = Piece<BF16>;
+  constexpr int kTogether = 4, kPieces = kNormRun / (kWave * P::V);
   const long base = (long)blockIdx.y * p.strideX;
   const int runs = (p.N + kNormRun - 1) / kNormRun;
   const int lane = threadIdx.x % kWave;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const long step = 4 * p.n_parts, all = (long)p.M * runs;
   double sum = 0;
-  for (long u = blockIdx.x * 4 + wave; u < (long)p.M * runs; u += 4 * p.n_parts) {
-    const long row = u / runs;
-    const int n = (int)(u - row * runs) * kNormRun + lane * 8;
-    float v[8];
-    load8<BF16>(static_cast<const char *>(p.X) + (base + row * p.ldx + n) * (BF16 ? 2 : 4),
-                p.N - n, v);
+  for (long u0 = blockIdx.x * 4 + wave; u0 < all; u0 += kTogether * step) {
+    P x[kTogether][kPieces];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sum += (double)v[e] * (double)v[e];
+    for (int i = 0; i < kTogether; ++i) {
+      const long u = u0 + i * step, row = u < all ? u / runs : 0;
+      const int n0 = u < all ? (int)(u - row * runs) * kNormRun : p.N;
+      const bool whole = p.N - n0 >= kNormRun;
+#pragma unroll
+      for (int k = 0; k < kPieces; ++k) {
+        const int n = n0 + (k * kWave + lane) * P::V;
+        x[i][k].load(p.X, base + row * p.ldx + n, p.N - n, whole);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kTogether; ++i)
+#pragma unroll
+      for (int k = 0; k < kPieces; ++k) {
+        float v[P::V];
+        x[i][k].get(v);
+#pragma unroll
+        for (int e = 0; e < P::V; ++e) sum += (double)v[e] * (double)v[e];
+      }
   }
   sum = group_sum(sum);
   if (threadIdx.x == 0) p.parts[(long)blockIdx.y * p.n_parts + blockIdx.x] = sum;
@@ -155,18 +172,21 @@ __global__ void __launch_bounds__(256) ortho_split_kernel(OrthoSplitArgs p, Fast
   const int block = blockIdx.x * 4 + wave, row = by_across(block);
   const int bm = row * 32, bn = (block - row * ((x.N + 31) / 32)) * 32;
   const int r32 = lane % 32, half = lane / 32;
+  // Every lane loads, from the nearest element there is, so that the loads go out
+  // together; what lies past the matrix is then dropped.
   float v[16];
+  const int n = bn + r32;
 #pragma unroll
   for (int e = 0; e < 16; ++e) {
-    const int m = bm + acc32_row(lane, e), n = bn + r32;
-    v[e] = m < x.M && n < x.N
-               ? load1<BF16>(x.X, (long)blockIdx.y * x.strideX + m * x.ldx + n) : 0.f;
+    const int m = min(bm + acc32_row(lane, e), x.M - 1);
+    v[e] = load1<BF16>(x.X, (long)blockIdx.y * x.strideX + m * x.ldx + min(n, x.N - 1));
   }
   const double norm = sqrt(group_sum(part)) + (double)p.eps;
   const double scale = norm > 0 ? ldexp(1.0, p.shift) / norm : norm;  // NaN stays
   if (bm >= x.M) return;  // whole waves: no barrier follows
 #pragma unroll
-  for (int e = 0; e < 16; ++e) v[e] = (float)(scale * (double)v[e]);
+  for (int e = 0; e < 16; ++e)
+    v[e] = bm + acc32_row(lane, e) < x.M && n < x.N ? (float)(scale * (double)v[e]) : 0.f;
   __shared__ __attribute__((aligned(16))) char images[4][2][4096];
   const BlockImage rows{images[wave][0]}, cols{images[wave][1]};
   split_block(v, r32, half, rows, cols, true);
@@ -212,18 +232,23 @@ ortho_product_kernel(OrthoProductArgs p, TileMap map, FastDiv by_triangle, int t
   // Blocks of E^T go out before the sums' operands; rows past N are zeros, and a row's
   // columns up to the next 32 are there.
   slice_i32x4 e_t[FM][FN][4];
+  auto load_e = [&](bool whole) {
 #pragma unroll
-  for (int i = 0; i < FM; ++i)
+    for (int i = 0; i < FM; ++i)
 #pragma unroll
-    for (int j = 0; j < FN; ++j)
+      for (int j = 0; j < FN; ++j)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int n = nw + j * 32 + 8 * k + lane / 8, m = mw + i * 32;
-        e_t[i][j][k] = slice_i32x4{0, 0, 0, 0};
-        if (p.e_t.at && n < N && m < M)
-          e_t[i][j][k] =
-              *reinterpret_cast<const slice_i32x4 *>(p.e_t.place(batch, n, m) + lane % 8 * 16);
-      }
+        for (int k = 0; k < 4; ++k) {
+          const int n = nw + j * 32 + 8 * k + lane / 8, m = mw + i * 32;
+          const auto *at =
+              reinterpret_cast<const slice_i32x4 *>(p.e_t.place(batch, n, m) + lane % 8 * 16);
+          if (whole)
+            e_t[i][j][k] = *at;
+          else
+            e_t[i][j][k] = n < N && m < M ? *at : slice_i32x4{0, 0, 0, 0};
+        }
+  };
+  if (p.e_t.at) load_e(mw + 32 * FM <= M && nw + 32 * FN <= N);
 
   auto rows = [&](const SplitMatrix &x, int first, int n) {
     return SliceRows{x.place(batch, first, 0), kSliceRow, (long)x.rows * kSliceRow, n};

@@ -30,6 +30,18 @@ __device__ __forceinline__ float load1(const void *x, long at) {
     return static_cast<const float *>(x)[at];
 }
 
+// A wave's n values, the rest -infinity.  Every lane loads, from the nearest element
+// there is: behind a test of its own each 2-byte load would be waited for before the
+// next one goes out.
+template <bool BF16, int EPL>
+__device__ __forceinline__ void load_row(const void *x, long at, int n, float v[EPL]) {
+  const int lane = threadIdx.x % kWave;
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) v[i] = load1<BF16>(x, at + min(i * kWave + lane, n - 1));
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) v[i] = i * kWave + lane < n ? v[i] : -__builtin_inff();
+}
+
 // op over the lanes by moves inside rows of 16 and from row to row; the result in
 // every lane.  A lane without a neighbour there combines with `rest`.
 template <class Op>
@@ -247,16 +259,10 @@ __global__ void __launch_bounds__(kTokens *kWave) route_kernel(RouteArgs p) {
   float *const row = reinterpret_cast<float *>(room[wave]);  // logits, or what is compared
 
   float l[EPL], bias[EPL];
+  load_row<BF16, EPL>(p.logits, t * p.ldl, p.experts, l);
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    const int e = i * kWave + lane;
-    l[i] = e < p.experts ? load1<BF16>(p.logits, t * p.ldl + e) : kMinusInf;
-  }
-#pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    const int e = i * kWave + lane;
-    bias[i] = p.bias && e < p.experts ? p.bias[e] : 0.f;
-  }
+  for (int i = 0; i < EPL; ++i) bias[i] = 0.f;
+  if (p.bias) load_row<false, EPL>(p.bias, 0, p.experts, bias);
   const bool by_logits = !p.bias && p.groups == 1;
   float top = l[0];
   bool odd = false;  // the row has a NaN, or softmax of an infinity
@@ -448,12 +454,9 @@ __global__ void __launch_bounds__(kTokens *kWave) route_backward_kernel(RouteBac
   wave_fence();
   if (whole) {
     float top = kMinusInf;
+    load_row<BF16, EPL>(p.logits, t * p.ldl, p.experts, s);
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      const int e = i * kWave + lane;
-      s[i] = e < p.experts ? load1<BF16>(p.logits, t * p.ldl + e) : kMinusInf;
-      top = fmaxf(top, s[i]);
-    }
+    for (int i = 0; i < EPL; ++i) top = fmaxf(top, s[i]);
     top = wave_max(top);
     if (top == kMinusInf) top = 0.f;
     float total = 0.f;
