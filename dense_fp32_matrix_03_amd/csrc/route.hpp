@@ -46,11 +46,13 @@ struct PlanArgs {
   int32_t *sources, *places;
   int *counts;  // [chunks][groups], in the workspace
 };
-constexpr int kPlanChunk = 4096;   // pairs of a chunk, at least
-constexpr int kPlanChunks = 256;   // chunks, at most
-inline int plan_chunk(long pairs) {
+constexpr int kPlanChunk = 2048;  // pairs of a chunk, at least where there are several
+constexpr int kPlanChunks = 256;  // chunks, at most
+inline int plan_chunk(long pairs) {  // a multiple of 256
   const long share = (pairs + kPlanChunks - 1) / kPlanChunks;
-  return (int)(share > kPlanChunk ? (share + 255) / 256 * 256 : kPlanChunk);
+  const long least = pairs < kPlanChunk ? pairs : kPlanChunk;
+  const long chunk = share > least ? share : least;
+  return (int)((chunk < 1 ? 1 : chunk) + 255) / 256 * 256;
 }
 inline int plan_chunks(long pairs) { return (int)((pairs + plan_chunk(pairs) - 1) / plan_chunk(pairs)); }
 hipError_t launch_route_plan(const PlanArgs &p, hipStream_t s);

@@ -9,6 +9,13 @@
 // and the number of lanes before it with the same group, which ballots over the
 // bits of the group's number give.  Nothing depends on the order of atomics:
 // they only count.
+//
+// Held by trips to memory, one after the other: picks, counts, places; 12 bytes a pair
+// would take 0.2 us for 65536 pairs.  So a lane loads up to 8 picks, and 16 chunks'
+// counts, together.  By graph replay: 48 pairs of 16 groups 3.1 us; 65536 of 128 groups
+// 10.7 us (23.5 with one load at a time and chunks of 4096 pairs, 15.0 with 16 picks
+// together and those chunks, but then 4.3 for 48 pairs, whose code is longer); 131072 of
+// 1024 groups 22 us, 16384 of 4096 groups 27 us.
 #include "route.hpp"
 
 namespace sgemm {
@@ -17,74 +24,107 @@ namespace {
 
 constexpr int kThreads = 256, kWaves = kThreads / kWave;
 
-// The group of a pair, or -1.
-__device__ __forceinline__ int group_of(const PlanArgs &p, int pair) {
-  const long g = (long)p.picks[pair] - p.first;
-  return g >= 0 && g < p.groups ? (int)g : -1;
+// The groups of pairs at + i * step + lane below `end` for i < H, or -1.  `at` and `end`
+// are the same for a wave.
+template <int H>
+__device__ __forceinline__ void load_groups(const PlanArgs &p, long at, int step, long end,
+                                            int g[H]) {
+  const int lane = threadIdx.x % kWave;
+  int pick[H];
+#pragma unroll
+  for (int i = 0; i < H; ++i) {
+    pick[i] = 0;
+    if (at + i * step < end) pick[i] = p.picks[min(at + i * step + lane, end - 1)];
+  }
+#pragma unroll
+  for (int i = 0; i < H; ++i) {
+    const long own = (long)pick[i] - p.first;
+    g[i] = at + i * step + lane < end && own >= 0 && own < p.groups ? (int)own : -1;
+  }
 }
 
-// G: groups that there is room for.
-template <int G>
+// G: groups that there is room for.  H: pairs of a lane whose picks are loaded together.
+template <int G, int H>
 __global__ void __launch_bounds__(kThreads) plan_count_kernel(PlanArgs p) {
   __shared__ int count[G];
   for (int g = threadIdx.x; g < p.groups; g += kThreads) count[g] = 0;
   __syncthreads();
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const long begin = (long)blockIdx.x * p.chunk, end = min(begin + p.chunk, (long)p.pairs);
-  for (long i = begin + threadIdx.x; i < end; i += kThreads) {
-    const int g = group_of(p, (int)i);
-    if (g >= 0) atomicAdd(&count[g], 1);
+  for (long at = begin + wave * kWave; at < end; at += kThreads * H) {
+    int g[H];
+    load_groups<H>(p, at, kThreads, end, g);
+#pragma unroll
+    for (int i = 0; i < H; ++i)
+      if (g[i] >= 0) atomicAdd(&count[g[i]], 1);
   }
   __syncthreads();
   for (int g = threadIdx.x; g < p.groups; g += kThreads)
     p.counts[(long)blockIdx.x * p.groups + g] = count[g];
 }
 
-template <int G>
+template <int G, int H>
 __global__ void __launch_bounds__(kThreads) plan_place_kernel(PlanArgs p) {
   __shared__ int next[kWaves * G];  // [waves][groups]: counts, then the next places
   __shared__ int base[G];           // totals, then the groups' first rows
   __shared__ int part[kThreads];
-  const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
+  const int tid = threadIdx.x, lane = tid % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int c = blockIdx.x;
   const long begin = (long)c * p.chunk, end = min(begin + p.chunk, (long)p.pairs);
-  const long quarter = p.chunk / kWaves;
+  const int quarter = p.chunk / kWaves;
   const long from = min(begin + wave * quarter, end), to = min(from + quarter, end);
+  constexpr int kStep = kWave * H;
 
+  int held[H];
+  load_groups<H>(p, from, kWave, to, held);
   for (int i = tid; i < kWaves * p.groups; i += kThreads) next[i] = 0;
   __syncthreads();
-  for (long i = from + lane; i < to; i += kWave) {
-    const int g = group_of(p, (int)i);
-    if (g >= 0) atomicAdd(&next[wave * p.groups + g], 1);
+  for (long at = from;;) {
+#pragma unroll
+    for (int i = 0; i < H; ++i)
+      if (held[i] >= 0) atomicAdd(&next[wave * p.groups + held[i]], 1);
+    at += kStep;
+    if (at >= to) break;
+    load_groups<H>(p, at, kWave, to, held);
   }
   __syncthreads();
 
-  // Each thread has `per` consecutive groups: their totals over all chunks, and a
-  // scan over the threads for the rows before them.
-  const int per = (p.groups + kThreads - 1) / kThreads;
-  int mine = 0;
-  for (int i = 0; i < per; ++i) {
-    const int g = tid * per + i;
-    if (g >= p.groups) break;
+  // Each group's total over all chunks, and where this chunk's waves place theirs, so
+  // far from the group's first row.
+  for (int g = tid; g < p.groups; g += kThreads) {
     int total = 0, before = 0;
     if (p.chunks > 1) {
-      for (int k = 0; k < p.chunks; ++k) {
-        const int n = p.counts[(long)k * p.groups + g];
-        before += k < c ? n : 0;
-        total += n;
+      constexpr int kTogether = 16;
+      for (int k = 0; k < p.chunks; k += kTogether) {
+        int n[kTogether];
+#pragma unroll
+        for (int j = 0; j < kTogether; ++j)
+          n[j] = p.counts[(long)min(k + j, p.chunks - 1) * p.groups + g];
+#pragma unroll
+        for (int j = 0; j < kTogether; ++j) {
+          before += k + j < c ? n[j] : 0;
+          total += k + j < p.chunks ? n[j] : 0;
+        }
       }
-    } else {
-      for (int w = 0; w < kWaves; ++w) total += next[w * p.groups + g];
     }
-    base[g] = total;
-    // The places in this chunk, so far from the group's first row.
     int at = before;
+#pragma unroll
     for (int w = 0; w < kWaves; ++w) {
       const int n = next[w * p.groups + g];
       next[w * p.groups + g] = at;
       at += n;
     }
-    mine += total;
+    base[g] = p.chunks > 1 ? total : at;
   }
+  __syncthreads();
+
+  // The groups' first rows: each thread has `per` consecutive groups, and a scan over
+  // the threads gives the rows before them.
+  const int per = (p.groups + kThreads - 1) / kThreads;
+  int mine = 0;
+  for (int i = 0; i < per; ++i)
+    if (tid * per + i < p.groups) mine += base[tid * per + i];
   part[tid] = mine;
   __syncthreads();
   for (int d = 1; d < kThreads; d *= 2) {
@@ -107,50 +147,58 @@ __global__ void __launch_bounds__(kThreads) plan_place_kernel(PlanArgs p) {
   __syncthreads();
 
   const int bits = p.groups > 1 ? 32 - __builtin_clz(p.groups - 1) : 0;
-  for (long i0 = from; i0 < to; i0 += kWave) {
-    const long i = i0 + lane;
-    const int g = i < to ? group_of(p, (int)i) : -1;
-    unsigned long long same = __ballot(g >= 0);
-    for (int b = 0; b < bits; ++b) {
-      const bool bit = g >> b & 1;
-      const unsigned long long ones = __ballot(bit);
-      same &= bit ? ones : ~ones;
-    }
-    if (g >= 0) {
-      const int before = __builtin_amdgcn_mbcnt_hi((unsigned)(same >> 32),
-                                                   __builtin_amdgcn_mbcnt_lo((unsigned)same, 0));
-      const int at = next[wave * p.groups + g];
-      const int place = base[g] + at + before;
-      p.places[i] = place;
-      p.sources[place] = (int)i;
-      // Every lane of the group has read the count by now; its last one moves it on.
+  for (long at = from; at < to; at += kStep) {
+    if (to - from > kStep) load_groups<H>(p, at, kWave, to, held);
+#pragma unroll
+    for (int k = 0; k < H; ++k) {
+      if (at + k * kWave >= to) break;
+      const long i = at + k * kWave + lane;
+      const int g = held[k];
+      unsigned long long same = __ballot(g >= 0);
+      for (int b = 0; b < bits; ++b) {
+        const bool bit = g >> b & 1;
+        const unsigned long long ones = __ballot(bit);
+        same &= bit ? ones : ~ones;
+      }
+      if (g >= 0) {
+        const int before = __builtin_amdgcn_mbcnt_hi((unsigned)(same >> 32),
+                                                     __builtin_amdgcn_mbcnt_lo((unsigned)same, 0));
+        const int at_g = next[wave * p.groups + g];
+        const int place = base[g] + at_g + before;
+        p.places[i] = place;
+        p.sources[place] = (int)i;
+        // Every lane of the group has read the count by now; its last one moves it on.
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        if (before == __builtin_popcountll(same) - 1)
+          next[wave * p.groups + g] = at_g + before + 1;
+      } else if (i < to) {
+        p.places[i] = -1;
+      }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      if (before == __builtin_popcountll(same) - 1) next[wave * p.groups + g] = at + before + 1;
-    } else if (i < to) {
-      p.places[i] = -1;
     }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   }
   for (long r = begin + tid; r < end; r += kThreads)
     if (r >= all) p.sources[r] = -1;
 }
 
-template <int G>
+template <int G, int H>
 hipError_t launch(const PlanArgs &p, hipStream_t s) {
   const dim3 grid((unsigned)p.chunks), block(kThreads);
   if (p.chunks > 1) {
-    hipLaunchKernelGGL(plan_count_kernel<G>, grid, block, 0, s, p);
+    hipLaunchKernelGGL((plan_count_kernel<G, H>), grid, block, 0, s, p);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
   }
-  hipLaunchKernelGGL(plan_place_kernel<G>, grid, block, 0, s, p);
+  hipLaunchKernelGGL((plan_place_kernel<G, H>), grid, block, 0, s, p);
   return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_route_plan(const PlanArgs &p, hipStream_t s) {
-  return p.groups <= 512 ? launch<512>(p, s) : launch<4096>(p, s);
+  if (p.groups > 512) return launch<4096, 8>(p, s);
+  // A chunk of 256 pairs is one load a lane.
+  return p.chunk <= kThreads ? launch<512, 1>(p, s) : launch<512, 8>(p, s);
 }
 
 }  // namespace sgemm

@@ -403,3 +403,22 @@ def test_bias_of_infinity(score, groups, keep):
     picks, _ = _route(l, 6, "f32", score, b, groups, keep, 1)
     assert not np.isin(picks, [3, 17]).any()
     assert (picks[:, :2] == [9, 30]).all()
+
+
+@pytest.mark.parametrize("pairs,groups", [(2048, 30), (2049, 30), (524288, 7), (700001, 100),
+                                          (700001, 4000)])
+def test_plan_of_many_pairs(pairs, groups):
+    """One chunk and two; all chunks in one step each, and in several."""
+    import torch
+    picks = np.random.default_rng(pairs).integers(-1, groups + 2, pairs).astype(np.int32)
+    need = sg.sgemm_route_plan_workspace_size(pairs, groups)
+    ws = torch.full((need + 16,), 0xFF, dtype=torch.uint8, device="cuda")
+    off = torch.full((groups + 2,), -5, dtype=torch.int64, device="cuda")
+    sources, places = (torch.full((pairs + 1,), -5, dtype=torch.int32, device="cuda")
+                       for _ in range(2))
+    sg.sgemm_route_plan(pairs, 0, groups, _cuda(picks), off, sources, places, ws, need)
+    torch.cuda.synchronize()
+    for got, want, rest in zip((off, sources, places), rm.plan(picks, 0, groups), (-5, -5, -5)):
+        got = got.cpu().numpy()
+        assert np.array_equal(got[:-1], want) and got[-1] == rest
+    assert (ws[need:] == 0xFF).all()

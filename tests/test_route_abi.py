@@ -66,9 +66,9 @@ PLAN = dict(pairs=10000, first=0, groups=8, picks=16, offsets=16, sources=16, pl
     (dict(pairs=2 ** 31), LARGE), (dict(groups=4097), LARGE), (dict(first=2 ** 31), LARGE),
     (dict(picks=None), INVALID), (dict(offsets=None), INVALID), (dict(offsets=12), INVALID),
     (dict(sources=None), INVALID), (dict(places=18), INVALID), (dict(workspace=None), INVALID),
-    (dict(workspace=24), INVALID), (dict(workspace_bytes=8 * 4 * 3 - 1), INVALID),
-    (dict(workspace_bytes=8 * 4 * 3), READY),
-    (dict(pairs=4096, workspace=None, workspace_bytes=0), READY),
+    (dict(workspace=24), INVALID), (dict(workspace_bytes=8 * 4 * 5 - 1), INVALID),
+    (dict(workspace_bytes=8 * 4 * 5), READY),
+    (dict(pairs=2048, workspace=None, workspace_bytes=0), READY),
     (dict(pairs=0, picks=None, sources=None, places=None, workspace=None), READY),
 ])
 def test_plan_checks(over, status):
@@ -76,8 +76,8 @@ def test_plan_checks(over, status):
 
 
 def test_plan_workspace():
-    assert sg.sgemm_route_plan_workspace_size(4096, 8) == 0
-    assert sg.sgemm_route_plan_workspace_size(4097, 8) == 2 * 8 * 4
+    assert sg.sgemm_route_plan_workspace_size(2048, 8) == 0
+    assert sg.sgemm_route_plan_workspace_size(2049, 8) == 2 * 8 * 4
     assert sg.sgemm_route_plan_workspace_size(2 ** 31 - 1, 4096) <= 256 * 4096 * 4
     with pytest.raises(sg.SgemmError):
         sg.sgemm_route_plan_workspace_size(5, 4097)
