@@ -17,6 +17,10 @@
 // while its first codes of B are on their way, the work-group's waves exchange
 // them, and then each casts the k that it multiplies, 4 values a lane; the codes
 // pass through LDS to the lanes that multiply them.
+//
+// 1 x 8192 x 2048 from bfloat16: 6.1 us by graph replay, of which reading B takes 3.4 at a
+// large copy's rate; the rest is the launch, and x, its largest magnitude and the codes
+// one after the other.
 #include "grouped_map.hpp"
 #include "int8.hpp"
 #include "mfma_dma.hpp"

@@ -184,11 +184,12 @@ __global__ void __launch_bounds__(kThreads) plan_place_kernel(PlanArgs p) {
 template <int G, int H>
 hipError_t launch(const PlanArgs &p, hipStream_t s) {
   const dim3 grid((unsigned)p.chunks), block(kThreads);
-  if (p.chunks > 1) {
-    hipLaunchKernelGGL((plan_count_kernel<G, H>), grid, block, 0, s, p);
-    const hipError_t err = hipGetLastError();
-    if (err != hipSuccess) return err;
-  }
+  if constexpr (H > 1)  // one load a lane: one chunk
+    if (p.chunks > 1) {
+      hipLaunchKernelGGL((plan_count_kernel<G, H>), grid, block, 0, s, p);
+      const hipError_t err = hipGetLastError();
+      if (err != hipSuccess) return err;
+    }
   hipLaunchKernelGGL((plan_place_kernel<G, H>), grid, block, 0, s, p);
   return hipGetLastError();
 }
