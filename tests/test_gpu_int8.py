@@ -308,3 +308,9 @@ def test_other_stream_and_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(C[lo:hi], want[lo:hi]) and torch.equal(C2, want2)
+
+
+@pytest.mark.parametrize("M,N,K", [(1 << 19, 5, 33), (3, 1 << 18, 40), (200003, 17, 130)])
+@pytest.mark.parametrize("kind", ["bf16", "int8"])
+def test_very_many_rows_or_columns(M, N, K, kind):
+    _product(M, N, K, kind, "f32", pads=(3, 0, 1))

@@ -167,3 +167,26 @@ def test_in_a_graph_and_on_another_stream():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(Y, want)
+
+
+@pytest.mark.parametrize("shape", [(1, 1, 1 << 20), (1, 1 << 20, 2), (1, 3, 300001)])
+def test_longest_rows(shape):
+    y, held = _run(_values(11, shape))
+    _check(y, held)
+
+
+def test_largest_batch():
+    shape = (65535, 2, 3)
+    y, held = _run(_values(12, shape))
+    some = np.r_[0:20, 32760:32780, 65515:65535]
+    _check(y[some], held[some])
+    # All: values stay below 1.3 and a step's slope below 3.5.  A step adds the errors of three
+    # products, each off by 3 2^-22 of its terms (S's and P's by |b| + 2 |c| |S| + |c| |S|^2 < 13
+    # of it on the way to Z), below 40 2^-22; five steps' are at most 3.5^5 / 2.5 times that.
+    z = held.astype(np.float64)
+    z /= np.sqrt((z * z).sum((1, 2), keepdims=True)) + float(np.float32(1e-7))
+    a, b, c = (float(np.float32(v)) for v in om.STEP)
+    for _ in range(5):
+        s = z @ z.transpose(0, 2, 1)
+        z = a * z + (b * s + c * s @ s) @ z
+    assert np.abs(y - z).max() <= 40 * 3.5 ** 5 * 2.0 ** -22

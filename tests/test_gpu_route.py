@@ -422,3 +422,27 @@ def test_plan_of_many_pairs(pairs, groups):
         got = got.cpu().numpy()
         assert np.array_equal(got[:-1], want) and got[-1] == rest
     assert (ws[need:] == 0xFF).all()
+
+
+def test_a_million_tokens():
+    """Distinct logits, so that the picks are those of a sort."""
+    import torch
+    tokens, experts, topk = (1 << 20) + 3, 9, 2
+    l = torch.rand(tokens, experts, device="cuda").argsort(1).float()
+    picks = torch.empty(tokens, topk, dtype=torch.int32, device="cuda")
+    weights = torch.empty(tokens, topk, device="cuda")
+    sg.sgemm_route(tokens, experts, topk, "softmax", "f32", l, experts, None, 1, 1, 1, True, 1.0,
+                   picks, weights)
+    best, at = l.topk(topk, 1)
+    assert torch.equal(picks.long(), at)
+    want = best.double().softmax(1)
+    assert ((weights - want).abs() <= (2 * 16 + 40) * U * want).all()
+    dw = torch.randn(tokens, topk, device="cuda")
+    dl = torch.full((tokens, experts), 5.0, device="cuda")
+    sg.sgemm_route_backward(tokens, experts, topk, "softmax", "f32", l, experts, True, 1.0, picks, dw,
+                            dl, experts)
+    d = want * (dw - (dw * want).sum(1, keepdim=True))
+    full = torch.zeros(tokens, experts, dtype=torch.float64, device="cuda").scatter_(1, at, d)
+    mag = want * (dw.abs() + (dw.abs() * want).sum(1, keepdim=True))
+    tol = torch.zeros_like(full).scatter_(1, at, (4 * 16 + 100) * U * mag)
+    assert ((dl - full).abs() <= tol).all()
