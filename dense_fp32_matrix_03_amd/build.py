@@ -42,7 +42,7 @@ SOURCES = ["api.hip", "mfma_kernels.hip", "mfma_layout_nn.hip", "mfma_layout_nn_
            "api_mxfp4.hip", "mxfp4_cast.hip", "mxfp4_gemm.hip", "mxfp4_tile.hip",
            "api_int8.hip", "int8_cast.hip", "int8_rows.hip", "int8_tile.hip",
            "api_route.hip", "route.hip", "route_plan.hip", "rows.hip",
-           "api_orthogonalize.hip", "orthogonalize.hip"]
+           "api_orthogonalize.hip", "orthogonalize.hip", "orthogonalize_short.hip"]
 ARCH = "gfx950"
 BUNDLE_TARGET = f"hipv4-amdgcn-amd-amdhsa--{ARCH}"
 # Packed single-precision ops that the device pass must not emit.

@@ -24,12 +24,16 @@ bool bad_type(int type) { return type != SGEMM_TYPE_F32 && type != SGEMM_TYPE_BF
 unsigned size_of(int type) { return type == SGEMM_TYPE_F32 ? 4 : 2; }
 
 // The workspace: Z, Z transposed twice (a step reads one and writes the other), S
-// and P of every matrix, and the parts of the norms.
+// and P of every matrix, and the parts of the norms.  Short matrices: the parts of the
+// norms, and Z and the parts of S twice.
 struct Layout {
   int m, n;
   int64_t z, zt, s;     // bytes of a matrix
   int64_t parts;        // of a norm
   int64_t total;
+  // Where m is short: Z and S's parts, twice each.
+  bool is_short;
+  int64_t short_z, short_parts;
   Layout(int64_t batch, int64_t M, int64_t N) {
     m = (int)(M < N ? M : N);
     n = (int)(M < N ? N : M);
@@ -38,7 +42,10 @@ struct Layout {
     s = sgemm::split_bytes(m, m);
     parts = tiles(M * tiles(N, sgemm::kNormRun), 16);
     if (parts > sgemm::kNormParts) parts = sgemm::kNormParts;
-    total = batch * (z + 2 * zt + 2 * s + 8 * parts);
+    is_short = m <= sgemm::kShort;
+    short_z = 4 * (int64_t)m * n;
+    short_parts = 4 * (int64_t)m * m * sgemm::short_slabs(n);
+    total = batch * (8 * parts + (is_short ? 2 * (short_z + short_parts) : z + 2 * zt + 2 * s));
   }
 };
 
@@ -76,6 +83,57 @@ int shift_for(double bound) {
   int e;
   frexp(fmax(bound * 1.02, ldexp(1.0, -60)), &e);  // below 2^e
   return 15 - e;
+}
+
+// The launches for a short matrix.
+int short_steps(const Layout &l, int64_t batch, int64_t M, int64_t N, int64_t steps, int64_t sets,
+                const float *coefficients, float eps, float alpha, int typeX, const void *X,
+                int64_t ldx, int64_t strideX, int typeY, void *Y, int64_t ldy, int64_t strideY,
+                void *workspace, hipStream_t s) {
+  const bool tall = M > N;
+  char *at = static_cast<char *>(workspace);
+  auto take = [&](int64_t bytes) {
+    char *const from = at;
+    at += batch * bytes;
+    return reinterpret_cast<float *>(from);
+  };
+  sgemm::OrthoShortArgs p{};
+  p.m = l.m;
+  p.n = l.n;
+  p.blocks = sgemm::short_blocks(l.n);
+  p.slabs = sgemm::short_slabs(l.n);
+  p.by_m = sgemm::make_fast_div(l.m);
+  p.X = X;
+  p.xr = tall ? 1 : ldx;
+  p.xc = tall ? ldx : 1;
+  p.strideX = strideX;
+  p.Y = Y;
+  p.yr = tall ? 1 : ldy;
+  p.yc = tall ? ldy : 1;
+  p.strideY = strideY;
+  p.norm = {(int)M, (int)N, X, ldx, strideX, reinterpret_cast<double *>(take(8 * l.parts)),
+            (int)l.parts};
+  p.eps = eps;
+  p.alpha = alpha;
+  float *const z[2] = {take(l.short_z), take(l.short_z)};
+  float *const part[2] = {take(l.short_parts), take(l.short_parts)};
+  p.z_out = z[0];
+  p.part_out = part[0];
+  const bool x_bf16 = typeX == SGEMM_TYPE_BF16, y_bf16 = typeY == SGEMM_TYPE_BF16;
+  hipError_t err = sgemm::launch_ortho_norm(p.norm, x_bf16, (int)batch, s);
+  if (err == hipSuccess) err = sgemm::launch_ortho_short(p, true, false, x_bf16, (int)batch, s);
+  for (int64_t k = 0; k < steps && err == hipSuccess; ++k) {
+    const float *c = coefficients + (sets == 1 ? 0 : 3 * k);
+    p.a = c[0];
+    p.b = c[1];
+    p.c = c[2];
+    p.z_in = z[k % 2];
+    p.part_in = part[k % 2];
+    p.z_out = z[1 - k % 2];
+    p.part_out = part[1 - k % 2];
+    err = sgemm::launch_ortho_short(p, false, k + 1 == steps, y_bf16, (int)batch, s);
+  }
+  return err == hipSuccess ? SGEMM_OK : SGEMM_ERR_LAUNCH;
 }
 
 }  // namespace
@@ -128,6 +186,9 @@ int sgemm_orthogonalize(int64_t batch, int64_t M, int64_t N, int64_t steps, int6
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
 
   const Layout l(batch, M, N);
+  if (l.is_short)
+    return short_steps(l, batch, M, N, steps, sets, coefficients, eps, alpha, typeX, X, ldx,
+                       strideX, typeY, Y, ldy, strideY, workspace, s);
   char *at = static_cast<char *>(workspace);
   auto matrix = [&](int rows, int cols) {
     const sgemm::SplitMatrix x{at, rows, cols, sgemm::split_bytes(rows, cols)};

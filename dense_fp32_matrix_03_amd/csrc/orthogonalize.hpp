@@ -62,4 +62,31 @@ struct OrthoProductArgs {
 hipError_t launch_ortho_product(const OrthoProductArgs &p, bool symmetric, bool y_bf16, int batch,
                                 int cus, hipStream_t s);
 
+// Matrices of at most kShort rows (Z, m x n): a launch for Z and S's parts, then one for
+// each step (orthogonalize_short.hip).  A slab is `blocks` times 64 columns.
+constexpr int kShort = 64;
+// At most 16 slabs, since each work-group adds up all their parts, 32 where a work-group
+// would have many blocks one after the other.  16 / 32 slabs: 32 of 64 x 4096 225 / 315 us,
+// 1 of 32 x 4096 116 / 100, 64 x 100000 1800 / 951.
+inline int short_blocks(int n) {
+  const int slabs = n <= 8192 ? 16 : 32;
+  return ((n + 63) / 64 + slabs - 1) / slabs;
+}
+inline int short_slabs(int n) { return ((n + 63) / 64 + short_blocks(n) - 1) / short_blocks(n); }
+struct OrthoShortArgs {
+  int m, n, slabs, blocks;
+  FastDiv by_m;
+  // Z(r, c) of X at r xr + c xc, of Y at r yr + c yc; one of the two is 1.
+  const void *X;
+  long xr, xc, strideX;
+  void *Y;
+  long yr, yc, strideY;
+  OrthoNormArgs norm;
+  float eps, a, b, c, alpha;
+  const float *z_in, *part_in;  // [batch][m][n]; [batch][slabs][m][m]
+  float *z_out, *part_out;
+};
+hipError_t launch_ortho_short(const OrthoShortArgs &p, bool first, bool last, bool bf16, int batch,
+                              hipStream_t s);
+
 }  // namespace sgemm

@@ -23,7 +23,8 @@
  * precision.  An operand is off by at most 2^-22 of its value + 2^-39 of the
  * largest that the singular values allow (of 2^-60 where that is less), a product of pieces that is left out
  * is below 2^-22 of the whole: results are those of single-precision products
- * within a small factor.  S and S S are symmetric; each is computed once.  Sums
+ * within a small factor.  S and S S are symmetric; each is computed once.
+ * Matrices with M <= 64 or N <= 64 are multiplied in single precision instead.  Sums
  * are taken in an order that is fixed for a call's sizes, so repeated calls give
  * identical bits, whatever the batch around a matrix.  X has to be finite.
  *

@@ -190,3 +190,13 @@ def test_largest_batch():
         s = z @ z.transpose(0, 2, 1)
         z = a * z + (b * s + c * s @ s) @ z
     assert np.abs(y - z).max() <= 40 * 3.5 ** 5 * 2.0 ** -22
+
+
+@pytest.mark.parametrize("out", TYPES)
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("shape", [(2, 64, 65), (2, 65, 64), (1, 64, 1024), (1, 1025, 63),
+                                   (3, 33, 2100), (1, 64, 8192), (1, 8193, 40)])
+def test_short_matrices(shape, kind, out):
+    """A side of at most 64: one slab of columns and several, of one block and several."""
+    y, held = _run(_values(21, shape), kind, out, pad=3)
+    _check(y, held, out)

@@ -57,8 +57,11 @@ def test_workspace():
     size = sg.sgemm_orthogonalize_workspace_size
     assert size(0, 5, 5) == 0 and size(3, 0, 5) == 0
     # Z, twice its transpose, S and P with 32 columns a block of 128 bytes; parts of a norm
-    assert size(1, 40, 70) == 40 * 3 * 128 + 2 * 70 * 2 * 128 + 2 * 40 * 2 * 128 + 8 * 3
-    assert size(7, 70, 40) == 7 * (40 * 3 * 128 + 2 * 70 * 2 * 128 + 2 * 40 * 2 * 128 + 8 * 5)
+    assert size(1, 65, 70) == 65 * 3 * 128 + 2 * 70 * 3 * 128 + 2 * 65 * 3 * 128 + 8 * 5
+    assert size(7, 70, 65) == 7 * (65 * 3 * 128 + 2 * 70 * 3 * 128 + 2 * 65 * 3 * 128 + 8 * 5)
+    # up to 64 rows or columns: Z and S's parts of 64 columns twice, in single precision
+    assert size(1, 40, 70) == 2 * 4 * (40 * 70 + 2 * 40 * 40) + 8 * 3
+    assert size(7, 70, 64) == 7 * (2 * 4 * (64 * 70 + 2 * 64 * 64) + 8 * 5)
     need = size(2, 5, 7)
     assert _status(workspace_bytes=need) == READY and _status(workspace_bytes=need - 1) == INVALID
     with pytest.raises(sg.SgemmError):
