@@ -323,7 +323,9 @@ __global__ void __launch_bounds__(kTokens *kWave) route_kernel(RouteArgs p) {
     wave_fence();
     const int share = p.group_share, g = lane / share;
     const Top2<float> best = group_top2(p, row);
-    const unsigned score = g < p.groups ? order_key(best.sum(p.group_top)) : 0;
+    const float sum = best.sum(p.group_top);
+    const bool some = g < p.groups && best.first != kMinusInf;  // the group has an expert
+    const unsigned score = some ? order_key(sum) : 0;
     int before = 0;  // groups that come before the lane's
     for (int o = 0; o < p.groups; ++o) {
       const unsigned other = (unsigned)__builtin_amdgcn_readlane((int)score, o * share);
@@ -331,10 +333,15 @@ __global__ void __launch_bounds__(kTokens *kWave) route_kernel(RouteArgs p) {
     }
     const bool mine = g < p.groups && before < p.keep;
     lanes = __ballot(mine);
-    // The lowest of the kept and the highest of the others have to be apart.
-    const unsigned low = ~wave_max(mine ? ~score : 0u);
-    const unsigned high = wave_max(g < p.groups && !mine ? score : 0u);
-    if (high != 0 && !apart(key_value(low), key_value(high), 2.f * off))
+    // A sum is off by what its two terms are off by, and three roundings that go by the
+    // terms' sizes: where the terms cancel, these are not small against the sum.  The
+    // lowest of the kept and the highest of the others have to be further apart, and
+    // every sum inside single precision's range.
+    const float second = p.group_top > 1 && best.second != kMinusInf ? fabsf(best.second) : 0.f;
+    const float error = 2.f * off + 0x1p-22f * (fabsf(best.first) + second);
+    const unsigned low = ~wave_max(mine && some ? ~order_key(sum - error) : 0u);
+    const unsigned high = wave_max(some && !mine ? order_key(sum + error) : 0u);
+    if (__ballot(some && !(fabsf(sum) < -kMinusInf)) != 0 || (high != 0 && low <= high))
       lanes = groups_in_double<EPL>(p, l, top, room[wave]);
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
