@@ -41,7 +41,7 @@ struct SplitFormat {
   struct Frag {
     f16x8 high, low;
   };
-  static constexpr int kSteps = 2, kReads = 2, kMfma = 3, kChains = 3;
+  static constexpr int kSteps = 2, kReads = 2, kMfma = 3, kChains = 1;
   template <int S, class At>
   __device__ __forceinline__ static Frag load(int half, At at) {
     return {__builtin_bit_cast(f16x8, *at(2 * S + half)),
@@ -274,13 +274,16 @@ ortho_product_kernel(OrthoProductArgs p, TileMap map, FastDiv by_triangle, int t
   // Register e of lane l holds row acc32_row(l, e), column l % 32 of a block: four
   // rows 8 q + 4 (l / 32) .. + 3, which are neighbours in a transposed matrix.
   const SplitMatrix &t = SYMMETRIC ? p.d : p.d_t;
-  const bool mirror = t.at && (!SYMMETRIC || tm != tn);
 #pragma unroll
   for (int i = 0; i < FM; ++i)
 #pragma unroll
     for (int j = 0; j < FN; ++j) {
       const int mb = mw + i * 32, nb = nw + j * 32;  // the block's origin
       if (mb >= M || nb >= N) continue;
+      // Blocks above the diagonal come from below it, in whatever tile they lie: an
+      // element's terms are added in the same order with every tile.
+      if (SYMMETRIC && mb < nb) continue;
+      const bool mirror = t.at && (!SYMMETRIC || mb > nb);
       float v[16];
 #pragma unroll
       for (int e = 0; e < 16; ++e) v[e] = p.f1 * acc[i][j][e];
