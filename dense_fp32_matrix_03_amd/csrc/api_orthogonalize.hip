@@ -17,19 +17,27 @@ using sgemm_api::kMaxWorkItems;
 constexpr int64_t kMaxSize = int64_t(1) << 20;  // of a matrix: a slice of it is below 2^31 bytes
 constexpr int64_t kMaxBatch = 65535;            // the second dimension of a launch
 constexpr int64_t kMaxSteps = 64;
+// Steps after which the rows and columns of Z are looked at again: until then they may
+// have grown by the polynomials' bound, 3.44 a step for common ones, where those that
+// are parallel to large ones did not.  8 such steps are 2^14.3 of the 2^17 that a held
+// element may lie below its row's bound with all of its digits.
+constexpr int64_t kLookAgain = 8;
+constexpr int64_t kLooks = (kMaxSteps - 1) / kLookAgain;
 
 int64_t tiles(int64_t n, int64_t t) { return (n + t - 1) / t; }
 bool misaligned(const void *p, unsigned to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
 bool bad_type(int type) { return type != SGEMM_TYPE_F32 && type != SGEMM_TYPE_BF16; }
 unsigned size_of(int type) { return type == SGEMM_TYPE_F32 ? 4 : 2; }
 
-// The workspace: Z, Z transposed twice (a step reads one and writes the other), S
-// and P of every matrix, and the parts of the norms.  Short matrices: the parts of the
-// norms, and Z and the parts of S twice.
+// The workspace: Z and Z transposed twice (a step reads one and writes the other), S and P
+// in pieces, Z transposed and S in floats; sizes of rows and columns, in parts, and then once for
+// each look at them.  Short matrices: the parts of the norms, and Z and the parts of S
+// twice.
 struct Layout {
   int m, n;
   int64_t z, zt, s;     // bytes of a matrix
   int64_t parts;        // of a norm
+  int64_t row_parts, col_parts, rows, cols;  // bytes of a matrix
   int64_t total;
   // Where m is short: Z and S's parts, twice each.
   bool is_short;
@@ -40,12 +48,22 @@ struct Layout {
     z = sgemm::split_bytes(m, n);
     zt = sgemm::split_bytes(n, m);
     s = sgemm::split_bytes(m, m);
-    parts = tiles(M * tiles(N, sgemm::kNormRun), 16);
-    if (parts > sgemm::kNormParts) parts = sgemm::kNormParts;
     is_short = m <= sgemm::kShort;
+    if (is_short) {
+      parts = tiles(M * tiles(N, sgemm::kNormRun), 16);
+      if (parts > sgemm::kNormParts) parts = sgemm::kNormParts;
+    } else {
+      parts = (int64_t)sgemm::sizes_bands(M, N) * sgemm::sizes_runs(N);
+    }
+    row_parts = 4 * sgemm::sizes_runs(N) * M;
+    col_parts = 4 * sgemm::sizes_bands(M, N) * N;
+    rows = 4 * (1 + kLooks) * M;
+    cols = 4 * (1 + kLooks) * N;
     short_z = 4 * (int64_t)m * n;
     short_parts = 4 * (int64_t)m * m * sgemm::short_slabs(n);
-    total = batch * (8 * parts + (is_short ? 2 * (short_z + short_parts) : z + 2 * zt + 2 * s));
+    total = batch * (8 * parts + (is_short ? 2 * (short_z + short_parts)
+                                           : 8 + z + 3 * zt + 3 * s + row_parts + col_parts + rows +
+                                                 cols));
   }
 };
 
@@ -77,12 +95,20 @@ double largest(double a, double b, double c, double top) {
   return most;
 }
 
-// The power of two by which a matrix with no element above `bound` is held: the
-// largest stays below 2^15, half of what half precision holds.
-int shift_for(double bound) {
+// The largest |a + b t + c t^2| for 0 <= t <= top: how much a step can make of a vector.
+double largest_growth(double a, double b, double c, double top) {
+  auto at = [&](double t) { return fabs(a + t * (b + t * c)); };
+  double most = fmax(at(0), at(top));
+  const double t = c != 0 ? -b / (2 * c) : 0;
+  return t > 0 && t < top ? fmax(most, at(t)) : most;
+}
+
+// The least e with bound < 2^e, with room for roundings.
+int exponent_of(double bound) {
+  if (!(bound > 0)) return -1000;
   int e;
-  frexp(fmax(bound * 1.02, ldexp(1.0, -60)), &e);  // below 2^e
-  return 15 - e;
+  frexp(bound * 1.02, &e);
+  return e;
 }
 
 // The launches for a short matrix.
@@ -190,69 +216,129 @@ int sgemm_orthogonalize(int64_t batch, int64_t M, int64_t N, int64_t steps, int6
     return short_steps(l, batch, M, N, steps, sets, coefficients, eps, alpha, typeX, X, ldx,
                        strideX, typeY, Y, ldy, strideY, workspace, s);
   char *at = static_cast<char *>(workspace);
+  auto take = [&](int64_t bytes) {
+    char *const from = at;
+    at += batch * bytes;
+    return from;
+  };
   auto matrix = [&](int rows, int cols) {
-    const sgemm::SplitMatrix x{at, rows, cols, sgemm::split_bytes(rows, cols)};
-    at += batch * x.stride;
-    return x;
+    const int64_t bytes = sgemm::split_bytes(rows, cols);
+    return sgemm::SplitMatrix{take(bytes), rows, cols, bytes};
   };
   const sgemm::SplitMatrix z = matrix(l.m, l.n), S = matrix(l.m, l.m), P = matrix(l.m, l.m);
   sgemm::SplitMatrix zt[2] = {matrix(l.n, l.m), matrix(l.n, l.m)};
-  const sgemm::SplitMatrix none{nullptr, 0, 0, 0};
+  const sgemm::SplitMatrix z_floats = matrix(l.n, l.m), s_floats = matrix(l.m, l.m), none{nullptr, 0, 0, 0};
   const bool tall = M > N;
 
-  sgemm::OrthoSplitArgs in;
-  in.x = {(int)M, (int)N, X, ldx, strideX, reinterpret_cast<double *>(at), (int)l.parts};
+  sgemm::OrthoSizesArgs in;
+  in.M = (int)M;
+  in.N = (int)N;
+  in.X = X;
+  in.ldx = ldx;
+  in.strideX = strideX;
   in.eps = eps;
-  int shift = shift_for(bound[0]);
-  in.shift = shift;
-  in.rows = tall ? zt[0] : z;
-  in.cols = tall ? z : zt[0];
+  in.band = sgemm::sizes_band(M, N);
+  in.bands = sgemm::sizes_bands(M, N);
+  in.runs = sgemm::sizes_runs(N);
+  in.summed = in.bands + in.runs > sgemm::kMostSizeParts;
+  in.parts = reinterpret_cast<double *>(take(8 * l.parts));
+  in.scale = reinterpret_cast<double *>(take(8));
+  in.row_parts = reinterpret_cast<unsigned *>(take(l.row_parts));
+  in.col_parts = reinterpret_cast<unsigned *>(take(l.col_parts));
+  in.rows = reinterpret_cast<unsigned *>(take(l.rows));
+  in.cols = reinterpret_cast<unsigned *>(take(l.cols));
+  in.again = (int)((steps - 1) / kLookAgain);
   const bool x_bf16 = typeX == SGEMM_TYPE_BF16, y_bf16 = typeY == SGEMM_TYPE_BF16;
-  hipError_t err = sgemm::launch_ortho_norm(in.x, x_bf16, (int)batch, s);
-  if (err == hipSuccess) err = sgemm::launch_ortho_split(in, x_bf16, (int)batch, s);
+
+  // Z's rows and columns: their largest magnitudes when they were last looked at, `look`,
+  // times the root of their length bound their norms (2^of_rows, 2^of_cols times the power
+  // of two above the magnitude), and `growth` what these have become since.
+  unsigned *const tops_m = tall ? in.cols : in.rows, *const tops_n = tall ? in.rows : in.cols;
+  const int of_rows = exponent_of(sqrt((double)l.n)), of_cols = exponent_of(sqrt((double)l.m));
+  int look = 0;
+  double growth = 1;
+  // The scale of Z's rows (or columns) before step k, and of what is as much larger as
+  // 2^more.
+  auto scale_of = [&](bool rows, int64_t k, int more) {
+    const int add = (rows ? of_rows : of_cols) + exponent_of(growth) - 126 + more;
+    return sgemm::RowScale{
+        rows ? tops_m + look * batch * l.m : tops_n + look * batch * l.n, add,
+        exponent_of(bound[k]) + more};
+  };
+  sgemm::OrthoSplitArgs split;
+  split.x = in;
+  sgemm::RowScale z_scale = scale_of(true, 0, 0), zt_scale = scale_of(false, 0, 0);  // as held
+  split.row_scale = tall ? zt_scale : z_scale;
+  split.col_scale = tall ? z_scale : zt_scale;
+  split.rows = tall ? zt[0] : z;
+  split.cols = tall ? z : zt[0];
+  split.floats = z_floats;
+  split.floats_turned = !tall;
+  hipError_t err = sgemm::launch_ortho_sizes(in, x_bf16, (int)batch, s);
+  if (err == hipSuccess) err = sgemm::launch_ortho_split(split, x_bf16, (int)batch, s);
   for (int64_t k = 0; k < steps && err == hipSuccess; ++k) {
     const float *c = coefficients + (sets == 1 ? 0 : 3 * k);
     const double top = bound[k] * bound[k];
-    const int shift_s = shift_for(top);
-    const int shift_p = shift_for(fabs(c[1]) * top + fabs(c[2]) * top * top);
+    // A row of S is at most the largest singular value times Z's row, one of P at most
+    // that times |b| + |c| |S|.
+    const int more_s = exponent_of(bound[k]);
+    const int more_p = exponent_of(bound[k] * (fabs(c[1]) + fabs(c[2]) * top));
     const bool last = k + 1 == steps;
-    const int shift_y = last ? 0 : shift_for(bound[k + 1]);
-    const double out = last ? alpha : 1.0;
-    sgemm::OrthoProductArgs p;
-    p.Y = nullptr;
-    p.ldy = p.strideY = 0;
-    p.y_transposed = false;
+    sgemm::OrthoProductArgs p{};
+    p.e = p.d_t = p.f_t = none;
     // S = Z Z^T
     p.a = p.b = z;
-    p.e_t = none;
-    p.f1 = (float)ldexp(1.0, shift_s - 2 * shift);
-    p.f2 = 0.f;
+    p.a_scale = p.b_scale = z_scale;
+    p.f1 = 1.f;
     p.d = S;
-    p.d_t = none;
+    p.d_scale = p.d_t_scale = scale_of(true, k, more_s);
+    p.f_t = s_floats;
     err = sgemm::launch_ortho_product(p, true, false, (int)batch, cus, s);
     if (err != hipSuccess) break;
     // P = b S + c S S
-    p.a = p.b = p.e_t = S;
-    p.f1 = (float)(c[2] * ldexp(1.0, shift_p - 2 * shift_s));
-    p.f2 = (float)(c[1] * ldexp(1.0, shift_p - shift_s));
+    p.a = p.b = S;
+    p.a_scale = p.b_scale = p.d_scale;
+    p.e = s_floats;
+    p.f_t = none;
+    p.f1 = c[2];
+    p.f2 = c[1];
     p.d = P;
+    p.d_scale = p.d_t_scale = scale_of(true, k, more_p);
     err = sgemm::launch_ortho_product(p, true, false, (int)batch, cus, s);
     if (err != hipSuccess) break;
     // a Z + P Z
     p.a = P;
-    p.b = p.e_t = zt[k % 2];
-    p.f1 = (float)(out * ldexp(1.0, shift_y - shift_p - shift));
-    p.f2 = (float)(out * c[0] * ldexp(1.0, shift_y - shift));
-    p.d = last ? none : z;
-    p.d_t = last ? none : zt[1 - k % 2];
+    p.b = zt[k % 2];
+    p.a_scale = p.d_scale;
+    p.b_scale = zt_scale;
+    p.e = z_floats;
+    p.f1 = 1.f;
+    p.f2 = c[0];
     if (last) {
+      p.d = none;
+      p.d_t_scale = p.b_scale;  // read, but not used, as d_scale is
       p.Y = Y;
       p.ldy = ldy;
       p.strideY = strideY;
       p.y_transposed = tall;
+      p.alpha = alpha;
+    } else {
+      growth = fmin(growth * 1.001 * largest_growth(c[0], c[1], c[2], top), 1e300);
+      p.d = z;
+      p.d_scale = scale_of(true, k + 1, 0);
+      p.d_t = zt[1 - k % 2];
+      p.d_t_scale = scale_of(false, k + 1, 0);
+      p.f_t = z_floats;
     }
     err = sgemm::launch_ortho_product(p, false, y_bf16, (int)batch, cus, s);
-    shift = shift_y;
+    z_scale = p.d_scale;
+    zt_scale = p.d_t_scale;
+    if (!last && (k + 1) % kLookAgain == 0 && err == hipSuccess) {
+      ++look;
+      growth = 1;
+      err = sgemm::launch_ortho_look(z_floats, tops_n + look * batch * l.n,
+                                     tops_m + look * batch * l.m, (int)batch, s);
+    }
   }
   return err == hipSuccess ? SGEMM_OK : SGEMM_ERR_LAUNCH;
 }

@@ -134,26 +134,60 @@ struct BlockImage {
   }
 };
 
-// The pieces of a block of sums (as the matrix instructions leave them) to images of
-// the block and, with `both`, of its transpose.
-__device__ __forceinline__ void split_block(const float v[16], int r32, int half,
-                                            const BlockImage &d, const BlockImage &t, bool both) {
+// 2^x.
+__device__ __forceinline__ float power_of_two(int x) {
+  return __uint_as_float((unsigned)(min(max(x, -126), 127) + 127) << 23);
+}
+
+// One of two for each lane, out of scalar registers: a reference to one or the other would
+// read the kernel's arguments through memory.
+__device__ __forceinline__ RowScale either(bool first, const RowScale a, const RowScale b) {
+  return {first ? a.top : b.top, first ? a.add : b.add, first ? a.cap : b.cap};
+}
+
+// The pieces of a block of sums (as the matrix instructions leave them) times `scale` of
+// each row to an image of the block.
+__device__ __forceinline__ void split_block(const float v[16], const float scale[16], int r32,
+                                            int half, const BlockImage &d) {
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    _Float16 h, l;
+    split(v[e] * scale[e], h, l);
+    const int m = 8 * (e / 4) + 4 * half + e % 4;
+    reinterpret_cast<_Float16 *>(d.chunk(m, r32 / 8))[r32 % 8] = h;
+    reinterpret_cast<_Float16 *>(d.chunk(m, 4 + r32 / 8))[r32 % 8] = l;
+  }
+}
+// The same of its transpose, whose row is the lane's.
+__device__ __forceinline__ void split_transposed(const float v[16], float scale, int r32, int half,
+                                                 const BlockImage &t) {
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     f16x4 high, low;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       _Float16 h, l;
-      split(v[4 * q + e], h, l);
+      split(v[4 * q + e] * scale, h, l);
       high[e] = h;
       low[e] = l;
-      const int m = 8 * q + 4 * half + e;
-      reinterpret_cast<_Float16 *>(d.chunk(m, r32 / 8))[r32 % 8] = h;
-      reinterpret_cast<_Float16 *>(d.chunk(m, 4 + r32 / 8))[r32 % 8] = l;
     }
-    if (both) {
-      *reinterpret_cast<f16x4 *>(t.chunk(r32, q) + 8 * half) = high;
-      *reinterpret_cast<f16x4 *>(t.chunk(r32, 4 + q) + 8 * half) = low;
+    *reinterpret_cast<f16x4 *>(t.chunk(r32, q) + 8 * half) = high;
+    *reinterpret_cast<f16x4 *>(t.chunk(r32, 4 + q) + 8 * half) = low;
+  }
+}
+// The floats: as they are, or transposed.
+__device__ __forceinline__ void floats_block(const float v[16], bool turned, int r32, int half,
+                                             const BlockImage &d) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int m = 8 * q + 4 * half;
+    if (turned) {
+      *reinterpret_cast<f32x4 *>(d.chunk(r32, m / 4)) =
+          f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        reinterpret_cast<float *>(d.chunk(m + e, r32 / 4))[r32 % 4] = v[4 * q + e];
     }
   }
 }
@@ -170,39 +204,226 @@ __device__ __forceinline__ void store_block(const SplitMatrix &x, int batch, int
   }
 }
 
+// A work-group's band of rows by 512 columns: a wave has every fourth row, 8 columns a
+// lane, and loads four of its rows together.
+template <bool BF16>
+__global__ void __launch_bounds__(256) ortho_sizes_kernel(OrthoSizesArgs p) {
+  using P = Piece<BF16>;
+  constexpr int kTogether = 4, kPieces = kNormRun / (kWave * P::V);
+  const int lane = threadIdx.x % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int run = blockIdx.x % p.runs, band = blockIdx.x / p.runs;
+  const long batch = blockIdx.y;
+  const int n0 = run * kNormRun, end = min((band + 1) * p.band, p.M);
+  const bool whole = p.N - n0 >= kNormRun;
+  const long base = batch * p.strideX;
+  unsigned *const row_parts = p.row_parts + (batch * p.runs + run) * p.M;
+  double sum = 0;
+  unsigned top[kPieces][P::V];  // of the lane's columns
+#pragma unroll
+  for (int k = 0; k < kPieces; ++k)
+#pragma unroll
+    for (int e = 0; e < P::V; ++e) top[k][e] = 0;
+  for (int row = band * p.band + wave; row < end; row += 4 * kTogether) {
+    P x[kTogether][kPieces];
+#pragma unroll
+    for (int i = 0; i < kTogether; ++i)
+#pragma unroll
+      for (int k = 0; k < kPieces; ++k) {
+        const int n = n0 + (k * kWave + lane) * P::V, r = row + 4 * i;
+        x[i][k].load(p.X, base + min(r, end - 1) * p.ldx + n, r < end ? p.N - n : 0,
+                     whole && r < end);
+      }
+    unsigned most[kTogether];
+#pragma unroll
+    for (int i = 0; i < kTogether; ++i) {
+      most[i] = 0;
+#pragma unroll
+      for (int k = 0; k < kPieces; ++k) {
+        float v[P::V];
+        x[i][k].get(v);
+        most[i] = max(most[i], x[i][k].top());
+#pragma unroll
+        for (int e = 0; e < P::V; ++e) {
+          sum += (double)v[e] * (double)v[e];
+          top[k][e] = max(top[k][e], __float_as_uint(v[e]) & 0x7fffffffu);
+        }
+      }
+    }
+#pragma unroll
+    for (int d = 32; d > 0; d /= 2)
+#pragma unroll
+      for (int i = 0; i < kTogether; ++i)
+        most[i] = max(most[i], (unsigned)__shfl_xor((int)most[i], d));
+#pragma unroll
+    for (int i = 0; i < kTogether; ++i)
+      if (lane == 0 && row + 4 * i < end) row_parts[row + 4 * i] = most[i];
+  }
+  __shared__ unsigned tops[4][kNormRun];
+#pragma unroll
+  for (int k = 0; k < kPieces; ++k)
+#pragma unroll
+    for (int e = 0; e < P::V; ++e) tops[wave][(k * kWave + lane) * P::V + e] = top[k][e];
+  sum = group_sum(sum);  // its barrier is for tops too
+  if (threadIdx.x == 0) p.parts[(batch * p.bands + band) * p.runs + run] = sum;
+  for (int i = threadIdx.x; i < kNormRun && n0 + i < p.N; i += 256)
+    p.col_parts[(batch * p.bands + band) * p.N + n0 + i] =
+        max(max(tops[0][i], tops[1][i]), max(tops[2][i], tops[3][i]));
+}
+
+// The largest of `count` numbers `step` apart.
+__device__ __forceinline__ unsigned top_of(const unsigned *part, int count, long step) {
+  constexpr int kTogether = 8;
+  unsigned top = 0;
+  for (int k = 0; k < count; k += kTogether) {
+    unsigned v[kTogether];
+#pragma unroll
+    for (int j = 0; j < kTogether; ++j) v[j] = part[min(k + j, count - 1) * step];
+#pragma unroll
+    for (int j = 0; j < kTogether; ++j) top = max(top, v[j]);
+  }
+  return top;
+}
+
+// What X is multiplied by, from the parts of its sum of squares.
+__device__ __forceinline__ double scale_of(const OrthoSizesArgs &p, long batch) {
+  const int all = p.bands * p.runs;
+  double sum = 0;
+  for (int k = threadIdx.x; k < all; k += 256) sum += p.parts[batch * all + k];
+  const double norm = sqrt(group_sum(sum)) + (double)p.eps;
+  return norm > 0 ? 1.0 / norm : norm;  // NaN stays
+}
+
+// Row (or column) i's size, now that the scale is known, to where the products find it.
+__device__ __forceinline__ unsigned keep_size(const OrthoSizesArgs &p, bool of_rows, long batch,
+                                              int i, unsigned top, double scale, bool write) {
+  const long n = of_rows ? p.M : p.N;
+  const unsigned size =
+      __float_as_uint((float)(scale * (double)__uint_as_float(top))) & 0x7fffffffu;
+  if (write) {
+    unsigned *const to = (of_rows ? p.rows : p.cols) + batch * n + i;
+    *to = size;
+    for (int k = 1; k <= p.again; ++k) to[k * gridDim.y * n] = 0;
+  }
+  return size;
+}
+
+// For very long rows or columns, whose sizes are in so many parts that each block of the
+// next launch would not add them up for itself: a thread has a row or a column.
+__global__ void __launch_bounds__(256) ortho_scales_kernel(OrthoSizesArgs p) {
+  const long batch = blockIdx.y;
+  const int row_groups = (p.M + 255) / 256;
+  const bool of_rows = (int)blockIdx.x < row_groups;
+  const int i = ((int)blockIdx.x - (of_rows ? 0 : row_groups)) * 256 + (int)threadIdx.x;
+  const int n = of_rows ? p.M : p.N, parts = of_rows ? p.runs : p.bands;
+  const unsigned top =
+      top_of((of_rows ? p.row_parts : p.col_parts) + batch * parts * n + min(i, n - 1), parts, n);
+  const double scale = scale_of(p, batch);
+  if (blockIdx.x == 0 && threadIdx.x == 0) p.scale[batch] = scale;
+  if (i < n) keep_size(p, of_rows, batch, i, top, scale, true);
+}
+
 // A block of 32 x 32 per wave, in the layout of the matrix instructions' results: lane
 // l has column l % 32 of rows 8 q + 4 (l / 32) .. + 3.
 template <bool BF16>
 __global__ void __launch_bounds__(256) ortho_split_kernel(OrthoSplitArgs p, FastDiv by_across) {
-  const OrthoNormArgs &x = p.x;
+  const OrthoSizesArgs &x = p.x;
   const int lane = threadIdx.x % kWave;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const double part = (int)threadIdx.x < x.n_parts
-                          ? x.parts[(long)blockIdx.y * x.n_parts + threadIdx.x] : 0.0;
   const int block = blockIdx.x * 4 + wave, row = by_across(block);
   const int bm = row * 32, bn = (block - row * ((x.N + 31) / 32)) * 32;
   const int r32 = lane % 32, half = lane / 32;
+  const long batch = blockIdx.y;
   // Every lane loads, from the nearest element there is, so that the loads go out
   // together; what lies past the matrix is then dropped.
   float v[16];
-  const int n = bn + r32;
+  const int n = min(bn + r32, x.N - 1);
 #pragma unroll
   for (int e = 0; e < 16; ++e) {
     const int m = min(bm + acc32_row(lane, e), x.M - 1);
-    v[e] = load1<BF16>(x.X, (long)blockIdx.y * x.strideX + m * x.ldx + min(n, x.N - 1));
+    v[e] = load1<BF16>(x.X, batch * x.strideX + m * x.ldx + n);
   }
-  const double norm = sqrt(group_sum(part)) + (double)p.eps;
-  const double scale = norm > 0 ? ldexp(1.0, p.shift) / norm : norm;  // NaN stays
+  // A lane has the size of a row, or of a column.
+  const bool of_rows = half == 0;
+  const int i = of_rows ? min(bm + r32, x.M - 1) : n;
+  double scale;
+  unsigned size;
+  if (x.summed) {
+    scale = x.scale[batch];
+    size = (of_rows ? x.rows + batch * x.M : x.cols + batch * x.N)[i];
+  } else {
+    const int parts = of_rows ? x.runs : x.bands, length = of_rows ? x.M : x.N;
+    const unsigned top = top_of(
+        (of_rows ? x.row_parts : x.col_parts) + batch * parts * length + i, parts, length);
+    scale = scale_of(x, batch);
+    size = keep_size(x, of_rows, batch, i, top, scale,
+                     of_rows ? bn == 0 && bm + r32 < x.M : bm == 0 && bn + r32 < x.N);
+  }
   if (bm >= x.M) return;  // whole waves: no barrier follows
+  const RowScale by = either(of_rows, p.row_scale, p.col_scale);
+  __shared__ __attribute__((aligned(16))) float scales[4][2][32];
+  scales[wave][half][r32] = power_of_two(kHeldTop - by.exponent(size));
+  wave_fence();
+  float row_scale[16];
 #pragma unroll
-  for (int e = 0; e < 16; ++e)
-    v[e] = bm + acc32_row(lane, e) < x.M && n < x.N ? (float)(scale * (double)v[e]) : 0.f;
+  for (int q = 0; q < 4; ++q) {
+    const f32x4 r = *reinterpret_cast<const f32x4 *>(&scales[wave][0][8 * q + 4 * half]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) row_scale[4 * q + e] = r[e];
+  }
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const bool in = bm + acc32_row(lane, e) < x.M && bn + r32 < x.N;
+    v[e] = in ? (float)(scale * (double)v[e]) : 0.f;
+  }
   __shared__ __attribute__((aligned(16))) char images[4][2][4096];
-  const BlockImage rows{images[wave][0]}, cols{images[wave][1]};
-  split_block(v, r32, half, rows, cols, true);
+  const BlockImage rows{images[wave][0]}, cols{images[wave][1]}, &floats = rows;
+  split_block(v, row_scale, r32, half, rows);
+  split_transposed(v, scales[wave][1][r32], r32, half, cols);
   wave_fence();
   store_block(p.rows, blockIdx.y, bm, bn, x.M, lane, rows);
   store_block(p.cols, blockIdx.y, bn, bm, x.N, lane, cols);
+  wave_fence();
+  floats_block(v, p.floats_turned, r32, half, floats);
+  wave_fence();
+  if (p.floats_turned)
+    store_block(p.floats, blockIdx.y, bn, bm, x.N, lane, floats);
+  else
+    store_block(p.floats, blockIdx.y, bm, bn, x.M, lane, floats);
+}
+
+// The largest magnitudes of the rows and columns of a matrix of floats: 8 lanes have a row
+// of 32 columns, a work-group 32 such rows at a time.
+__global__ void __launch_bounds__(256) ortho_look_kernel(SplitMatrix x, unsigned *rows,
+                                                         unsigned *cols) {
+  const int lane = threadIdx.x % kWave, part = threadIdx.x % 8;
+  const long batch = blockIdx.z;
+  const int c0 = blockIdx.y * 32;
+  unsigned top[4] = {0, 0, 0, 0};  // of the lane's columns
+  for (int r0 = blockIdx.x * kLookRows; r0 < min((int)(blockIdx.x + 1) * kLookRows, x.rows); r0 += 32) {
+    const int r = r0 + (int)threadIdx.x / 8;
+    unsigned most = 0;
+    if (r < x.rows) {
+      const slice_i32x4 v =
+          *reinterpret_cast<const slice_i32x4 *>(x.place(blockIdx.z, r, c0) + part * 16);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const unsigned size = (unsigned)v[e] & 0x7fffffffu;
+        top[e] = max(top[e], size);
+        most = max(most, size);
+      }
+    }
+#pragma unroll
+    for (int d = 4; d > 0; d /= 2) most = max(most, (unsigned)__shfl_xor((int)most, d));
+    if (r < x.rows && part == 0) atomicMax(rows + batch * x.rows + r, most);
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+#pragma unroll
+    for (int d = 32; d > 4; d /= 2) top[e] = max(top[e], (unsigned)__shfl_xor((int)top[e], d));
+    const int c = c0 + part * 4 + e;
+    if (lane < 8 && c < x.cols) atomicMax(cols + batch * x.cols + c, top[e]);
+  }
 }
 
 // Position `id` of the tiles on and below a diagonal, row by row: row t has t + 1.
@@ -251,21 +472,37 @@ ortho_product_kernel(OrthoProductArgs p, TileMap map, FastDiv by_triangle, int t
         for (int k = 0; k < 4; ++k) {
           const int n = nw + j * 32 + 8 * k + lane / 8, m = mw + i * 32;
           const auto *at =
-              reinterpret_cast<const slice_i32x4 *>(p.e_t.place(batch, n, m) + lane % 8 * 16);
+              reinterpret_cast<const slice_i32x4 *>(p.e.place(batch, n, m) + lane % 8 * 16);
           if (whole)
             e_t[i][j][k] = *at;
           else
             e_t[i][j][k] = n < N && m < M ? *at : slice_i32x4{0, 0, 0, 0};
         }
   };
-  if (p.e_t.at) load_e(mw + 32 * FM <= M && nw + 32 * FN <= N);
+  if (p.e.at) load_e(mw + 32 * FM <= M && nw + 32 * FN <= N);
 
   auto rows = [&](const SplitMatrix &x, int first, int n) {
     return SliceRows{x.place(batch, first, 0), kSliceRow, (long)x.rows * kSliceRow, n};
   };
+  // A thread has a row of A or of B: the sizes that its scales go by are loaded here, and
+  // waited for after the sums.
+  static_assert(BM + BN <= Tile::kThreads, "a thread for each row");
+  const bool of_a = threadIdx.x < BM;
+  const long at = of_a ? (long)batch * M + min(m0 + (int)threadIdx.x, M - 1)
+                       : (long)batch * N + min(n0 + (int)threadIdx.x - BM, N - 1);
+  const RowScale from = either(of_a, p.a_scale, p.b_scale), to = either(of_a, p.d_scale, p.d_t_scale);
+  const unsigned top_in = from.top[at], top_out = to.top[at];
+
   f32x16 acc[FM][FN];
   char *lds[NST];
   Tile::run(rows(p.a, m0, rows_a), rows(p.b, n0, rows_b), (p.a.cols + 31) / 32, acc, lds);
+  // What a row's and a column's sums are multiplied by, and the powers of two under which
+  // the results are held.
+  __shared__ __attribute__((aligned(16))) float in_scales[BM + BN], out_scales[BM + BN];
+  if (threadIdx.x < BM + BN) {
+    in_scales[threadIdx.x] = power_of_two(from.exponent(top_in) - kHeldTop) * (of_a ? p.f1 : 1.f);
+    out_scales[threadIdx.x] = power_of_two(kHeldTop - to.exponent(top_out));
+  }
   __syncthreads();  // no loads into the stages are left, of any wave
   const int wave = Tile::wave_id();
   const BlockImage e_image{lds[0] + wave * 4096}, t_image{lds[1] + wave * 4096},
@@ -284,20 +521,29 @@ ortho_product_kernel(OrthoProductArgs p, TileMap map, FastDiv by_triangle, int t
       // element's terms are added in the same order with every tile.
       if (SYMMETRIC && mb < nb) continue;
       const bool mirror = t.at && (!SYMMETRIC || mb > nb);
-      float v[16];
+      float v[16], scale_out[16];
+      const int of_b = BM + Tile::col0() + j * 32 + r32;
+      const float scale_b = in_scales[of_b];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) v[e] = p.f1 * acc[i][j][e];
-      if (p.e_t.at) {
+      for (int q = 0; q < 4; ++q) {
+        const int at = Tile::row0() + i * 32 + 8 * q + 4 * half;
+        const f32x4 in = *reinterpret_cast<const f32x4 *>(in_scales + at);
+        const f32x4 out = *reinterpret_cast<const f32x4 *>(out_scales + at);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[4 * q + e] = acc[i][j][4 * q + e] * scale_b * in[e];
+          scale_out[4 * q + e] = out[e];
+        }
+      }
+      if (p.e.at) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) *e_image.linear(lane, k) = e_t[i][j][k];
         wave_fence();
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const f16x4 high = *reinterpret_cast<const f16x4 *>(e_image.chunk(r32, q) + 8 * half);
-          const f16x4 low = *reinterpret_cast<const f16x4 *>(e_image.chunk(r32, 4 + q) + 8 * half);
+          const f32x4 e4 = *reinterpret_cast<const f32x4 *>(e_image.chunk(r32, 2 * q + half));
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            v[4 * q + e] = fmaf(p.f2, (float)high[e] + (float)low[e], v[4 * q + e]);
+          for (int e = 0; e < 4; ++e) v[4 * q + e] = fmaf(p.f2, e4[e], v[4 * q + e]);
         }
         wave_fence();
       }
@@ -305,17 +551,8 @@ ortho_product_kernel(OrthoProductArgs p, TileMap map, FastDiv by_triangle, int t
         // Floats, as the user's rows run: 32 of them are 128 bytes too.
         const bool turned = p.y_transposed;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int m = 8 * q + 4 * half;
-          if (turned) {
-            *reinterpret_cast<f32x4 *>(d_image.chunk(r32, m / 4)) =
-                f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
-          } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              reinterpret_cast<float *>(d_image.chunk(m + e, r32 / 4))[r32 % 4] = v[4 * q + e];
-          }
-        }
+        for (int e = 0; e < 16; ++e) v[e] *= p.alpha;
+        floats_block(v, turned, r32, half, d_image);
         wave_fence();
         const int r0 = turned ? nb : mb, c0 = (turned ? mb : nb) + lane % 8 * 4;
         const int rows = turned ? N : M, left = (turned ? M : N) - c0;
@@ -344,12 +581,15 @@ ortho_product_kernel(OrthoProductArgs p, TileMap map, FastDiv by_triangle, int t
         wave_fence();
         continue;
       }
-      split_block(v, r32, half, d_image, t_image, mirror);
+      split_block(v, scale_out, r32, half, d_image);
+      if (mirror) split_transposed(v, out_scales[of_b], r32, half, t_image);
+      if (p.f_t.at) floats_block(v, true, r32, half, e_image);
       wave_fence();
       // Rows of a result are written up to the end of their last 32 columns: past
       // its own columns the sums are 0.
       store_block(p.d, batch, mb, nb, M, lane, d_image);
       if (mirror) store_block(t, batch, nb, mb, N, lane, t_image);
+      if (p.f_t.at) store_block(p.f_t, batch, nb, mb, N, lane, e_image);
       wave_fence();
     }
 }
@@ -386,6 +626,19 @@ hipError_t launch_ortho_norm(const OrthoNormArgs &p, bool bf16, int batch, hipSt
   return hipGetLastError();
 }
 
+hipError_t launch_ortho_sizes(const OrthoSizesArgs &p, bool bf16, int batch, hipStream_t s) {
+  const dim3 block(256), grid((unsigned)((long)p.bands * p.runs), (unsigned)batch);
+  if (bf16)
+    hipLaunchKernelGGL(ortho_sizes_kernel<true>, grid, block, 0, s, p);
+  else
+    hipLaunchKernelGGL(ortho_sizes_kernel<false>, grid, block, 0, s, p);
+  const hipError_t err = hipGetLastError();
+  if (err != hipSuccess || !p.summed) return err;
+  const dim3 all((unsigned)((p.M + 255) / 256 + (p.N + 255) / 256), (unsigned)batch);
+  hipLaunchKernelGGL(ortho_scales_kernel, all, block, 0, s, p);
+  return hipGetLastError();
+}
+
 hipError_t launch_ortho_split(const OrthoSplitArgs &p, bool bf16, int batch, hipStream_t s) {
   const long blocks = ((p.x.M + 31L) / 32) * ((p.x.N + 31L) / 32);
   const dim3 grid((unsigned)((blocks + 3) / 4), (unsigned)batch), block(256);
@@ -397,40 +650,21 @@ hipError_t launch_ortho_split(const OrthoSplitArgs &p, bool bf16, int batch, hip
   return hipGetLastError();
 }
 
-// The tile by times in microseconds, n the tiles for each of the chip's compute units,
-// nk slices.  Measured on 256 compute units (S = Z Z^T, or a Z + P Z; m x n of Z, tiles
-// of 64 x 64 / 128 x 128 / 128 x 256):
-//   S    1024 x 1024      10.0 / 18.8       2048 x 2048      45 / 41
-//        2600 x 2600      91 / 58           2048 x 4096      80 / 58
-//        16 of 512 x 512  17.5 / 16.1       1500 x 1500      22 / 26
-//   a Z + P Z
-//        1024 x 1024      13.3 / 22 / 34    2048 x 2048      64 / 54 / 69
-//        2600 x 2600      132 / 116 / 107   2048 x 4096      122 / 103 / 92
-//        16 of 512 x 512  28 / 24 / 29      1500 x 1500      36 / 32 / 47
-// A tile of 64 x 64 is bound by what the caches deliver, 85 bytes a nanosecond and
-// compute unit; larger ones by the matrix cores, at the power limit once the chip is
-// full (1.1 PFLOP/s of half precision, where a large library product has 1.3).
+hipError_t launch_ortho_look(const SplitMatrix &x, unsigned *rows, unsigned *cols, int batch,
+                             hipStream_t s) {
+  // The third dimension of a launch ends at 65535, as a batch does.
+  const dim3 grid((unsigned)((x.rows + kLookRows - 1) / kLookRows), (unsigned)((x.cols + 31) / 32),
+                  (unsigned)batch);
+  hipLaunchKernelGGL(ortho_look_kernel, grid, dim3(256), 0, s, x, rows, cols);
+  return hipGetLastError();
+}
+
 hipError_t launch_ortho_product(const OrthoProductArgs &p, bool symmetric, bool y_bf16, int batch,
                                 int cus, hipStream_t s) {
-  const double nk = (p.a.cols + 31) / 32;
-  auto tiles = [&](int bm, int bn) {
-    const double tm = (p.a.rows + bm - 1) / bm, tn = (p.b.rows + bn - 1) / bn;
-    return batch * (symmetric ? tm * (tm + 1) / 2 : tm * tn) / cus;
-  };
-  const double n64 = tiles(64, 64), n128 = tiles(128, 128);
-  const double c64 = ceil(n64) * (0.2 * nk + 2);
-  if (symmetric) {
-    const double c128 = ceil(n128) * (0.38 * nk + 6 + 12 * fmin(n128, 1));
-    return c64 <= c128 ? launch<64, 64, 2, 2, 4>(p, true, y_bf16, batch, s)
-                       : launch<128, 128, 2, 4, 3>(p, true, y_bf16, batch, s);
-  }
-  const double c128 =
-      fmax(1, (ceil(n128) + n128) / 2) * ((0.38 + 0.22 * fmin(n128, 1)) * nk + 11);
-  const double n256 = tiles(128, 256);
-  const double c256 = ceil(n256) * (0.85 * nk + 12 + 50 * fmin(fmax(n256 - 0.6, 0), 0.4));
-  if (c64 <= c128 && c64 <= c256) return launch<64, 64, 2, 2, 4>(p, false, y_bf16, batch, s);
-  return c128 <= c256 ? launch<128, 128, 2, 4, 3>(p, false, y_bf16, batch, s)
-                      : launch<128, 256, 2, 4, 3>(p, false, y_bf16, batch, s);
+  const OrthoTile tile = ortho_tile(p.a.rows, p.b.rows, p.a.cols, symmetric, batch, cus);
+  if (tile == OrthoTile::k64) return launch<64, 64, 2, 2, 4>(p, symmetric, y_bf16, batch, s);
+  return tile == OrthoTile::k128 ? launch<128, 128, 2, 4, 3>(p, symmetric, y_bf16, batch, s)
+                                 : launch<128, 256, 2, 4, 3>(p, false, y_bf16, batch, s);
 }
 
 }  // namespace sgemm

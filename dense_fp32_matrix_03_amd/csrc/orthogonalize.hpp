@@ -3,26 +3,44 @@
 #pragma once
 
 #include <hip/hip_runtime.h>
+#include <math.h>
 #include <stdint.h>
 
 #include "common.hpp"
 
 namespace sgemm {
 
-// A batch of matrices in pieces: [cols / 32][rows] blocks of 128 bytes, 32 high
-// pieces of a row and then 32 low ones, the last columns padded with zeros.  A
-// value is (high + low) 2^-s with an s that the host keeps.
+// A batch of matrices in blocks of 128 bytes, [cols / 32][rows], the last columns padded
+// with zeros.  In pieces: 32 high pieces of a row and then 32 low ones, a value being
+// (high + low) 2^(e - kHeldTop) with the row's e (RowScale).  Or 32 floats.
 struct SplitMatrix {
   char *at;
   int rows, cols;
   long stride;  // bytes from one matrix to the next
-  // Where the high piece of (r, c) lies; the low one is 64 bytes after it.
+  // Where the high piece of (r, c) lies, the low one 64 bytes after it; of floats, the
+  // block's row.
   __device__ __forceinline__ char *place(int batch, int r, int c) const {
     return at + batch * stride + ((long)(c / 32) * rows + r) * 128 + c % 32 * 2;
   }
   __host__ __device__ __forceinline__ int padded() const { return (cols + 31) / 32 * 32; }
 };
 inline long split_bytes(long rows, long cols) { return (cols + 31) / 32 * rows * 128; }
+
+// The range of a row of a held matrix: no element reaches 2^e.  A row of one size among
+// rows of another keeps its digits only if e goes by the row.  e is known before the row
+// is: a product with Z's row or from the left can make no more of its norm than the
+// polynomials' bounds allow, so that every e is a constant of the step past the exponent
+// of the norm that Z's row had when it was last looked at, and at most a constant of
+// the step, as the whole matrix has it.
+constexpr int kHeldTop = 15;         // a held element is below 2^15, half of half precision's range
+constexpr int kLeastExponent = -100;
+struct RowScale {
+  const unsigned *top;  // [batch][rows] the bits of the largest magnitudes of Z's rows
+  int add, cap;
+  __device__ __forceinline__ int exponent(unsigned top) const {
+    return max(min((int)(top >> 23) + add, cap), kLeastExponent);
+  }
+};
 
 // The sum of squares, in parts, of every matrix of the batch.
 struct OrthoNormArgs {
@@ -36,31 +54,103 @@ constexpr int kNormRun = 512;    // elements of a row that a wave adds up at a t
 constexpr int kNormParts = 256;  // parts, at most: a work-group each, of 16 such runs or more
 hipError_t launch_ortho_norm(const OrthoNormArgs &p, bool bf16, int batch, hipStream_t s);
 
-// X 2^shift / (|X| + eps), in pieces, as it is and transposed.
-struct OrthoSplitArgs {
-  OrthoNormArgs x;
+// 1 / (|X| + eps) of every matrix, and the largest magnitudes of the rows and columns of X
+// times that.
+struct OrthoSizesArgs {
+  int M, N;
+  const void *X;
+  long ldx, strideX;
   float eps;
-  int shift;
-  SplitMatrix rows, cols;  // M x N and N x M
+  // A work-group has `band` rows by 512 columns, and writes its sum of squares and the
+  // largest magnitudes of its rows and columns.
+  int band, bands, runs;
+  double *parts;                    // [batch][bands][runs]
+  unsigned *row_parts, *col_parts;  // [batch][runs][M], [batch][bands][N]
+  bool summed;                      // by a launch of its own: very many parts
+  double *scale;                    // [batch], where summed
+  unsigned *rows, *cols;            // [1 + again][batch][M], [..][N]
+  int again;                        // sets after the first: zeros
+};
+inline int sizes_runs(long N) { return (int)((N + kNormRun - 1) / kNormRun); }
+// A multiple of 16, for about 224 work-groups: with what rounding adds, 65535 matrices
+// stay below 2^32 work-items.
+inline int sizes_band(long M, long N) {
+  const long share = (M * sizes_runs(N) + 223) / 224;
+  return (int)((share < M ? share : M) + 15) / 16 * 16;
+}
+inline int sizes_bands(long M, long N) { return (int)((M + sizes_band(M, N) - 1) / sizes_band(M, N)); }
+constexpr int kMostSizeParts = 24;  // of a row and of a column that each block adds up for itself
+hipError_t launch_ortho_sizes(const OrthoSizesArgs &p, bool bf16, int batch, hipStream_t s);
+
+// X times its scale, in pieces, as it is and transposed, and in floats.
+struct OrthoSplitArgs {
+  OrthoSizesArgs x;
+  RowScale row_scale, col_scale;   // of X's rows and columns
+  SplitMatrix rows, cols, floats;  // M x N and N x M; floats is one of the two
+  bool floats_turned;              // floats is N x M
 };
 hipError_t launch_ortho_split(const OrthoSplitArgs &p, bool bf16, int batch, hipStream_t s);
+
+// The largest magnitudes of the rows and columns of x, in floats: the larger of them and of
+// what rows and cols hold.
+constexpr int kLookRows = 512;
+hipError_t launch_ortho_look(const SplitMatrix &x, unsigned *rows, unsigned *cols, int batch,
+                             hipStream_t s);
 
 // D = f1 A B^T + f2 E, of A's rows by B's rows.
 struct OrthoProductArgs {
   SplitMatrix a, b;
-  SplitMatrix e_t;  // E transposed; at == null: none
+  RowScale a_scale, b_scale;
+  SplitMatrix e;  // E transposed, in floats; at == null: none
   float f1, f2;
-  SplitMatrix d, d_t;  // D as it is and transposed; at == null: not written
-  // The last product's D instead, in a user's type: element (m, n) at m ld + n, or
-  // at n ld + m.
+  SplitMatrix d, d_t;  // D as it is and transposed; d_t.at == null: not written
+  RowScale d_scale, d_t_scale;  // valid ones in any case
+  SplitMatrix f_t;  // D transposed, in floats; at == null: not written.  May be e
+  // The last product's D times alpha instead, in a user's type: element (m, n) at m ld +
+  // n, or at n ld + m.
   void *Y;
   long ldy, strideY;
   bool y_transposed;
+  float alpha;
 };
-// symmetric: D is symmetric, A and B the same, and one half of its tiles is
-// computed.
+// symmetric: D is symmetric, A and B the same, and one half of it is computed: of D
+// transposed in floats, and of E, that half is all there is.
 hipError_t launch_ortho_product(const OrthoProductArgs &p, bool symmetric, bool y_bf16, int batch,
                                 int cus, hipStream_t s);
+
+// The tile by times in microseconds, n the tiles for each of the chip's compute units,
+// nk slices.  Measured on 256 compute units (S = Z Z^T, or a Z + P Z; m x n of Z, tiles
+// of 64 x 64 / 128 x 128 / 128 x 256):
+//   S    1024 x 1024      10.0 / 18.8       2048 x 2048      45 / 41
+//        2600 x 2600      91 / 58           2048 x 4096      80 / 58
+//        16 of 512 x 512  17.5 / 16.1       1500 x 1500      22 / 26
+//   a Z + P Z
+//        1024 x 1024      13.3 / 22 / 34    2048 x 2048      64 / 54 / 69
+//        2600 x 2600      132 / 116 / 107   2048 x 4096      122 / 103 / 92
+//        16 of 512 x 512  28 / 24 / 29      1500 x 1500      36 / 32 / 47
+// A tile of 64 x 64 is bound by what the caches deliver, 85 bytes a nanosecond and
+// compute unit; larger ones by the matrix cores, at the power limit once the chip is
+// full (1.1 PFLOP/s of half precision, where a large library product has 1.3).
+enum class OrthoTile { k64, k128, k128x256 };
+inline OrthoTile ortho_tile(int rows_a, int rows_b, int cols, bool symmetric, int batch, int cus) {
+  const double nk = (cols + 31) / 32;
+  auto tiles = [&](int bm, int bn) {
+    const double tm = (rows_a + bm - 1) / bm, tn = (rows_b + bn - 1) / bn;
+    return batch * (symmetric ? tm * (tm + 1) / 2 : tm * tn) / cus;
+  };
+  const double n64 = tiles(64, 64), n128 = tiles(128, 128);
+  const double c64 = ceil(n64) * (0.2 * nk + 2);
+  if (symmetric) {
+    const double c128 = ceil(n128) * (0.38 * nk + 6 + 12 * fmin(n128, 1));
+    return c64 <= c128 ? OrthoTile::k64 : OrthoTile::k128;
+  }
+  const double c128 =
+      fmax(1, (ceil(n128) + n128) / 2) * ((0.38 + 0.22 * fmin(n128, 1)) * nk + 11);
+  const double n256 = tiles(128, 256);
+  const double c256 = ceil(n256) * (0.85 * nk + 12 + 50 * fmin(fmax(n256 - 0.6, 0), 0.4));
+  if (c64 <= c128 && c64 <= c256) return OrthoTile::k64;
+  return c128 <= c256 ? OrthoTile::k128 : OrthoTile::k128x256;
+}
 
 // Matrices of at most kShort rows (Z, m x n): a launch for Z and S's parts, then one for
 // each step (orthogonalize_short.hip).  A slab is `blocks` times 64 columns.
