@@ -271,9 +271,9 @@ __global__ void __launch_bounds__(256) ortho_sizes_kernel(OrthoSizesArgs p) {
         max(max(tops[0][i], tops[1][i]), max(tops[2][i], tops[3][i]));
 }
 
-// The largest of `count` numbers `step` apart.
+// The largest of `count` numbers `step` apart, of which kTogether are loaded together.
+template <int kTogether>
 __device__ __forceinline__ unsigned top_of(const unsigned *part, int count, long step) {
-  constexpr int kTogether = 8;
   unsigned top = 0;
   for (int k = 0; k < count; k += kTogether) {
     unsigned v[kTogether];
@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(256) ortho_scales_kernel(OrthoSizesArgs p) {
   const int i = ((int)blockIdx.x - (of_rows ? 0 : row_groups)) * 256 + (int)threadIdx.x;
   const int n = of_rows ? p.M : p.N, parts = of_rows ? p.runs : p.bands;
   const unsigned top =
-      top_of((of_rows ? p.row_parts : p.col_parts) + batch * parts * n + min(i, n - 1), parts, n);
+      top_of<32>((of_rows ? p.row_parts : p.col_parts) + batch * parts * n + min(i, n - 1), parts, n);
   const double scale = scale_of(p, batch);
   if (blockIdx.x == 0 && threadIdx.x == 0) p.scale[batch] = scale;
   if (i < n) keep_size(p, of_rows, batch, i, top, scale, true);
@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(256) ortho_split_kernel(OrthoSplitArgs p, Fast
     size = (of_rows ? x.rows + batch * x.M : x.cols + batch * x.N)[i];
   } else {
     const int parts = of_rows ? x.runs : x.bands, length = of_rows ? x.M : x.N;
-    const unsigned top = top_of(
+    const unsigned top = top_of<8>(
         (of_rows ? x.row_parts : x.col_parts) + batch * parts * length + i, parts, length);
     scale = scale_of(x, batch);
     size = keep_size(x, of_rows, batch, i, top, scale,
@@ -547,7 +547,7 @@ ortho_product_kernel(OrthoProductArgs p, TileMap map, FastDiv by_triangle, int t
         }
         wave_fence();
       }
-      if (p.Y) {
+      if (!SYMMETRIC && p.Y) {
         // Floats, as the user's rows run: 32 of them are 128 bytes too.
         const bool turned = p.y_transposed;
 #pragma unroll
