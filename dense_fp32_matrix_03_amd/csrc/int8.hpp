@@ -3,6 +3,7 @@
 #pragma once
 
 #include <hip/hip_runtime.h>
+#include <math.h>
 #include <stdint.h>
 
 #include "common.hpp"
@@ -56,6 +57,60 @@ bool int8_casts(const Int8Args &p, int cus);
 hipError_t launch_int8_product(const Int8Args &p, int a_type, bool c_bf16, int cus, hipStream_t s);
 // int8_tile.hip: tiles through LDS; A held.
 hipError_t launch_int8_tile(const Int8Args &p, bool c_bf16, int cus, hipStream_t s);
+
+// Rows spread thin over groups, in few work-groups (16 columns each; the host
+// counts a row of tiles for each group that can have rows).  With the cast first: 8
+// groups, 16 rows by 4096 x 4096 26 us (tiles of 64 x 64 35), 16 groups, 24 rows by 2048 x
+// 2048 14.7 (15.7); 8 groups, 64 rows by 4096 x 4096 41 (40), 64 groups, 512 rows by 1024
+// x 1024 27 (19).
+inline bool int8_spread_thin(const Int8Args &p, int cus) {
+  const long groups = p.groups < p.M ? p.groups : p.M;
+  return p.M <= 2L * p.groups && groups * ((p.N + 15L) / 16) <= 8L * cus;
+}
+
+// Up to 16 rows, and rows spread thin over groups, the kernel for few rows, but from 5
+// rows on tiles of 64 x 64 where they reach most of the compute units: 16 x 8192 x 8192
+// 22.9 us with it (tiles 24), 16 x 8192 x 2048 11.2 (12.3), 16 x 14336 x 4096 23.0 (16.3); 4 x 14336 x
+// 4096 19.2 (16.3, but 4 x 8192 x 8192 18.7, 24); 32 x 8192 x 8192 in two blocks of 16
+// rows 29.7 (24).
+inline bool int8_few_rows(const Int8Args &p, int cus) {
+  if (p.offsets) return int8_spread_thin(p, cus);
+  return p.M <= 4 || (p.M <= 16 && 4L * ((p.N + 63L) / 64) < 3L * cus);
+}
+
+// The tile by times in microseconds: rounds of tiles on the compute units, each with nk
+// slices of 128 k.  Groups count with their mean length: the host does not know more.
+// Measured on 256 compute units, A cast first (5 to 8 us of it) and C of bfloat16, tiles
+// of 64 x 64 / 128 x 128 / 128 x 256 / 256 x 256:
+//   N = K = 8192   M = 64   26 / 36 / 55 / 88     M = 256  43 / 45 / 61 / 98
+//                  M = 512  76 / 49 / 63 / 101    M = 1024 136 / 91 / 75 / 106
+//                  M = 2048 258 / 174 / 143 / 128
+//   8192 x 2048    M = 128  13 / 16 / 20 / 30     M = 1024 39 / 32 / 29 / 34
+// Stages of a 64 x 64 tile, 2 / 3 / 4: 64 x 8192 x 8192 49 / - / 26 us (two sets of waves
+// over k 37, four 32); in groups, where many tiles share a compute unit, 32 groups,
+// 48 rows by 4096 x 2048 48 / 43 / 44, 32 groups, 600 rows by 2048 x 2048 45 / 38 / 40, 64
+// groups, 512 rows by 1024 x 1024 19.0 / 21.6 / 20.9.  In groups, 64 x 64 and 128 x 128:
+// 64 groups, 4099 rows by 1000 x 777 29 and 36, 8 groups, 2000 rows by 4096 x 1024 30 and
+// 35, 16 groups, 8192 rows by 2048 x 2048 93 and 80.
+enum class Int8Tile { k64_2, k64_3, k64_4, k128, k128x256, k256 };  // 64 x 64: _stages
+inline Int8Tile int8_tile(const Int8Args &p, int cus) {
+  const long groups = !p.offsets ? 1 : p.groups < p.M ? p.groups : p.M;
+  const double mean = (double)p.M / groups, nk = (p.K + 127) / 128;
+  auto rounds = [&](long bm, long bn) {
+    const double rows = p.offsets ? fmax(1.0, mean / bm + 0.5) : ceil(mean / bm);
+    return ceil(groups * rows * ((p.N + bn - 1) / bn) / cus);
+  };
+  const double c64 = rounds(64, 64) * (0.22 * nk + 1.5) + 6;
+  const double c128 = rounds(128, 128) * (0.6 * nk + 2.5) + 6;
+  const double c128x256 = rounds(128, 256) * (nk + 3.5) + 6;
+  const double c256 = rounds(256, 256) * (1.55 * nk + 5) + 12;
+  const double large = fmin(c128x256, c256);
+  // Groups of unequal length leave larger tiles emptier.
+  if (p.offsets ? mean <= 96 || c64 <= 1.3 * fmin(c128, large) : c64 <= fmin(c128, large))
+    return !p.offsets ? Int8Tile::k64_4 : nk <= 8 ? Int8Tile::k64_2 : Int8Tile::k64_3;
+  if (c128 <= large) return Int8Tile::k128;
+  return c128x256 <= c256 ? Int8Tile::k128x256 : Int8Tile::k256;
+}
 
 typedef int i32x16 __attribute__((ext_vector_type(16)));
 

@@ -1,6 +1,6 @@
 // int8_rows.hip -- products of few rows, or few rows a group, with a matrix held in
-// 8-bit integers (include/sgemm_int8.h), and the choice between this kernel and the
-// tiles of int8_tile.hip.
+// 8-bit integers (include/sgemm_int8.h), and the launch of this kernel or of the tiles of
+// int8_tile.hip.
 //
 // C(m, n) = alpha sa(m) sb(n) sum_k a(m, k) b(n, k) + beta C(m, n), on
 // v_mfma_i32_16x16x64_i8: 16 rows of A by 16 rows of B over 64 k, lane quarter q
@@ -220,16 +220,6 @@ hipError_t launch_rows(const Int8Args &p, bool c_bf16, hipStream_t s) {
   return p.K > 1024 ? launch<8, TA, false>(p, c_bf16, s) : launch<4, TA, false>(p, c_bf16, s);
 }
 
-// Rows spread thin over groups, in few work-groups (16 columns each; the host
-// counts a row of tiles for each group that can have rows).  With the cast first: 8
-// groups, 16 rows by 4096 x 4096 26 us (tiles of 64 x 64 35), 16 groups, 24 rows by 2048 x
-// 2048 14.7 (15.7); 8 groups, 64 rows by 4096 x 4096 41 (40), 64 groups, 512 rows by 1024
-// x 1024 27 (19).
-bool spread_thin(const Int8Args &p, int cus) {
-  const long groups = p.groups < p.M ? p.groups : p.M;
-  return p.M <= 2L * p.groups && groups * ((p.N + 15L) / 16) <= 8L * cus;
-}
-
 }  // namespace
 
 // Casting a row in every work-group beats a launch of the cast while the values are few
@@ -240,21 +230,15 @@ bool spread_thin(const Int8Args &p, int cus) {
 bool int8_casts(const Int8Args &p, int cus) {
   if (p.K > 2048) return false;
   if (p.offsets)
-    return spread_thin(p, cus) && p.M <= p.groups && (long)p.M * p.K <= 16384;
+    return int8_spread_thin(p, cus) && p.M <= p.groups && (long)p.M * p.K <= 16384;
   return p.M <= 16 && (long)p.M * p.K <= 8192;
 }
 
-// Up to 16 rows, and rows spread thin over groups, this kernel, but from 5 rows on tiles
-// of 64 x 64 where they reach most of the compute units: 16 x 8192 x 8192 22.9 us here
-// (tiles 24), 16 x 8192 x 2048 11.2 (12.3), 16 x 14336 x 4096 23.0 (16.3); 4 x 14336 x
-// 4096 19.2 (16.3, but 4 x 8192 x 8192 18.7, 24); 32 x 8192 x 8192 in two blocks of 16
-// rows 29.7 (24).
 hipError_t launch_int8_product(const Int8Args &p, int a_type, bool c_bf16, int cus, hipStream_t s) {
   if (a_type == SGEMM_TYPE_F32) return launch_rows<SGEMM_TYPE_F32>(p, c_bf16, s);
   if (a_type == SGEMM_TYPE_BF16) return launch_rows<SGEMM_TYPE_BF16>(p, c_bf16, s);
-  const bool few = p.M <= 4 || (p.M <= 16 && 4L * ((p.N + 63L) / 64) < 3L * cus);
-  return (p.offsets ? spread_thin(p, cus) : few) ? launch_rows<SGEMM_TYPE_INT8>(p, c_bf16, s)
-                                                 : launch_int8_tile(p, c_bf16, cus, s);
+  return int8_few_rows(p, cus) ? launch_rows<SGEMM_TYPE_INT8>(p, c_bf16, s)
+                               : launch_int8_tile(p, c_bf16, cus, s);
 }
 
 }  // namespace sgemm

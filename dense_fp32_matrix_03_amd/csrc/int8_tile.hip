@@ -11,8 +11,6 @@
 // cast A: 430 us a product (2.55 POPS; a library product of 8-bit integers 465), the
 // matrix cores 68% busy at the clock that power leaves them, after 40 us for the cast of
 // A.  32 groups, 48 rows by 4096 x 2048: 37 us (5.2 TB/s of B's codes), and 5 for the cast.
-#include <math.h>
-
 #include "grouped_map.hpp"
 #include "int8.hpp"
 #include "slice_tile.hpp"
@@ -149,40 +147,15 @@ hipError_t launch(const Int8Args &p, bool c_bf16, hipStream_t s) {
 
 }  // namespace
 
-// The tile by times in microseconds: rounds of tiles on the compute units, each with nk
-// slices of 128 k.  Groups count with their mean length: the host does not know more.
-// Measured on 256 compute units, A cast first (5 to 8 us of it) and C of bfloat16, tiles
-// of 64 x 64 / 128 x 128 / 128 x 256 / 256 x 256:
-//   N = K = 8192   M = 64   26 / 36 / 55 / 88     M = 256  43 / 45 / 61 / 98
-//                  M = 512  76 / 49 / 63 / 101    M = 1024 136 / 91 / 75 / 106
-//                  M = 2048 258 / 174 / 143 / 128
-//   8192 x 2048    M = 128  13 / 16 / 20 / 30     M = 1024 39 / 32 / 29 / 34
-// Stages of a 64 x 64 tile, 2 / 3 / 4: 64 x 8192 x 8192 49 / - / 26 us (two sets of waves
-// over k 37, four 32); in groups, where many tiles share a compute unit, 32 groups,
-// 48 rows by 4096 x 2048 48 / 43 / 44, 32 groups, 600 rows by 2048 x 2048 45 / 38 / 40, 64
-// groups, 512 rows by 1024 x 1024 19.0 / 21.6 / 20.9.  In groups, 64 x 64 and 128 x 128:
-// 64 groups, 4099 rows by 1000 x 777 29 and 36, 8 groups, 2000 rows by 4096 x 1024 30 and
-// 35, 16 groups, 8192 rows by 2048 x 2048 93 and 80.
 hipError_t launch_int8_tile(const Int8Args &p, bool c_bf16, int cus, hipStream_t s) {
-  const long groups = !p.offsets ? 1 : p.groups < p.M ? p.groups : p.M;
-  const double mean = (double)p.M / groups, nk = (p.K + 127) / 128;
-  auto rounds = [&](long bm, long bn) {
-    const double rows = p.offsets ? fmax(1.0, mean / bm + 0.5) : ceil(mean / bm);
-    return ceil(groups * rows * ((p.N + bn - 1) / bn) / cus);
-  };
-  const double c64 = rounds(64, 64) * (0.22 * nk + 1.5) + 6;
-  const double c128 = rounds(128, 128) * (0.6 * nk + 2.5) + 6;
-  const double c128x256 = rounds(128, 256) * (nk + 3.5) + 6;
-  const double c256 = rounds(256, 256) * (1.55 * nk + 5) + 12;
-  const double large = fmin(c128x256, c256);
-  // Groups of unequal length leave larger tiles emptier.
-  if (p.offsets ? mean <= 96 || c64 <= 1.3 * fmin(c128, large) : c64 <= fmin(c128, large))
-    return !p.offsets ? launch<64, 64, 2, 2, 4>(p, c_bf16, s)
-           : nk <= 8  ? launch<64, 64, 2, 2, 2>(p, c_bf16, s)
-                      : launch<64, 64, 2, 2, 3>(p, c_bf16, s);
-  if (c128 <= large) return launch<128, 128, 2, 4, 4>(p, c_bf16, s);
-  return c128x256 <= c256 ? launch<128, 256, 2, 4, 3>(p, c_bf16, s)
-                          : launch<256, 256, 2, 4, 2>(p, c_bf16, s);
+  switch (int8_tile(p, cus)) {
+    case Int8Tile::k64_2: return launch<64, 64, 2, 2, 2>(p, c_bf16, s);
+    case Int8Tile::k64_3: return launch<64, 64, 2, 2, 3>(p, c_bf16, s);
+    case Int8Tile::k64_4: return launch<64, 64, 2, 2, 4>(p, c_bf16, s);
+    case Int8Tile::k128: return launch<128, 128, 2, 4, 4>(p, c_bf16, s);
+    case Int8Tile::k128x256: return launch<128, 256, 2, 4, 3>(p, c_bf16, s);
+    default: return launch<256, 256, 2, 4, 2>(p, c_bf16, s);
+  }
 }
 
 }  // namespace sgemm
