@@ -22,23 +22,25 @@ constexpr int64_t kMaxSteps = 64;
 // are parallel to large ones did not.  8 such steps are 2^14.3 of the 2^17 that a held
 // element may lie below its row's bound with all of its digits.
 constexpr int64_t kLookAgain = 8;
-constexpr int64_t kLooks = (kMaxSteps - 1) / kLookAgain;
 
 int64_t tiles(int64_t n, int64_t t) { return (n + t - 1) / t; }
 bool misaligned(const void *p, unsigned to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
 bool bad_type(int type) { return type != SGEMM_TYPE_F32 && type != SGEMM_TYPE_BF16; }
 unsigned size_of(int type) { return type == SGEMM_TYPE_F32 ? 4 : 2; }
 
-// The workspace: Z and Z transposed twice (a step reads one and writes the other), S and P
-// in pieces, Z transposed and S in floats; sizes of rows and columns, in parts, and then once for
-// each look at them.  Short matrices: the parts of the norms, and Z and the parts of S
-// twice.
+// The workspace: Z, P, Z transposed, S, Z transposed again (a step reads one and writes the
+// other).  The exponents of the rows' and columns' norms, twice (as Z is held, and as it was
+// last looked at), have an end of S's room, the one away from the transposed Z that the
+// step writes: S, until then, reaches into that, and the step's last launch moves the
+// exponents to the other end.  (All of S there, 16 of 256 x 256 took 10.2 us for 7.9.)
+// Before, the parts of the norms and sizes are in the second transposed Z.  Short matrices:
+// the parts of the norms, and Z and the parts of S twice.
 struct Layout {
   int m, n;
   int64_t z, zt, s;     // bytes of a matrix
   int64_t parts;        // of a norm
-  int64_t row_parts, col_parts, rows, cols;  // bytes of a matrix
   int64_t total;
+  int shared;           // 2^shared columns of Z share an exponent, so that there is room
   // Where m is short: Z and S's parts, twice each.
   bool is_short;
   int64_t short_z, short_parts;
@@ -48,23 +50,18 @@ struct Layout {
     z = sgemm::split_bytes(m, n);
     zt = sgemm::split_bytes(n, m);
     s = sgemm::split_bytes(m, m);
+    parts = tiles(M * tiles(N, sgemm::kNormRun), 16);
+    if (parts > sgemm::kNormParts) parts = sgemm::kNormParts;
     is_short = m <= sgemm::kShort;
-    if (is_short) {
-      parts = tiles(M * tiles(N, sgemm::kNormRun), 16);
-      if (parts > sgemm::kNormParts) parts = sgemm::kNormParts;
-    } else {
-      parts = (int64_t)sgemm::sizes_bands(M, N) * sgemm::sizes_runs(N);
-    }
-    row_parts = 4 * sgemm::sizes_runs(N) * M;
-    col_parts = 4 * sgemm::sizes_bands(M, N) * N;
-    rows = 4 * (1 + kLooks) * M;
-    cols = 4 * (1 + kLooks) * N;
+    shared = 0;
+    while (!is_short && 2 * norms(1) > s) ++shared;  // ends: 65 rows have 24960 bytes
     short_z = 4 * (int64_t)m * n;
     short_parts = 4 * (int64_t)m * m * sgemm::short_slabs(n);
-    total = batch * (8 * parts + (is_short ? 2 * (short_z + short_parts)
-                                           : 8 + z + 3 * zt + 3 * s + row_parts + col_parts + rows +
-                                                 cols));
+    total = batch * (8 * parts + (is_short ? 2 * (short_z + short_parts) : z + 2 * zt + 2 * s));
   }
+  int64_t columns() const { return (int64_t)((n - 1) >> shared) + 1; }
+  // Bytes of the exponents, and of the scale.
+  int64_t norms(int64_t batch) const { return tiles(batch * (8 + 2 * (m + columns())), 128) * 128; }
 };
 
 int check_sizes(int64_t batch, int64_t M, int64_t N) {
@@ -225,10 +222,33 @@ int sgemm_orthogonalize(int64_t batch, int64_t M, int64_t N, int64_t steps, int6
     const int64_t bytes = sgemm::split_bytes(rows, cols);
     return sgemm::SplitMatrix{take(bytes), rows, cols, bytes};
   };
-  const sgemm::SplitMatrix z = matrix(l.m, l.n), S = matrix(l.m, l.m), P = matrix(l.m, l.m);
-  sgemm::SplitMatrix zt[2] = {matrix(l.n, l.m), matrix(l.n, l.m)};
-  const sgemm::SplitMatrix z_floats = matrix(l.n, l.m), s_floats = matrix(l.m, l.m), none{nullptr, 0, 0, 0};
+  const sgemm::SplitMatrix z = matrix(l.m, l.n), P = matrix(l.m, l.m), zt0 = matrix(l.n, l.m),
+                           room = matrix(l.m, l.m), zt1 = matrix(l.n, l.m);
+  const sgemm::SplitMatrix zt[2] = {zt0, zt1}, none{nullptr, 0, 0, 0};
   const bool tall = M > N;
+  const int64_t norms = l.norms(batch);
+  // Where step k has the exponents.
+  auto norms_at = [&](int64_t k) { return k % 2 ? room.at + batch * l.s - norms : room.at; };
+
+  // Z's rows and columns by exponents of their norms: those of `set`, which are from when
+  // they were looked at last, and what the steps since can have made of them; and at most
+  // those of the whole matrix.
+  struct Range {
+    int set, grown, most;
+    Range with(int more) const { return {set, grown + more, most + more}; }
+  };
+  auto norms_of = [&](int64_t k, int set, bool rows) {
+    return reinterpret_cast<signed char *>(norms_at(k)) +
+           batch * (8 + set * (l.m + l.columns()) + (rows ? 0 : l.m));
+  };
+  auto scale_of = [&](int64_t k, const Range &x, bool rows) {
+    return sgemm::RowScale{norms_of(k, x.set, rows), rows ? l.m : (int)l.columns(),
+                           rows ? 0 : l.shared, x.grown, x.most};
+  };
+  int set = 0;
+  double growth = 1;
+  auto range = [&](int64_t k) { return Range{set, exponent_of(growth), exponent_of(bound[k])}; };
+  Range held = range(0);  // Z, as it is held
 
   sgemm::OrthoSizesArgs in;
   in.M = (int)M;
@@ -240,40 +260,24 @@ int sgemm_orthogonalize(int64_t batch, int64_t M, int64_t N, int64_t steps, int6
   in.band = sgemm::sizes_band(M, N);
   in.bands = sgemm::sizes_bands(M, N);
   in.runs = sgemm::sizes_runs(N);
-  in.summed = in.bands + in.runs > sgemm::kMostSizeParts;
-  in.parts = reinterpret_cast<double *>(take(8 * l.parts));
-  in.scale = reinterpret_cast<double *>(take(8));
-  in.row_parts = reinterpret_cast<unsigned *>(take(l.row_parts));
-  in.col_parts = reinterpret_cast<unsigned *>(take(l.col_parts));
-  in.rows = reinterpret_cast<unsigned *>(take(l.rows));
-  in.cols = reinterpret_cast<unsigned *>(take(l.cols));
-  in.again = (int)((steps - 1) / kLookAgain);
+  in.parts = reinterpret_cast<double *>(zt1.at);
+  in.row_parts = reinterpret_cast<unsigned *>(in.parts + batch * in.bands * in.runs);
+  in.col_parts = in.row_parts + batch * in.runs * M;
+  in.summed = l.shared > 0 || in.bands + in.runs > sgemm::kMostSizeParts;
+  in.scale = reinterpret_cast<double *>(norms_at(0));
+  in.rows = norms_of(0, 0, !tall);
+  in.cols = norms_of(0, 0, tall);
+  in.row_shift = tall ? l.shared : 0;
+  in.col_shift = tall ? 0 : l.shared;
+  in.row_length = exponent_of(sqrt((double)N));
+  in.col_length = exponent_of(sqrt((double)M));
   const bool x_bf16 = typeX == SGEMM_TYPE_BF16, y_bf16 = typeY == SGEMM_TYPE_BF16;
-
-  // Z's rows and columns: their largest magnitudes when they were last looked at, `look`,
-  // times the root of their length bound their norms (2^of_rows, 2^of_cols times the power
-  // of two above the magnitude), and `growth` what these have become since.
-  unsigned *const tops_m = tall ? in.cols : in.rows, *const tops_n = tall ? in.rows : in.cols;
-  const int of_rows = exponent_of(sqrt((double)l.n)), of_cols = exponent_of(sqrt((double)l.m));
-  int look = 0;
-  double growth = 1;
-  // The scale of Z's rows (or columns) before step k, and of what is as much larger as
-  // 2^more.
-  auto scale_of = [&](bool rows, int64_t k, int more) {
-    const int add = (rows ? of_rows : of_cols) + exponent_of(growth) - 126 + more;
-    return sgemm::RowScale{
-        rows ? tops_m + look * batch * l.m : tops_n + look * batch * l.n, add,
-        exponent_of(bound[k]) + more};
-  };
   sgemm::OrthoSplitArgs split;
   split.x = in;
-  sgemm::RowScale z_scale = scale_of(true, 0, 0), zt_scale = scale_of(false, 0, 0);  // as held
-  split.row_scale = tall ? zt_scale : z_scale;
-  split.col_scale = tall ? z_scale : zt_scale;
-  split.rows = tall ? zt[0] : z;
-  split.cols = tall ? z : zt[0];
-  split.floats = z_floats;
-  split.floats_turned = !tall;
+  split.row_scale = scale_of(0, held, !tall);
+  split.col_scale = scale_of(0, held, tall);
+  split.rows = tall ? zt0 : z;
+  split.cols = tall ? z : zt0;
   hipError_t err = sgemm::launch_ortho_sizes(in, x_bf16, (int)batch, s);
   if (err == hipSuccess) err = sgemm::launch_ortho_split(split, x_bf16, (int)batch, s);
   for (int64_t k = 0; k < steps && err == hipSuccess; ++k) {
@@ -284,34 +288,33 @@ int sgemm_orthogonalize(int64_t batch, int64_t M, int64_t N, int64_t steps, int6
     const int more_s = exponent_of(bound[k]);
     const int more_p = exponent_of(bound[k] * (fabs(c[1]) + fabs(c[2]) * top));
     const bool last = k + 1 == steps;
+    const sgemm::SplitMatrix S{k % 2 ? room.at - norms : room.at + norms, l.m, l.m, l.s};
     sgemm::OrthoProductArgs p{};
-    p.e = p.d_t = p.f_t = none;
+    p.e = p.e_t = p.d_t = none;
     // S = Z Z^T
     p.a = p.b = z;
-    p.a_scale = p.b_scale = z_scale;
+    p.a_scale = p.b_scale = p.e_scale = scale_of(k, held, true);
     p.f1 = 1.f;
     p.d = S;
-    p.d_scale = p.d_t_scale = scale_of(true, k, more_s);
-    p.f_t = s_floats;
+    p.d_scale = p.d_t_scale = scale_of(k, range(k).with(more_s), true);
     err = sgemm::launch_ortho_product(p, true, false, (int)batch, cus, s);
     if (err != hipSuccess) break;
     // P = b S + c S S
-    p.a = p.b = S;
-    p.a_scale = p.b_scale = p.d_scale;
-    p.e = s_floats;
-    p.f_t = none;
+    p.a = p.b = p.e = p.e_t = S;
+    p.a_scale = p.b_scale = p.e_scale = p.d_scale;
     p.f1 = c[2];
     p.f2 = c[1];
     p.d = P;
-    p.d_scale = p.d_t_scale = scale_of(true, k, more_p);
+    p.d_scale = p.d_t_scale = scale_of(k, range(k).with(more_p), true);
     err = sgemm::launch_ortho_product(p, true, false, (int)batch, cus, s);
     if (err != hipSuccess) break;
     // a Z + P Z
     p.a = P;
-    p.b = zt[k % 2];
+    p.b = p.e_t = zt[k % 2];
+    p.e = z;
     p.a_scale = p.d_scale;
-    p.b_scale = zt_scale;
-    p.e = z_floats;
+    p.b_scale = scale_of(k, held, false);
+    p.e_scale = scale_of(k, held, true);
     p.f1 = 1.f;
     p.f2 = c[0];
     if (last) {
@@ -324,20 +327,31 @@ int sgemm_orthogonalize(int64_t batch, int64_t M, int64_t N, int64_t steps, int6
       p.alpha = alpha;
     } else {
       growth = fmin(growth * 1.001 * largest_growth(c[0], c[1], c[2], top), 1e300);
+      held = range(k + 1);
       p.d = z;
-      p.d_scale = scale_of(true, k + 1, 0);
+      p.d_scale = scale_of(k, held, true);
       p.d_t = zt[1 - k % 2];
-      p.d_t_scale = scale_of(false, k + 1, 0);
-      p.f_t = z_floats;
+      p.d_t_scale = scale_of(k, held, false);
+      p.move_from = norms_at(k);
+      p.move_to = norms_at(k + 1);
+      p.moves = (unsigned)(norms / 16);  // below 2^27
     }
     err = sgemm::launch_ortho_product(p, false, y_bf16, (int)batch, cus, s);
-    z_scale = p.d_scale;
-    zt_scale = p.d_t_scale;
     if (!last && (k + 1) % kLookAgain == 0 && err == hipSuccess) {
-      ++look;
+      set = 1 - set;
       growth = 1;
-      err = sgemm::launch_ortho_look(z_floats, tops_n + look * batch * l.n,
-                                     tops_m + look * batch * l.m, (int)batch, s);
+      sgemm::OrthoSizesArgs again{};
+      again.M = l.m;
+      again.N = l.n;
+      again.bands = again.runs = 1;
+      again.row_parts = reinterpret_cast<unsigned *>(zt[k % 2].at);
+      again.col_parts = again.row_parts + batch * l.m;
+      again.rows = norms_of(k + 1, set, true);
+      again.cols = norms_of(k + 1, set, false);
+      again.col_shift = l.shared;
+      again.row_length = exponent_of(sqrt((double)l.n));
+      again.col_length = exponent_of(sqrt((double)l.m));
+      err = sgemm::launch_ortho_look(again, z, scale_of(k + 1, held, true), (int)batch, s);
     }
   }
   return err == hipSuccess ? SGEMM_OK : SGEMM_ERR_LAUNCH;

@@ -134,6 +134,17 @@ struct BlockImage {
   }
 };
 
+// The largest of a half of the lanes, in its last one, by moves inside rows of 16 and from
+// row to row.
+__device__ __forceinline__ int half_wave_max(int v) {
+  constexpr int least = -(1 << 30);
+  v = max(v, __builtin_amdgcn_update_dpp(least, v, 0x111, 0xf, 0xf, false));  // 1 lane before
+  v = max(v, __builtin_amdgcn_update_dpp(least, v, 0x112, 0xf, 0xf, false));  // 2
+  v = max(v, __builtin_amdgcn_update_dpp(least, v, 0x114, 0xf, 0xf, false));  // 4
+  v = max(v, __builtin_amdgcn_update_dpp(least, v, 0x118, 0xf, 0xf, false));  // 8
+  return max(v, __builtin_amdgcn_update_dpp(least, v, 0x142, 0xa, 0xf, false));  // the row before's
+}
+
 // 2^x.
 __device__ __forceinline__ float power_of_two(int x) {
   return __uint_as_float((unsigned)(min(max(x, -126), 127) + 127) << 23);
@@ -142,7 +153,8 @@ __device__ __forceinline__ float power_of_two(int x) {
 // One of two for each lane, out of scalar registers: a reference to one or the other would
 // read the kernel's arguments through memory.
 __device__ __forceinline__ RowScale either(bool first, const RowScale a, const RowScale b) {
-  return {first ? a.top : b.top, first ? a.add : b.add, first ? a.cap : b.cap};
+  return {first ? a.norm : b.norm, first ? a.count : b.count, first ? a.shift : b.shift,
+          first ? a.add : b.add, first ? a.cap : b.cap};
 }
 
 // The pieces of a block of sums (as the matrix instructions leave them) times `scale` of
@@ -294,33 +306,74 @@ __device__ __forceinline__ double scale_of(const OrthoSizesArgs &p, long batch) 
   return norm > 0 ? 1.0 / norm : norm;  // NaN stays
 }
 
-// Row (or column) i's size, now that the scale is known, to where the products find it.
-__device__ __forceinline__ unsigned keep_size(const OrthoSizesArgs &p, bool of_rows, long batch,
-                                              int i, unsigned top, double scale, bool write) {
-  const long n = of_rows ? p.M : p.N;
-  const unsigned size =
-      __float_as_uint((float)(scale * (double)__uint_as_float(top))) & 0x7fffffffu;
-  if (write) {
-    unsigned *const to = (of_rows ? p.rows : p.cols) + batch * n + i;
-    *to = size;
-    for (int k = 1; k <= p.again; ++k) to[k * gridDim.y * n] = 0;
-  }
-  return size;
+__device__ __forceinline__ signed char scaled_exponent(unsigned top, double scale, int length) {
+  const float size = (float)(scale * (double)__uint_as_float(top));
+  return norm_exponent(__float_as_uint(size) & 0x7fffffffu, length);
 }
 
 // For very long rows or columns, whose sizes are in so many parts that each block of the
-// next launch would not add them up for itself: a thread has a row or a column.
+// next launch would not add them up for itself: a thread has a row or a column, or
+// the 2^shift that share an exponent.
 __global__ void __launch_bounds__(256) ortho_scales_kernel(OrthoSizesArgs p) {
   const long batch = blockIdx.y;
-  const int row_groups = (p.M + 255) / 256;
+  const int row_count = ((p.M - 1) >> p.row_shift) + 1, col_count = ((p.N - 1) >> p.col_shift) + 1;
+  const int row_groups = (row_count + 255) / 256;
   const bool of_rows = (int)blockIdx.x < row_groups;
   const int i = ((int)blockIdx.x - (of_rows ? 0 : row_groups)) * 256 + (int)threadIdx.x;
+  const int count = of_rows ? row_count : col_count, shift = of_rows ? p.row_shift : p.col_shift;
   const int n = of_rows ? p.M : p.N, parts = of_rows ? p.runs : p.bands;
-  const unsigned top =
-      top_of<32>((of_rows ? p.row_parts : p.col_parts) + batch * parts * n + min(i, n - 1), parts, n);
-  const double scale = scale_of(p, batch);
-  if (blockIdx.x == 0 && threadIdx.x == 0) p.scale[batch] = scale;
-  if (i < n) keep_size(p, of_rows, batch, i, top, scale, true);
+  const unsigned *const from = (of_rows ? p.row_parts : p.col_parts) + batch * parts * n;
+  unsigned top = 0;
+  for (int k = 0; k < 1 << shift; ++k)
+    top = max(top, top_of<32>(from + min((min(i, count - 1) << shift) + k, n - 1), parts, n));
+  const double scale = p.scale ? scale_of(p, batch) : 1.0;
+  if (p.scale && blockIdx.x == 0 && threadIdx.x == 0) p.scale[batch] = scale;
+  if (i < count)
+    (of_rows ? p.rows : p.cols)[batch * count + i] =
+        scaled_exponent(top, scale, of_rows ? p.row_length : p.col_length);
+}
+
+__global__ void __launch_bounds__(256) ortho_clear_kernel(unsigned *at, long n) {
+  const long i = (long)blockIdx.x * 256 + threadIdx.x;
+  if (i < n) at[i] = 0;
+}
+
+// The largest magnitudes of the rows and columns of a held matrix, into zeros: 4 lanes have
+// 32 columns of a row, a work-group kLookRows rows, 64 at a time.
+constexpr int kLookRows = 512;
+__global__ void __launch_bounds__(256) ortho_look_kernel(SplitMatrix z, RowScale by, unsigned *rows,
+                                                         unsigned *cols) {
+  const int lane = threadIdx.x % kWave, part = threadIdx.x % 4;
+  const int c0 = blockIdx.y * 32, first = (int)blockIdx.x * kLookRows;
+  const long batch = blockIdx.z;
+  float top[8];  // of the lane's columns
+#pragma unroll
+  for (int e = 0; e < 8; ++e) top[e] = 0.f;
+  for (int r0 = first; r0 < min(first + kLookRows, z.rows); r0 += 64) {
+    const int r = r0 + (int)threadIdx.x / 4;
+    float most = 0.f;
+    if (r < z.rows) {
+      const f16x8 high =
+          *reinterpret_cast<const f16x8 *>(z.place(blockIdx.z, r, c0) + part * 16);
+      const float scale = power_of_two(by.exponent(by.norm[by.index(batch, r)]) - kHeldTop);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float size = fabsf((float)high[e]) * scale;
+        top[e] = fmaxf(top[e], size);
+        most = fmaxf(most, size);
+      }
+    }
+    most = fmaxf(most, __shfl_xor(most, 1));
+    most = fmaxf(most, __shfl_xor(most, 2));
+    if (r < z.rows && part == 0) atomicMax(rows + batch * z.rows + r, __float_as_uint(most));
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+#pragma unroll
+    for (int d = 32; d > 2; d /= 2) top[e] = fmaxf(top[e], __shfl_xor(top[e], d));
+    const int c = c0 + part * 8 + e;
+    if (lane < 4 && c < z.cols) atomicMax(cols + batch * z.cols + c, __float_as_uint(top[e]));
+  }
 }
 
 // A block of 32 x 32 per wave, in the layout of the matrix instructions' results: lane
@@ -343,26 +396,28 @@ __global__ void __launch_bounds__(256) ortho_split_kernel(OrthoSplitArgs p, Fast
     const int m = min(bm + acc32_row(lane, e), x.M - 1);
     v[e] = load1<BF16>(x.X, batch * x.strideX + m * x.ldx + n);
   }
-  // A lane has the size of a row, or of a column.
+  // A lane has the exponent of a row, or of a column.
   const bool of_rows = half == 0;
+  const RowScale by = either(of_rows, p.row_scale, p.col_scale);
   const int i = of_rows ? min(bm + r32, x.M - 1) : n;
   double scale;
-  unsigned size;
+  int norm;
   if (x.summed) {
     scale = x.scale[batch];
-    size = (of_rows ? x.rows + batch * x.M : x.cols + batch * x.N)[i];
+    norm = by.norm[by.index(batch, i)];
   } else {
     const int parts = of_rows ? x.runs : x.bands, length = of_rows ? x.M : x.N;
     const unsigned top = top_of<8>(
         (of_rows ? x.row_parts : x.col_parts) + batch * parts * length + i, parts, length);
     scale = scale_of(x, batch);
-    size = keep_size(x, of_rows, batch, i, top, scale,
-                     of_rows ? bn == 0 && bm + r32 < x.M : bm == 0 && bn + r32 < x.N);
+    const signed char e = scaled_exponent(top, scale, of_rows ? x.row_length : x.col_length);
+    if (of_rows ? bn == 0 && bm + r32 < x.M : bm == 0 && bn + r32 < x.N)
+      (of_rows ? x.rows : x.cols)[batch * length + i] = e;
+    norm = e;
   }
   if (bm >= x.M) return;  // whole waves: no barrier follows
-  const RowScale by = either(of_rows, p.row_scale, p.col_scale);
   __shared__ __attribute__((aligned(16))) float scales[4][2][32];
-  scales[wave][half][r32] = power_of_two(kHeldTop - by.exponent(size));
+  scales[wave][half][r32] = power_of_two(kHeldTop - by.exponent(norm));
   wave_fence();
   float row_scale[16];
 #pragma unroll
@@ -377,53 +432,12 @@ __global__ void __launch_bounds__(256) ortho_split_kernel(OrthoSplitArgs p, Fast
     v[e] = in ? (float)(scale * (double)v[e]) : 0.f;
   }
   __shared__ __attribute__((aligned(16))) char images[4][2][4096];
-  const BlockImage rows{images[wave][0]}, cols{images[wave][1]}, &floats = rows;
+  const BlockImage rows{images[wave][0]}, cols{images[wave][1]};
   split_block(v, row_scale, r32, half, rows);
   split_transposed(v, scales[wave][1][r32], r32, half, cols);
   wave_fence();
   store_block(p.rows, blockIdx.y, bm, bn, x.M, lane, rows);
   store_block(p.cols, blockIdx.y, bn, bm, x.N, lane, cols);
-  wave_fence();
-  floats_block(v, p.floats_turned, r32, half, floats);
-  wave_fence();
-  if (p.floats_turned)
-    store_block(p.floats, blockIdx.y, bn, bm, x.N, lane, floats);
-  else
-    store_block(p.floats, blockIdx.y, bm, bn, x.M, lane, floats);
-}
-
-// The largest magnitudes of the rows and columns of a matrix of floats: 8 lanes have a row
-// of 32 columns, a work-group 32 such rows at a time.
-__global__ void __launch_bounds__(256) ortho_look_kernel(SplitMatrix x, unsigned *rows,
-                                                         unsigned *cols) {
-  const int lane = threadIdx.x % kWave, part = threadIdx.x % 8;
-  const long batch = blockIdx.z;
-  const int c0 = blockIdx.y * 32;
-  unsigned top[4] = {0, 0, 0, 0};  // of the lane's columns
-  for (int r0 = blockIdx.x * kLookRows; r0 < min((int)(blockIdx.x + 1) * kLookRows, x.rows); r0 += 32) {
-    const int r = r0 + (int)threadIdx.x / 8;
-    unsigned most = 0;
-    if (r < x.rows) {
-      const slice_i32x4 v =
-          *reinterpret_cast<const slice_i32x4 *>(x.place(blockIdx.z, r, c0) + part * 16);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const unsigned size = (unsigned)v[e] & 0x7fffffffu;
-        top[e] = max(top[e], size);
-        most = max(most, size);
-      }
-    }
-#pragma unroll
-    for (int d = 4; d > 0; d /= 2) most = max(most, (unsigned)__shfl_xor((int)most, d));
-    if (r < x.rows && part == 0) atomicMax(rows + batch * x.rows + r, most);
-  }
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-#pragma unroll
-    for (int d = 32; d > 4; d /= 2) top[e] = max(top[e], (unsigned)__shfl_xor((int)top[e], d));
-    const int c = c0 + part * 4 + e;
-    if (lane < 8 && c < x.cols) atomicMax(cols + batch * x.cols + c, top[e]);
-  }
 }
 
 // Position `id` of the tiles on and below a diagonal, row by row: row t has t + 1.
@@ -463,46 +477,56 @@ ortho_product_kernel(OrthoProductArgs p, TileMap map, FastDiv by_triangle, int t
   // Blocks of E^T go out before the sums' operands; rows past N are zeros, and a row's
   // columns up to the next 32 are there.
   slice_i32x4 e_t[FM][FN][4];
-  auto load_e = [&](bool whole) {
+  const bool whole = mw + 32 * FM <= M && nw + 32 * FN <= N;
+  auto load_e = [&](const SplitMatrix &x, int r0, int c, int k) {
+    const int r = r0 + 8 * k + lane / 8;
+    const auto *at = reinterpret_cast<const slice_i32x4 *>(x.place(batch, r, c) + lane % 8 * 16);
+    if (whole) return *at;
+    return r < x.rows && c < x.cols ? *at : slice_i32x4{0, 0, 0, 0};
+  };
+  if (p.e.at) {
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
       for (int j = 0; j < FN; ++j)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int n = nw + j * 32 + 8 * k + lane / 8, m = mw + i * 32;
-          const auto *at =
-              reinterpret_cast<const slice_i32x4 *>(p.e.place(batch, n, m) + lane % 8 * 16);
-          if (whole)
-            e_t[i][j][k] = *at;
-          else
-            e_t[i][j][k] = n < N && m < M ? *at : slice_i32x4{0, 0, 0, 0};
-        }
-  };
-  if (p.e.at) load_e(mw + 32 * FM <= M && nw + 32 * FN <= N);
+        for (int k = 0; k < 4; ++k) e_t[i][j][k] = load_e(p.e_t, nw + j * 32, mw + i * 32, k);
+  }
 
   auto rows = [&](const SplitMatrix &x, int first, int n) {
     return SliceRows{x.place(batch, first, 0), kSliceRow, (long)x.rows * kSliceRow, n};
   };
-  // A thread has a row of A or of B: the sizes that its scales go by are loaded here, and
-  // waited for after the sums.
+  // A thread has a row of A or of B: the norms that its scales go by are loaded here, and
+  // waited for while the first slices come.  The threads there are more do the same, for
+  // nothing: behind a test the compiler would load them there, after the slices.
   static_assert(BM + BN <= Tile::kThreads, "a thread for each row");
   const bool of_a = threadIdx.x < BM;
-  const long at = of_a ? (long)batch * M + min(m0 + (int)threadIdx.x, M - 1)
-                       : (long)batch * N + min(n0 + (int)threadIdx.x - BM, N - 1);
-  const RowScale from = either(of_a, p.a_scale, p.b_scale), to = either(of_a, p.d_scale, p.d_t_scale);
-  const unsigned top_in = from.top[at], top_out = to.top[at];
+  const int own = of_a ? min(m0 + (int)threadIdx.x, M - 1) : min(n0 + (int)threadIdx.x - BM, N - 1);
+  const RowScale from = either(of_a, p.a_scale, p.b_scale), to = either(of_a, p.d_scale, p.d_t_scale),
+                 of_e = either(of_a, p.e_scale, p.b_scale);
+  auto norm_of = [&](const RowScale &x) -> int {
+    return x.norm[x.index(batch, own)];
+  };
+  const int norm_in = norm_of(from), norm_out = norm_of(to), norm_e = norm_of(of_e);
 
+  // What a row's and a column's sums are multiplied by, and the powers of two under which
+  // the results, and E's rows, are held; and of every 32 rows the least exponent of E's,
+  // negative, of every 32 columns the largest.
+  __shared__ __attribute__((aligned(16))) float in_scales[Tile::kThreads],
+      out_scales[Tile::kThreads], e_scales[Tile::kThreads];
+  __shared__ int ranges[Tile::kThreads / 32];
+  auto keep_scales = [&] {
+    const int e = of_e.exponent(norm_e);
+    in_scales[threadIdx.x] = power_of_two(from.exponent(norm_in) - kHeldTop) * (of_a ? p.f1 : 1.f);
+    out_scales[threadIdx.x] = power_of_two(kHeldTop - to.exponent(norm_out));
+    e_scales[threadIdx.x] = power_of_two(e - kHeldTop);
+    const int top = half_wave_max(of_a ? -e : e);
+    if (r32 == 31) ranges[threadIdx.x / 32] = top;
+  };
   f32x16 acc[FM][FN];
   char *lds[NST];
-  Tile::run(rows(p.a, m0, rows_a), rows(p.b, n0, rows_b), (p.a.cols + 31) / 32, acc, lds);
-  // What a row's and a column's sums are multiplied by, and the powers of two under which
-  // the results are held.
-  __shared__ __attribute__((aligned(16))) float in_scales[BM + BN], out_scales[BM + BN];
-  if (threadIdx.x < BM + BN) {
-    in_scales[threadIdx.x] = power_of_two(from.exponent(top_in) - kHeldTop) * (of_a ? p.f1 : 1.f);
-    out_scales[threadIdx.x] = power_of_two(kHeldTop - to.exponent(top_out));
-  }
+  Tile::run(rows(p.a, m0, rows_a), rows(p.b, n0, rows_b), (p.a.cols + 31) / 32, acc, lds,
+            keep_scales);
   __syncthreads();  // no loads into the stages are left, of any wave
   const int wave = Tile::wave_id();
   const BlockImage e_image{lds[0] + wave * 4096}, t_image{lds[1] + wave * 4096},
@@ -536,17 +560,41 @@ ortho_product_kernel(OrthoProductArgs p, TileMap map, FastDiv by_triangle, int t
         }
       }
       if (p.e.at) {
+        // By columns, where none of them has a range 2^8 times that of a row: what is held to
+        // 2^-40 of its column is then held to 2^-32 of its row too.
+        const bool by_rows = __builtin_amdgcn_readfirstlane(
+            ranges[Tile::row0() / 32 + i] + ranges[(BM + Tile::col0()) / 32 + j] > 8);
 #pragma unroll
         for (int k = 0; k < 4; ++k) *e_image.linear(lane, k) = e_t[i][j][k];
+        if (by_rows) {
+#pragma unroll 1  // rarely: no registers are spent on it
+          for (int k = 0; k < 4; ++k) *t_image.linear(lane, k) = load_e(p.e, mb, nb, k);
+        }
         wave_fence();
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const f32x4 e4 = *reinterpret_cast<const f32x4 *>(e_image.chunk(r32, 2 * q + half));
+          const f16x4 high = *reinterpret_cast<const f16x4 *>(e_image.chunk(r32, q) + 8 * half);
+          const f16x4 low = *reinterpret_cast<const f16x4 *>(e_image.chunk(r32, 4 + q) + 8 * half);
+          f32x4 value;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) v[4 * q + e] = fmaf(p.f2, e4[e], v[4 * q + e]);
+          for (int e = 0; e < 4; ++e) value[e] = ((float)high[e] + (float)low[e]) * scale_b;
+          if (by_rows) {
+            const int m = 8 * q + 4 * half;
+            const f32x4 scale_e =
+                *reinterpret_cast<const f32x4 *>(e_scales + Tile::row0() + i * 32 + m);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const auto piece = [&](int c) {
+                return (float)reinterpret_cast<_Float16 *>(t_image.chunk(m + e, c + r32 / 8))[r32 % 8];
+              };
+              if (scale_e[e] < scale_b) value[e] = (piece(0) + piece(4)) * scale_e[e];
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[4 * q + e] = fmaf(p.f2, value[e], v[4 * q + e]);
         }
-        wave_fence();
       }
+      wave_fence();
       if (!SYMMETRIC && p.Y) {
         // Floats, as the user's rows run: 32 of them are 128 bytes too.
         const bool turned = p.y_transposed;
@@ -583,15 +631,17 @@ ortho_product_kernel(OrthoProductArgs p, TileMap map, FastDiv by_triangle, int t
       }
       split_block(v, scale_out, r32, half, d_image);
       if (mirror) split_transposed(v, out_scales[of_b], r32, half, t_image);
-      if (p.f_t.at) floats_block(v, true, r32, half, e_image);
       wave_fence();
       // Rows of a result are written up to the end of their last 32 columns: past
       // its own columns the sums are 0.
       store_block(p.d, batch, mb, nb, M, lane, d_image);
       if (mirror) store_block(t, batch, nb, mb, N, lane, t_image);
-      if (p.f_t.at) store_block(p.f_t, batch, nb, mb, N, lane, e_image);
       wave_fence();
     }
+  for (unsigned at = blockIdx.x * Tile::kThreads + threadIdx.x; at < p.moves;
+       at += gridDim.x * Tile::kThreads)
+    reinterpret_cast<slice_i32x4 *>(p.move_to)[at] =
+        reinterpret_cast<const slice_i32x4 *>(p.move_from)[at];
 }
 
 template <int BM, int BN, int WM, int WN, int NST>
@@ -626,6 +676,17 @@ hipError_t launch_ortho_norm(const OrthoNormArgs &p, bool bf16, int batch, hipSt
   return hipGetLastError();
 }
 
+namespace {
+
+hipError_t launch_scales(const OrthoSizesArgs &p, int batch, hipStream_t s) {
+  const int rows = ((p.M - 1) >> p.row_shift) + 1, cols = ((p.N - 1) >> p.col_shift) + 1;
+  const dim3 grid((unsigned)((rows + 255) / 256 + (cols + 255) / 256), (unsigned)batch);
+  hipLaunchKernelGGL(ortho_scales_kernel, grid, dim3(256), 0, s, p);
+  return hipGetLastError();
+}
+
+}  // namespace
+
 hipError_t launch_ortho_sizes(const OrthoSizesArgs &p, bool bf16, int batch, hipStream_t s) {
   const dim3 block(256), grid((unsigned)((long)p.bands * p.runs), (unsigned)batch);
   if (bf16)
@@ -633,10 +694,21 @@ hipError_t launch_ortho_sizes(const OrthoSizesArgs &p, bool bf16, int batch, hip
   else
     hipLaunchKernelGGL(ortho_sizes_kernel<false>, grid, block, 0, s, p);
   const hipError_t err = hipGetLastError();
-  if (err != hipSuccess || !p.summed) return err;
-  const dim3 all((unsigned)((p.M + 255) / 256 + (p.N + 255) / 256), (unsigned)batch);
-  hipLaunchKernelGGL(ortho_scales_kernel, all, block, 0, s, p);
-  return hipGetLastError();
+  return err != hipSuccess || !p.summed ? err : launch_scales(p, batch, s);
+}
+
+hipError_t launch_ortho_look(const OrthoSizesArgs &p, const SplitMatrix &z, const RowScale &z_scale,
+                             int batch, hipStream_t s) {
+  const long tops = (long)batch * (p.M + p.N);
+  hipLaunchKernelGGL(ortho_clear_kernel, dim3((unsigned)((tops + 255) / 256)), dim3(256), 0, s,
+                     p.row_parts, tops);
+  hipError_t err = hipGetLastError();
+  if (err != hipSuccess) return err;
+  const dim3 grid((unsigned)((z.rows + kLookRows - 1) / kLookRows), (unsigned)((z.cols + 31) / 32),
+                  (unsigned)batch);
+  hipLaunchKernelGGL(ortho_look_kernel, grid, dim3(256), 0, s, z, z_scale, p.row_parts, p.col_parts);
+  err = hipGetLastError();
+  return err != hipSuccess ? err : launch_scales(p, batch, s);
 }
 
 hipError_t launch_ortho_split(const OrthoSplitArgs &p, bool bf16, int batch, hipStream_t s) {
@@ -647,15 +719,6 @@ hipError_t launch_ortho_split(const OrthoSplitArgs &p, bool bf16, int batch, hip
     hipLaunchKernelGGL(ortho_split_kernel<true>, grid, block, 0, s, p, by_across);
   else
     hipLaunchKernelGGL(ortho_split_kernel<false>, grid, block, 0, s, p, by_across);
-  return hipGetLastError();
-}
-
-hipError_t launch_ortho_look(const SplitMatrix &x, unsigned *rows, unsigned *cols, int batch,
-                             hipStream_t s) {
-  // The third dimension of a launch ends at 65535, as a batch does.
-  const dim3 grid((unsigned)((x.rows + kLookRows - 1) / kLookRows), (unsigned)((x.cols + 31) / 32),
-                  (unsigned)batch);
-  hipLaunchKernelGGL(ortho_look_kernel, grid, dim3(256), 0, s, x, rows, cols);
   return hipGetLastError();
 }
 

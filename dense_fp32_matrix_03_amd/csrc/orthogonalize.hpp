@@ -10,15 +10,14 @@
 
 namespace sgemm {
 
-// A batch of matrices in blocks of 128 bytes, [cols / 32][rows], the last columns padded
-// with zeros.  In pieces: 32 high pieces of a row and then 32 low ones, a value being
-// (high + low) 2^(e - kHeldTop) with the row's e (RowScale).  Or 32 floats.
+// A batch of matrices in pieces: [cols / 32][rows] blocks of 128 bytes, 32 high
+// pieces of a row and then 32 low ones, the last columns padded with zeros.  A
+// value is (high + low) 2^(e - kHeldTop) with the row's e (RowScale).
 struct SplitMatrix {
   char *at;
   int rows, cols;
   long stride;  // bytes from one matrix to the next
-  // Where the high piece of (r, c) lies, the low one 64 bytes after it; of floats, the
-  // block's row.
+  // Where the high piece of (r, c) lies; the low one is 64 bytes after it.
   __device__ __forceinline__ char *place(int batch, int r, int c) const {
     return at + batch * stride + ((long)(c / 32) * rows + r) * 128 + c % 32 * 2;
   }
@@ -32,15 +31,25 @@ inline long split_bytes(long rows, long cols) { return (cols + 31) / 32 * rows *
 // polynomials' bounds allow, so that every e is a constant of the step past the exponent
 // of the norm that Z's row had when it was last looked at, and at most a constant of
 // the step, as the whole matrix has it.
-constexpr int kHeldTop = 15;         // a held element is below 2^15, half of half precision's range
+constexpr int kHeldTop = 15;  // a held element is below 2^15, half of half precision's range
 constexpr int kLeastExponent = -100;
 struct RowScale {
-  const unsigned *top;  // [batch][rows] the bits of the largest magnitudes of Z's rows
+  const signed char *norm;  // [batch][count]: the norm of rows i with this i >> shift is below 2^norm
+  int count, shift;
   int add, cap;
-  __device__ __forceinline__ int exponent(unsigned top) const {
-    return max(min((int)(top >> 23) + add, cap), kLeastExponent);
+  __device__ __forceinline__ unsigned index(int batch, int row) const {  // below 2^29
+    return (unsigned)batch * (unsigned)count + (unsigned)(row >> shift);
+  }
+  __device__ __forceinline__ int exponent(int norm) const {
+    return max(min(norm + add, cap), kLeastExponent);
   }
 };
+// A norm's exponent, from the bits of the largest magnitude of a row and the exponent of
+// the root of its length.
+__host__ __device__ __forceinline__ signed char norm_exponent(unsigned top, int length) {
+  const int e = (int)(top >> 23) - 126 + length;
+  return (signed char)(e < -127 ? -127 : e > 127 ? 127 : e);
+}
 
 // The sum of squares, in parts, of every matrix of the batch.
 struct OrthoNormArgs {
@@ -54,7 +63,7 @@ constexpr int kNormRun = 512;    // elements of a row that a wave adds up at a t
 constexpr int kNormParts = 256;  // parts, at most: a work-group each, of 16 such runs or more
 hipError_t launch_ortho_norm(const OrthoNormArgs &p, bool bf16, int batch, hipStream_t s);
 
-// 1 / (|X| + eps) of every matrix, and the largest magnitudes of the rows and columns of X
+// 1 / (|X| + eps) of every matrix, and the norms' exponents of the rows and columns of X
 // times that.
 struct OrthoSizesArgs {
   int M, N;
@@ -67,9 +76,10 @@ struct OrthoSizesArgs {
   double *parts;                    // [batch][bands][runs]
   unsigned *row_parts, *col_parts;  // [batch][runs][M], [batch][bands][N]
   bool summed;                      // by a launch of its own: very many parts
-  double *scale;                    // [batch], where summed
-  unsigned *rows, *cols;            // [1 + again][batch][M], [..][N]
-  int again;                        // sets after the first: zeros
+  double *scale;                    // [batch], where summed; null: 1
+  signed char *rows, *cols;         // as in RowScale
+  int row_shift, col_shift;         // both 0 but where summed
+  int row_length, col_length;       // exponents of the roots of N and M
 };
 inline int sizes_runs(long N) { return (int)((N + kNormRun - 1) / kNormRun); }
 // A multiple of 16, for about 224 work-groups: with what rounding adds, 65535 matrices
@@ -82,39 +92,41 @@ inline int sizes_bands(long M, long N) { return (int)((M + sizes_band(M, N) - 1)
 constexpr int kMostSizeParts = 24;  // of a row and of a column that each block adds up for itself
 hipError_t launch_ortho_sizes(const OrthoSizesArgs &p, bool bf16, int batch, hipStream_t s);
 
-// X times its scale, in pieces, as it is and transposed, and in floats.
+// X times its scale, in pieces, as it is and transposed.
 struct OrthoSplitArgs {
   OrthoSizesArgs x;
-  RowScale row_scale, col_scale;   // of X's rows and columns
-  SplitMatrix rows, cols, floats;  // M x N and N x M; floats is one of the two
-  bool floats_turned;              // floats is N x M
+  RowScale row_scale, col_scale;  // of X's rows and columns
+  SplitMatrix rows, cols;         // M x N and N x M
 };
 hipError_t launch_ortho_split(const OrthoSplitArgs &p, bool bf16, int batch, hipStream_t s);
 
-// The largest magnitudes of the rows and columns of x, in floats: the larger of them and of
-// what rows and cols hold.
-constexpr int kLookRows = 512;
-hipError_t launch_ortho_look(const SplitMatrix &x, unsigned *rows, unsigned *cols, int batch,
-                             hipStream_t s);
+// The norms' exponents of the rows and columns of z, which is held by z_scale.  p: M and N of
+// z, rows, cols and what they go by; row_parts and col_parts, one after the other, are room.
+hipError_t launch_ortho_look(const OrthoSizesArgs &p, const SplitMatrix &z, const RowScale &z_scale,
+                             int batch, hipStream_t s);
 
-// D = f1 A B^T + f2 E, of A's rows by B's rows.
+// D = f1 A B^T + f2 E, of A's rows by B's rows.  E is held twice, by its rows and, transposed,
+// by its columns, as B is: an element is taken from the copy whose range is the smaller.
 struct OrthoProductArgs {
   SplitMatrix a, b;
   RowScale a_scale, b_scale;
-  SplitMatrix e;  // E transposed, in floats; at == null: none
+  SplitMatrix e, e_t;  // e.at == null: none.  e may be d
+  RowScale e_scale;    // valid in any case, as the two below
   float f1, f2;
-  SplitMatrix d, d_t;  // D as it is and transposed; d_t.at == null: not written
-  RowScale d_scale, d_t_scale;  // valid ones in any case
-  SplitMatrix f_t;  // D transposed, in floats; at == null: not written.  May be e
+  SplitMatrix d, d_t;  // D as it is and transposed; at == null: not written
+  RowScale d_scale, d_t_scale;
   // The last product's D times alpha instead, in a user's type: element (m, n) at m ld +
   // n, or at n ld + m.
   void *Y;
   long ldy, strideY;
   bool y_transposed;
   float alpha;
+  // What the launch moves besides, 16 bytes at a time.
+  const char *move_from;
+  char *move_to;
+  unsigned moves;
 };
-// symmetric: D is symmetric, A and B the same, and one half of it is computed: of D
-// transposed in floats, and of E, that half is all there is.
+// symmetric: D is symmetric, A and B the same, and one half of D is computed.
 hipError_t launch_ortho_product(const OrthoProductArgs &p, bool symmetric, bool y_bf16, int batch,
                                 int cus, hipStream_t s);
 

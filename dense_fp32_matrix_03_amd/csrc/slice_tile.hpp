@@ -89,10 +89,16 @@ struct SliceTile {
   __device__ __forceinline__ static int col0() { return wave_id() % WN * WTN; }
 
   // acc = the tile's sums over nk slices.  lds: the stages' memory (STAGE_BYTES each),
-  // free once all waves have passed another barrier.
+  // free once all waves have passed another barrier.  meanwhile(): work for the time that
+  // the first slices take, before the first of run's barriers (where nk > 0).
   static constexpr int STAGE_BYTES = (BM + BN) * kSliceRow;
+  struct Nothing {
+    __device__ __forceinline__ void operator()() const {}
+  };
+  template <class Meanwhile = Nothing>
   __device__ __forceinline__ static void run(const SliceRows &rows_a, const SliceRows &rows_b,
-                                             int nk, Acc (&acc)[FM][FN], char *(&lds)[NST]) {
+                                             int nk, Acc (&acc)[FM][FN], char *(&lds)[NST],
+                                             const Meanwhile &meanwhile = Meanwhile()) {
     const SliceRows a = rows_a.uniform(), b = rows_b.uniform();
     // One LDS array per stage, so that the compiler sees that loads into one stage do
     // not touch the one that is read (mfma_dma.hpp).  It tells four arrays apart; with
@@ -260,6 +266,7 @@ struct SliceTile {
 
     if (nk > 0) {
       static_for<NST>([&](auto S) { dma(S); });
+      meanwhile();
       slice_barrier<(NST - 1) * kLoads>();
       read_ahead(S0(), cur);
       // Whole rounds of the stages without a test between them, then the rest: at a

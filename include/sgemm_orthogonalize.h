@@ -17,15 +17,23 @@
  * zeros gives zeros.
  *
  * Numerics.  Norms are summed in double precision.  The products run on the
- * half-precision matrix cores: each operand is held as the sum of two
- * half-precision numbers under a power of two that keeps it in range, 22 bits,
- * and three of the four products of the pieces are added up in single
- * precision.  An operand is off by at most 2^-22 of its value + 2^-39 of the
- * largest that the singular values allow (of 2^-60 where that is less), a product of pieces that is left out
- * is below 2^-22 of the whole: results are those of single-precision products
- * within a small factor.  S and S S are symmetric; each is computed once.
+ * half-precision matrix cores: each operand, Z between the steps among them, is
+ * held as the sum of two half-precision numbers, 22 bits, under a power of two
+ * for each row, and three of the four products of the pieces are added up in
+ * single precision.  A product of operands is off by 3 2^-22 of itself at most,
+ * where one in single precision is off by 2^-24; sums of many differ by less.
+ * A row's power of two goes by the row's own norm as it was up to eight steps
+ * before, times what the polynomials can have made of it since (and at most by the
+ * largest singular value there can be): an element is off by 2^-40 of that range
+ * at most, of its row's range and of its column's, so that rows or columns that
+ * are small against the others keep their digits.  What is in a small row and a
+ * small column, far below either's range, keeps them while the product of the steps'
+ * largest |a + b s^2 + c s^4| stays below about 2^15 (eight steps of 3.44): past
+ * that such a column (of M x N with M > N, such a row) loses digits, and the others
+ * do not.  Where one side is longer than about the square of the other, runs of
+ * its rows or columns share a range, the largest of theirs.
  * Matrices with M <= 64 or N <= 64 are multiplied in single precision instead.  Sums
- * are taken in an order that is fixed for a call's sizes, so repeated calls give
+ * are taken in an order that is fixed for a matrix' sizes, so repeated calls give
  * identical bits, whatever the batch around a matrix.  X has to be finite.
  *
  * Ranges.  `coefficients` are on the host, read during the call: 3 * sets floats,

