@@ -12,8 +12,8 @@
  *   (the products, grouped)
  *   sgemm_rows_combine          the experts' rows back to tokens, weighted and added
  * and backwards sgemm_rows_combine_backward, the products' gradients,
- * sgemm_rows_combine without weights (the gradient of sgemm_rows_gather) and
- * sgemm_route_backward.  Nothing is read on the host: the calls can be captured
+ * sgemm_rows_combine without weights (the gradient of sgemm_rows_gather without
+ * them) and sgemm_route_backward.  Nothing is read on the host: the calls can be captured
  * into a graph that is replayed with other tokens.
  *
  * Element types are SGEMM_TYPE_F32 and SGEMM_TYPE_BF16 (`type`), of every matrix
@@ -122,6 +122,10 @@ int sgemm_route_plan(int64_t pairs, int64_t first, int64_t groups, const int32_t
  * w = weights[pair], or 1 where weights is null (a copy of the bits).  Rows
  * whose source is not in [0, pairs) are not written; X has pairs / topk rows
  * (pairs a multiple of topk).  One rounding, of the product.
+ *
+ * Its gradients, for dY that of Y and the plan's places: of X, sgemm_rows_combine of dY
+ * with the same weights; of the weights, sgemm_rows_combine_backward with dY in
+ * the place of its X and X in that of its dY, weights and dX null.
  */
 int sgemm_rows_gather(int64_t rows, int64_t pairs, int64_t topk, int64_t N, int type,
                       const void *X, int64_t ldx, const int32_t *sources, const float *weights,
