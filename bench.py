@@ -485,46 +485,111 @@ def operand_sets(nbytes: int) -> int:
 MOST_SETS = 256
 
 
+# Sizes besides those of perf/more_operators.py, in its terms: matrices with a short side,
+# 8-bit products of 16 to 1024 rows and of a prompt's groups, few tokens' rows and a prompt's.
+def _orthogonalize(batch, M, N):
+    return dict(name=f"orthogonalize {batch} of {M} x {N}", op="orthogonalize", batch=batch, M=M,
+                N=N, type="f32", steps=5)
+
+
+def _int8(M, N, K):
+    return dict(name=f"int8 {M} x {N} x {K}", op="int8", M=M, N=N, K=K, type="bf16", out="bf16")
+
+
+def _int8_grouped(groups, rows, N, K):
+    return dict(name=f"int8_grouped {groups} groups, {rows} rows by {N} x {K}", op="int8_grouped",
+                groups=groups, rows=rows, N=N, K=K, type="bf16", out="bf16", sizes=7)
+
+
+def _moved(op, tokens, experts, N):
+    return dict(name=f"{op} {tokens} tokens, 8 of {experts} experts, {N}", op=op, tokens=tokens,
+                experts=experts, topk=8, N=N, type="bf16", first=0, groups=experts)
+
+
+MORE_SIZES = (
+    [_orthogonalize(*x) for x in ((1, 64, 64), (1, 64, 512), (1, 64, 2048), (1, 32, 4096),
+                                  (32, 64, 4096), (8, 20, 1000), (4000, 64, 1))]
+    + [_int8(*x) for x in ((16, 8192, 8192), (64, 8192, 8192), (256, 8192, 8192),
+                           (512, 8192, 8192), (1024, 8192, 8192), (128, 8192, 2048))]
+    + [_int8_grouped(*x) for x in ((16, 8192, 2048, 2048), (8, 2000, 4096, 1024),
+                                   (64, 4099, 1000, 777))]
+    + [_moved(*x) for x in (("combine", 1, 64, 2048), ("combine", 24, 64, 2048),
+                            ("combine", 24, 64, 7168), ("dispatch", 8192, 128, 2048))]
+    + [dict(name="route 8192 tokens, logits", op="route", tokens=8192, experts=256, topk=8,
+            score="softmax", type="bf16", bias=False, groups=1, keep=1, top=1, norm=True,
+            scale=1.0, masked=0)])
+
+
+def time_calls(calls, settle: float) -> float:
+    """Microseconds of a call, over many of `calls` in turn after `settle` seconds of them."""
+    import torch
+
+    stream = torch.cuda.current_stream()
+    for call in calls:
+        call()
+    torch.cuda.synchronize()
+    steps, t_end = 0, time.perf_counter() + settle
+    while time.perf_counter() < t_end or steps < 20:
+        for call in calls:
+            call()
+        torch.cuda.synchronize()
+        steps += len(calls)
+    steps = max(1, min(400, steps) // len(calls)) * len(calls)
+    t0 = torch.cuda.Event(enable_timing=True)
+    t1 = torch.cuda.Event(enable_timing=True)
+    t0.record(stream)
+    for i in range(steps):
+        calls[i % len(calls)]()
+    t1.record(stream)
+    torch.cuda.synchronize()
+    return t0.elapsed_time(t1) / steps * 1e3
+
+
 def experts_table(settle: float, name: str = "operators") -> list[dict]:
     """Time the calls of perf/operators.py's cases (products of grouped rows,
     casts to 4-bit floats and products of them), or of more_operators.py's
-    (routing, rows moved, 8-bit products, orthogonalised updates), one JSON
-    line each.  Several sets of operands are used in turn, more of them than
-    the caches hold."""
+    (routing, rows moved, 8-bit products, orthogonalised updates) and of
+    MORE_SIZES, one JSON line each.  Several sets of operands are used in turn,
+    more of them than the caches hold."""
+    import functools
+
     import torch
 
     ops = operators(name)
     ops.own = True
     rows = []
-    stream = torch.cuda.current_stream()
-    for case in ops.listed():
+    for case in ops.listed() + (MORE_SIZES if name == "more_operators" else []):
         need = ops.work(case)
         sets = [ops.prepare(case, i)
                 for i in range(min(MOST_SETS, operand_sets(need["bytes"])))]
-        for st in sets:
-            ops.run(st)
-        torch.cuda.synchronize()
-        steps, t_end = 0, time.perf_counter() + settle
-        while time.perf_counter() < t_end or steps < 20:
-            for st in sets:
-                ops.run(st)
-            torch.cuda.synchronize()
-            steps += len(sets)
-        steps = max(1, min(400, steps) // len(sets)) * len(sets)
-        t0 = torch.cuda.Event(enable_timing=True)
-        t1 = torch.cuda.Event(enable_timing=True)
-        t0.record(stream)
-        for i in range(steps):
-            ops.run(sets[i % len(sets)])
-        t1.record(stream)
-        torch.cuda.synchronize()
-        us = t0.elapsed_time(t1) / steps * 1e3
+        us = time_calls([functools.partial(ops.run, st) for st in sets], settle)
         r = {"case": case["name"], "us": round(us, 2), "gb_per_s": round(need["bytes"] / us / 1e3),
              "tflops": round(need["flops"] / us / 1e6, 2)}
         print(json.dumps(r), flush=True)
         rows.append(r)
-        del sets, st
+        del sets
         torch.cuda.empty_cache()
+    return rows
+
+
+def int8_casts(settle: float) -> list[dict]:
+    """Time the cast of 8192 x 8192 weights to 8-bit integers, stored by rows and transposed."""
+    import torch
+
+    import dense_fp32_matrix_03_amd as sg
+
+    n, rows = 8192, []
+    for kind, dtype in (("f32", torch.float32), ("bf16", torch.bfloat16)):
+        X = [torch.randn(n, n, device="cuda").to(dtype) for _ in range(4)]
+        codes = torch.empty(n, n, dtype=torch.int8, device="cuda")
+        scales = torch.empty(n, device="cuda")
+        for trans in (0, 1):
+            us = time_calls([lambda x=x: sg.sgemm_int8_quantize(trans, n, n, kind, x, n, codes, n,
+                                                                scales) for x in X], settle)
+            r = {"case": f"int8 cast {n} x {n} {kind}" + (", transposed" if trans else ""),
+                 "us": round(us, 2), "gb_per_s": round(n * n * (X[0].element_size() + 1) / us / 1e3)}
+            print(json.dumps(r), flush=True)
+            rows.append(r)
     return rows
 
 
@@ -994,8 +1059,8 @@ def main(argv=None) -> int:
                          "them on the cases of perf/operators.py, one JSON line each")
     ap.add_argument("--more-operators", action="store_true",
                     help="time routing, rows to experts and back, 8-bit products and "
-                         "orthogonalised updates on the cases of perf/more_operators.py, one "
-                         "JSON line each")
+                         "orthogonalised updates on the cases of perf/more_operators.py and at "
+                         "more sizes, one JSON line each")
     ap.add_argument("--kscan", action="store_true",
                     help="time sgemm_run at M = N = 256 and 1024 over K = 32 .. 4096, two "
                          "floor cases and the five workloads, one JSON line each (with the "
@@ -1064,6 +1129,8 @@ def main(argv=None) -> int:
         return 0
     if a.experts or a.more_operators:
         experts_table(a.settle, "more_operators" if a.more_operators else "operators")
+        if a.more_operators:
+            int8_casts(a.settle)
         sg.sgemm_destroy()
         return 0
     if a.vector_add:

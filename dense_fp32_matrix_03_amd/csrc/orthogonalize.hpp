@@ -169,7 +169,9 @@ inline OrthoTile ortho_tile(int rows_a, int rows_b, int cols, bool symmetric, in
 constexpr int kShort = 64;
 // At most 16 slabs, since each work-group adds up all their parts, 32 where a work-group
 // would have many blocks one after the other.  16 / 32 slabs: 32 of 64 x 4096 225 / 315 us,
-// 1 of 32 x 4096 116 / 100, 64 x 100000 1800 / 951.
+// 1 of 32 x 4096 116 / 100, 64 x 100000 1800 / 951.  The batch would tell the first two
+// apart, but the slabs are the order in which S is summed, and a matrix has the same bits
+// whatever the batch around it: what a batch loses by 32 is more than one gains.
 inline int short_blocks(int n) {
   const int slabs = n <= 8192 ? 16 : 32;
   return ((n + 63) / 64 + slabs - 1) / slabs;
