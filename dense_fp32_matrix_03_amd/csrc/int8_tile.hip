@@ -8,9 +8,9 @@
 // instruction adds does not matter, as long as A and B agree).
 //
 // Sums of whole numbers are exact, so that any tile gives the same bits.  8192^3 with a
-// cast A: 430 us a product (2.55 POPS; a library product of 8-bit integers 465), the
-// matrix cores 68% busy at the clock that power leaves them, after 40 us for the cast of
-// A.  32 groups, 48 rows by 4096 x 2048: 37 us (5.2 TB/s of B's codes), and 5 for the cast.
+// cast A: 430 to 476 us a product, by the card (2.3 to 2.55 POPS; a library product of
+// 8-bit integers 465), the matrix cores 70% busy at the clock that power leaves them,
+// after 40 to 47 us for the cast of A.  32 groups, 48 rows by 4096 x 2048: 37 us (5.2 TB/s of B's codes), and 5 for the cast.
 #include "grouped_map.hpp"
 #include "int8.hpp"
 #include "slice_tile.hpp"

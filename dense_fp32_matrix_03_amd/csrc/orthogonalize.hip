@@ -4,23 +4,27 @@
 // A value v is held as high + low, two half-precision numbers, high = v rounded and
 // low = v - high rounded: off by 2^-22 of v at most.  A product a b is then
 // al bh + ah bl + ah bh, three instructions instead of one (al bl, below 2^-22 of
-// it, is left out).  All matrices are scaled by powers of two so that the largest
-// element that their singular values allow stays below 2^15.
+// it, is left out).  Every row is scaled by a power of two of its own, which keeps it
+// below 2^15 (RowScale).  One power of two for a matrix was up to 1 us a launch
+// faster (16 x 256 x 512 125.6 us for 145) and left rows and columns that are small
+// against the others with few digits.
 //
 // With m <= n a step is S = Z Z^T, P = b S + c S S and a Z + P Z.  All three are
 // products of rows by rows once Z is held transposed too: the epilogue writes a
-// result as it is and transposed.  S and P are symmetric: tiles on and below the
-// diagonal are computed, and written to both sides.
+// result as it is and transposed, each by its rows' scales.  S and P are symmetric: blocks
+// on and below the diagonal are computed, and written to both sides.  All tiles add
+// an element's terms in the same order.
 //
 // Three times the operations of the formula at half precision's rate (1.33 PFLOP/s in a
-// large library product) are the floor.  Five steps, microseconds and the floor:
-//   1 x 2048 x 4096      945 - 965   676    the power limit: a Z + P Z 92 (1.12 PFLOP/s), S
-//                                           48 - 60 and P 37 (136 tiles on 256 compute units)
-//   1 x 1500 x 1001      200          62    S and P 11 each, a Z + P Z 17.5: 1.5 rounds of
+// large library product) are the floor.  Five steps, microseconds by the card and the floor:
+//   1 x 2048 x 4096      978 - 1070  676    the power limit: a Z + P Z 97 (1.06 PFLOP/s), S
+//                                           and P 53 (136 tiles on 256 compute units)
+//   1 x 1500 x 1001      216 - 256   62     S and P 13 each, a Z + P Z 19: 1.5 rounds of
 //                                           tiles, fixed costs of 4 to 5 us a launch
-//   16 x 256 x 512       115          21    17 launches of 4 to 11 us, of which 4 to 5 are
+//   16 x 256 x 512       134 - 161   21     17 launches of 5 to 14 us, of which 4 to 6 are
 //                                           fixed: first loads from memory, and the stores
-// The norm and the split are bound by memory: 2048 x 4096 9.1 us (3.7 TB/s) and 16.5 (6.1).
+// Sizes and the split are bound by memory: 2048 x 4096 11.8 us (2.9 TB/s), 4.7 for the
+// parts, and 18 (5.6).
 #include <math.h>
 
 #include "orthogonalize.hpp"

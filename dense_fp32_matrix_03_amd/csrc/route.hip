@@ -15,9 +15,9 @@
 // Without bias and groups the logits are compared, which is exact.
 //
 // By graph replay, top 8 of 64 experts for one token: 2.9 us; of 256 experts for 8192
-// tokens, bfloat16: 7.7 us; sigmoid with a bias 9.9; with 8 groups too 12.9 (28.4 with
-// everything in double precision and exchanges through LDS), 640 vector instructions a
-// wave, eight waves on every SIMD and 4 cycles an instruction: 8.5 us of issue; reading the
+// tokens, bfloat16: 7.7 us; sigmoid with a bias 9.9; with 8 groups too 13.2 (28.4 with
+// everything in double precision and exchanges through LDS), 662 vector instructions a
+// wave, eight waves on every SIMD and 4 cycles an instruction: 8.8 us of issue; reading the
 // logits would take 0.9.
 #include "mxfp4.hpp"
 #include "route.hpp"
