@@ -154,3 +154,71 @@ def test_zero_rows_and_columns():
         keep_r = torch.arange(shape[1], device="cuda") != 5
         keep_c = torch.arange(shape[2], device="cuda") != 17
         _check(x[:, keep_r][:, :, keep_c], y[:, keep_r][:, :, keep_c], 5, om.STEP)
+
+
+@pytest.mark.parametrize("shape,steps", [((2, 90, 141), 18), ((4, 1000, 1000), 9), ((1, 1501, 2203), 5)])
+def test_replayed_with_other_matrices(shape, steps):
+    """A captured call, its sizes looked at again on the way, replayed with rows of other sizes and a
+    workspace that something else has used in between."""
+    import torch
+    B, M, N = shape
+    X, Y = _values(shape, seed=9), torch.empty(shape, device="cuda")
+    need = sg.sgemm_orthogonalize_workspace_size(B, M, N)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+
+    def body():
+        sg.sgemm_orthogonalize(B, M, N, steps, om.STEP, 0.0, 1.0, "f32", X, N, M * N, "f32", Y, N,
+                               M * N, ws, need)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        body()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        body()
+    for r in range(4):
+        X[:, r::3] *= 1e-4
+        X[:, :, r::5] *= 30
+        body()
+        torch.cuda.synchronize()
+        want = Y.clone()
+        Y.fill_(9)
+        ws.fill_(255 - 85 * r)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(Y, want)
+
+
+def test_two_calls_at_once():
+    """On two streams, each with a workspace of its own, beside a batch of broadcast matrices."""
+    import torch
+    shapes = [(3, 130, 1403), (1, 700, 515)]
+    xs = [_values(s, seed=i) for i, s in enumerate(shapes)]
+    want = [_run(x, 10, om.STEP) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    for _ in range(3):
+        got = []
+        for x, s in zip(xs, streams):
+            B, M, N = x.shape
+            with torch.cuda.stream(s):
+                Y = torch.empty_like(x)
+                need = sg.sgemm_orthogonalize_workspace_size(B, M, N)
+                ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+                sg.sgemm_orthogonalize(B, M, N, 10, om.STEP, 0.0, 1.0, "f32", x, N, M * N, "f32", Y,
+                                       N, M * N, ws, need)
+            got.append((Y, ws))
+        torch.cuda.synchronize()
+        for (Y, _), w in zip(got, want):
+            assert torch.equal(Y, w)
+    x = xs[1]
+    B, M, N = 4, x.shape[1], x.shape[2]
+    Y = torch.empty(B, M, N, device="cuda")
+    need = sg.sgemm_orthogonalize_workspace_size(B, M, N)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    sg.sgemm_orthogonalize(B, M, N, 10, om.STEP, 0.0, 1.0, "f32", x, N, 0, "f32", Y, N, M * N, ws, need)
+    for y in Y:
+        assert torch.equal(y, want[1][0])
