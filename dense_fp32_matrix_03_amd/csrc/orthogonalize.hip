@@ -565,7 +565,8 @@ ortho_product_kernel(OrthoProductArgs p, TileMap map, FastDiv by_triangle, int t
       }
       if (p.e.at) {
         // By columns, where none of them has a range 2^8 times that of a row: what is held to
-        // 2^-40 of its column is then held to 2^-32 of its row too.
+        // 2^-40 of its column is then held to 2^-32 of its row too.  Read by rows as well (all
+        // blocks, every other row 1e-6 of the next): 2048 x 4096 1027 us for 997.
         const bool by_rows = __builtin_amdgcn_readfirstlane(
             ranges[Tile::row0() / 32 + i] + ranges[(BM + Tile::col0()) / 32 + j] > 8);
 #pragma unroll
